@@ -1,0 +1,148 @@
+// linattn.cuh -- shared pieces of the linear-attention kernels (decay per head, no erase):
+// one run, the cut of long sequences into pieces, and the launchers.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace gdn2 {
+namespace lin {
+
+// Sequences cut into pieces of whole 128-token chunks.  A sequence of at least two `target`s of
+// tokens is cut into len / target pieces; the rest stay whole.
+constexpr int kChunk = 128;
+constexpr int kNoCut = 0x7fffffff;
+struct Cut {
+  const int32_t *cu;       // device [n_seqs + 1] token offsets, or NULL: n_seqs x seq_len tokens
+  const int32_t *seg_off;  // device [n_seqs + 1]: first piece of every sequence (packed batches with
+                           // cuts), or NULL: every sequence has `per_seq` pieces
+  int n_seqs, seq_len, H;
+  int per_seq;             // pieces per sequence without seg_off
+  int n_pieces;            // pieces in all (an upper bound with seg_off)
+  int target;
+  int t_total;
+};
+
+// Length of the pieces of a sequence of `len` tokens, and their number.
+__host__ __device__ inline int piece_len(int len, int target) {
+  const int count = len / target;
+  if (count < 2) return len > 0 ? len : 1;
+  const int each = (len + count - 1) / count;
+  return (each + kChunk - 1) / kChunk * kChunk;
+}
+__host__ __device__ inline int piece_count(int len, int target) {
+  const int pl = piece_len(len, target);
+  return len > 0 ? (len + pl - 1) / pl : 1;
+}
+
+struct Piece {
+  int n, s, count;  // sequence, index of the piece in it, pieces of the sequence
+  int t0, len;      // first token, tokens
+  int first_piece;  // global index of the sequence's piece 0
+};
+
+// Bounds of sequence n; offsets outside [0, t_total] or out of order are cut back to it.
+__device__ __forceinline__ void seq_bounds(const Cut &c, int n, int *t0, int *len) {
+  if (!c.cu) {
+    *t0 = n * c.seq_len;
+    *len = c.seq_len;
+    return;
+  }
+  const int a = min(max(c.cu[n], 0), c.t_total), b = min(max(c.cu[n + 1], a), c.t_total);
+  *t0 = a;
+  *len = b - a;
+}
+
+// Piece number g; false past the last one (the grid covers an upper bound).
+__device__ __forceinline__ bool find_piece(const Cut &c, int g, Piece *p) {
+  int n, first;
+  if (c.seg_off) {
+    if (g >= c.seg_off[c.n_seqs]) return false;
+    int lo = 0, hi = c.n_seqs;  // last n with seg_off[n] <= g
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (c.seg_off[mid] <= g) lo = mid; else hi = mid;
+    }
+    n = lo;
+    first = c.seg_off[n];
+  } else {
+    n = g / c.per_seq;
+    first = n * c.per_seq;
+  }
+  int t0, len;
+  seq_bounds(c, n, &t0, &len);
+  const int pl = piece_len(len, c.target);
+  p->n = n;
+  p->s = g - first;
+  p->count = c.seg_off ? c.seg_off[n + 1] - first : c.per_seq;
+  p->first_piece = first;
+  p->t0 = t0 + min(p->s * pl, len);
+  p->len = min(pl, len - min(p->s * pl, len));
+  return true;
+}
+
+// log_a below this is a reset: e^-256 is 0 in fp32, and sums over a chunk stay finite.
+constexpr float kMinLog = -256.f;
+
+// One run over all (piece, head) units:
+//   forward:   out_t = sum_{j <= t} e^{L_t - L_j} (x_t . y_j) z_j + e^{L_t} start^T x_t
+//   backward:  out_t = sum_{j >= t} e^{L_j - L_t} (x_t . y_j) z_j + e^{L_end - L_t} start^T x_t
+// with L the running sum of log_a inside the sequence (inclusive).  x, y have dy columns; z and
+// out have dz.  The state sum w_j y_j z_j^T is dy x dz fp32.
+struct Run {
+  const void *x, *y, *z;
+  int Hx, Hy, Hz;        // their heads: head h reads head h / (H / Hx) and so on
+  const void *log_a;     // [T, H] of the inputs' type, or fp32 [H] with per_head
+  int per_head;
+  const float *start;    // [N, H, dy, dz] (or [dz, dy] with start_t), or NULL: zeros
+  int start_t;
+  float *fin;            // the state after the last step of the run (the same shapes), or NULL
+  int fin_t;
+  void *out;             // [T, H, dz]
+  int out_f32;           // out is fp32 whatever the inputs' type
+  int dy, dz;
+  int back;              // the backward form
+  // Cut sequences: the end state of every piece from a zero start, then the start of every
+  // piece (natural [dy][dz] layout), and the sum of its log_a.
+  float *piece_state;    // [n_pieces * H][dy * dz], NULL when nothing is cut
+  double *piece_log;     // [n_pieces * H]
+  int state_only;        // write piece_state and piece_log, no out
+  // For the gradient of log_a: partial dots of every out row with the row of m (Hm heads, dz
+  // columns) over the columns of one slice, [slices][T, H]; NULL: none.
+  const void *m;
+  int Hm;
+  float *dots;
+  Cut cut;
+  int dtype;
+};
+
+cudaError_t launch_plan(const Cut &c, int32_t *seg_off, cudaStream_t stream);
+cudaError_t launch_join(const Run &r, cudaStream_t stream);
+int simt_slices(int dz);
+cudaError_t launch_run_simt(const Run &r, cudaStream_t stream);
+// dlog_a of the fp32 runs: dots_q (of dq with q), dots_k (of dk with k), and <S_T, dS_T> (S_T
+// may be NULL with dS_T).
+cudaError_t launch_dlog_simt(const float *dots_q, int nq, const float *dots_k, int nk, const float *S_T,
+                             const float *dS_T, int dk, int dv, const Cut &c, void *dlog, int dtype,
+                             cudaStream_t stream);
+// out[t, g, :] = sum over the heads of group g of part[t, h, :]
+cudaError_t launch_group_sum(const float *part, void *out, const Cut &c, int Hg, int d, int dtype,
+                             cudaStream_t stream);
+
+struct StepProblem {
+  const void *q, *k, *v, *log_a;
+  float *S;
+  const int32_t *state_idx;
+  void *o;
+  int n_slots, N, H, Hqk, dk, dv, per_head, dtype_in, dtype_out;
+};
+cudaError_t launch_step(const StepProblem &p, cudaStream_t stream);
+
+}  // namespace lin
+
+// 8-bit checkpoints (ckpt8.cu)
+cudaError_t launch_ckpt8_save(const void *x, int8_t *codes, uint8_t *scales, int64_t rows, int cols, int dtype,
+                              cudaStream_t stream);
+cudaError_t launch_ckpt8_restore(const int8_t *codes, const uint8_t *scales, void *x, int64_t rows, int cols, int dtype,
+                                 cudaStream_t stream);
+}  // namespace gdn2

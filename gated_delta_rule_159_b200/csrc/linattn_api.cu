@@ -1,0 +1,435 @@
+// linattn_api.cu -- the extern "C" entry points of linear attention with a decay per head and of
+// the 8-bit checkpoints (include/gdn2.h): argument checks, workspace layout, the order of the
+// runs.  Nothing here computes; every step runs in the kernels.
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include "linattn.cuh"
+
+namespace {
+
+using gdn2::lin::Cut;
+using gdn2::lin::Run;
+
+int fail(int code, const char *fmt, ...) {
+  char text[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(text, sizeof(text), fmt, ap);
+  va_end(ap);
+  return gdn2::set_last_error(code, text);
+}
+void clear_error() { gdn2::set_last_error(0, ""); }
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+constexpr size_t kHeader = 256;  // [0] status word
+
+int check_dims(const gdn2_linattn_dims *d, bool one_type) {
+  if (!d) return fail(GDN2_ERR_INVALID_ARG, "dims is NULL");
+  if (d->reserved != 0) return fail(GDN2_ERR_INVALID_ARG, "dims.reserved must be 0");
+  if (d->n_seqs < 1 || d->seq_len < 0 || d->n_heads < 1 || d->n_qk_heads < 1 || d->d_k < 1 || d->d_v < 1)
+    return fail(GDN2_ERR_INVALID_ARG, "bad dims (n_seqs=%d seq_len=%d n_heads=%d n_qk_heads=%d d_k=%d d_v=%d)",
+                d->n_seqs, d->seq_len, d->n_heads, d->n_qk_heads, d->d_k, d->d_v);
+  if (d->n_heads % d->n_qk_heads)
+    return fail(GDN2_ERR_INVALID_ARG, "n_heads=%d is not a multiple of n_qk_heads=%d", d->n_heads, d->n_qk_heads);
+  if ((d->dtype_in != GDN2_BF16 && d->dtype_in != GDN2_F32) || (d->dtype_out != GDN2_BF16 && d->dtype_out != GDN2_F32))
+    return fail(GDN2_ERR_INVALID_ARG, "bad dtype_in=%d / dtype_out=%d", d->dtype_in, d->dtype_out);
+  if (d->flags & ~(uint32_t)GDN2_LINATTN_HEAD_DECAY)
+    return fail(GDN2_ERR_INVALID_ARG, "unknown flag bits 0x%x", d->flags & ~(uint32_t)GDN2_LINATTN_HEAD_DECAY);
+  if (one_type && d->dtype_in != d->dtype_out)
+    return fail(GDN2_ERR_UNSUPPORTED, "dtype_out must be dtype_in here");
+  if (d->d_k > 128 || d->d_v > 128)
+    return fail(GDN2_ERR_UNSUPPORTED, "no kernel for d_k=%d d_v=%d (both at most 128)", d->d_k, d->d_v);
+  return GDN2_OK;
+}
+
+int64_t tokens_of(const gdn2_linattn_dims *d, bool packed) {
+  return packed ? (int64_t)d->seq_len : (int64_t)d->n_seqs * d->seq_len;
+}
+
+// Limits of the launches: 32-bit token numbers, (piece, head) units in one grid dimension.
+int check_sizes(const gdn2_linattn_dims *d, bool packed) {
+  if (tokens_of(d, packed) >= ((int64_t)1 << 31)) return fail(GDN2_ERR_UNSUPPORTED, "T_tot must be below 2^31");
+  if ((int64_t)d->n_seqs * d->n_heads >= ((int64_t)1 << 30))
+    return fail(GDN2_ERR_UNSUPPORTED, "n_seqs * n_heads must be below 2^30");
+  return GDN2_OK;
+}
+
+bool tensor_core(const gdn2_linattn_dims *d) { return d->d_k == 128 && d->d_v == 128 && d->dtype_in == GDN2_BF16; }
+
+// Where the (sequence, head) units alone leave SMs idle, long sequences are cut into pieces that
+// run side by side (each piece's end state first, the join, then the outputs): half as much again
+// of the work, spread over all SMs.  The target is the balanced share of tokens per worker; the
+// tensor-core run has one worker per SM, the fp32 run (a slice of 32 state columns each) four.
+Cut make_cut(const gdn2_linattn_dims *d, const int32_t *cu, bool packed) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    sms = 148;
+  }
+  const int64_t T = tokens_of(d, packed);
+  const bool tc = tensor_core(d);
+  const int slices = tc ? 1 : gdn2::lin::simt_slices(d->d_k < d->d_v ? d->d_k : d->d_v);
+  const int64_t workers = tc ? sms : 4 * (int64_t)sms;
+  int64_t target = (T * d->n_heads * slices + workers - 1) / workers;
+  const int64_t least = tc ? 512 : 256;
+  if (target < least) target = least;
+  Cut c;
+  memset(&c, 0, sizeof(c));
+  c.cu = cu;
+  c.n_seqs = d->n_seqs;
+  c.seq_len = d->seq_len;
+  c.H = d->n_heads;
+  c.t_total = (int)T;
+  c.target = target < gdn2::lin::kNoCut / 2 ? (int)target : gdn2::lin::kNoCut;
+  if (packed) {
+    const bool any = T / c.target >= 2;
+    if (!any) c.target = gdn2::lin::kNoCut;
+    c.per_seq = 1;
+    c.n_pieces = any ? (int)(d->n_seqs + T / c.target) : d->n_seqs;
+  } else {
+    c.per_seq = gdn2::lin::piece_count(d->seq_len, c.target);
+    c.n_pieces = d->n_seqs * c.per_seq;
+  }
+  return c;
+}
+bool has_cuts(const Cut &c) { return c.n_pieces > c.n_seqs; }
+
+// The cut's part of a workspace: piece offsets, log sums and states.
+struct CutLayout {
+  size_t off_seg, off_log, off_state, end;
+};
+CutLayout cut_layout(const Cut &c, size_t at, size_t state) {
+  CutLayout L;
+  const size_t units = has_cuts(c) ? (size_t)c.n_pieces * c.H : 0;
+  L.off_seg = at;
+  L.off_log = L.off_seg + (units ? up256(((size_t)c.n_seqs + 1) * sizeof(int32_t)) : 0);
+  L.off_state = L.off_log + up256(units * sizeof(double));
+  L.end = L.off_state + up256(units * state * sizeof(float));
+  return L;
+}
+
+int check_workspace(const void *ws, size_t have, size_t need) {
+  if (!ws || !aligned(ws, 256)) return fail(GDN2_ERR_WORKSPACE, "workspace must be non-NULL and 256-byte aligned");
+  if (have < need) return fail(GDN2_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", have, need);
+  return GDN2_OK;
+}
+
+int check_tensors(int64_t tokens, const void *const *p, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (!p[i] && tokens > 0) return fail(GDN2_ERR_INVALID_ARG, "a per-token pointer is NULL");
+    if (!aligned(p[i], 16)) return fail(GDN2_ERR_INVALID_ARG, "pointer %p is not 16-byte aligned", p[i]);
+  }
+  return GDN2_OK;
+}
+int check_log_a(const gdn2_linattn_dims *d, int64_t tokens, const void *log_a) {
+  const bool head = (d->flags & GDN2_LINATTN_HEAD_DECAY) != 0;
+  if (!log_a && (head || tokens > 0)) return fail(GDN2_ERR_INVALID_ARG, "log_a is NULL");
+  if (!aligned(log_a, head || d->dtype_in == GDN2_F32 ? 4 : 2))
+    return fail(GDN2_ERR_INVALID_ARG, "log_a pointer %p is misaligned", log_a);
+  return GDN2_OK;
+}
+
+int cuda_fail(const char *what, cudaError_t e) { return fail(GDN2_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e)); }
+
+// A run, with its cut sequences' piece states and join first.
+cudaError_t full_run(Run r, cudaStream_t s) {
+  cudaError_t e;
+  if (has_cuts(r.cut)) {
+    Run first = r;
+    first.state_only = 1;
+    first.m = nullptr;
+    if ((e = gdn2::lin::launch_run_simt(first, s)) != cudaSuccess) return e;
+    if ((e = gdn2::lin::launch_join(r, s)) != cudaSuccess) return e;
+  } else {
+    r.piece_state = nullptr;
+  }
+  return gdn2::lin::launch_run_simt(r, s);
+}
+
+cudaError_t prepare(Cut &c, char *ws, const CutLayout &L, cudaStream_t s) {
+  cudaError_t e = cudaMemsetAsync(ws, 0, kHeader, s);
+  if (e != cudaSuccess) return e;
+  if (c.cu && has_cuts(c)) {
+    int32_t *off = reinterpret_cast<int32_t *>(ws + L.off_seg);
+    e = gdn2::lin::launch_plan(c, off, s);
+    c.seg_off = off;
+  }
+  return e;
+}
+
+Run base_run(const gdn2_linattn_dims *d, const void *log_a, const Cut &c, char *ws, const CutLayout &L) {
+  Run r;
+  memset(&r, 0, sizeof(r));
+  r.log_a = log_a;
+  r.per_head = (d->flags & GDN2_LINATTN_HEAD_DECAY) != 0;
+  r.cut = c;
+  r.dtype = d->dtype_in;
+  r.piece_log = reinterpret_cast<double *>(ws + L.off_log);
+  r.piece_state = reinterpret_cast<float *>(ws + L.off_state);
+  return r;
+}
+
+// gdn2_linattn_bwd's workspace: header, the cut, the final state (for dlog_a with dS_T), the
+// per-head parts of dq and dk where heads share q and k (one buffer, used twice), the dots.
+struct BwdLayout {
+  CutLayout cut;
+  size_t off_fin, off_part, off_dq, off_dk, off_restored[3], total;
+};
+BwdLayout bwd_layout(const gdn2_linattn_dims *d, const Cut &c, bool ckpt8) {
+  BwdLayout L;
+  const size_t state = (size_t)d->d_k * d->d_v, T = (size_t)c.t_total, H = d->n_heads;
+  const bool dlog = !(d->flags & GDN2_LINATTN_HEAD_DECAY);
+  L.cut = cut_layout(c, kHeader, state);
+  L.off_fin = L.cut.end;
+  L.off_part = L.off_fin + (dlog ? up256((size_t)d->n_seqs * H * state * sizeof(float)) : 0);
+  L.off_dq = L.off_part + (d->n_qk_heads < d->n_heads ? up256(T * H * d->d_k * sizeof(float)) : 0);
+  const size_t dots = dlog ? up256(T * H * gdn2::lin::simt_slices(d->d_k) * sizeof(float)) : 0;
+  L.off_dk = L.off_dq + dots;
+  L.total = L.off_dk + dots;
+  const size_t es = d->dtype_in == GDN2_BF16 ? 2 : 4;
+  const size_t rows[3] = {T * d->n_qk_heads * d->d_k * es, T * d->n_qk_heads * d->d_k * es, T * H * d->d_v * es};
+  for (int i = 0; i < 3; ++i) {
+    L.off_restored[i] = L.total;
+    if (ckpt8) L.total += up256(rows[i]);
+  }
+  return L;
+}
+
+int bwd_runs(const void *q, const void *k, const void *v, const void *log_a, const float *S0,
+             const int32_t *cu, const void *dO, const float *dS_T, void *dq, void *dk, void *dv, void *dlog_a,
+             float *dS0, const gdn2_linattn_dims *d, Cut c, char *ws, const BwdLayout &L, cudaStream_t s) {
+  (void)cu;
+  const int H = d->n_heads, Hq = d->n_qk_heads;
+  const bool shared = Hq < H;
+  float *part = reinterpret_cast<float *>(ws + L.off_part);
+  float *dots_q = reinterpret_cast<float *>(ws + L.off_dq), *dots_k = reinterpret_cast<float *>(ws + L.off_dk);
+  float *fin = dlog_a && dS_T ? reinterpret_cast<float *>(ws + L.off_fin) : nullptr;
+  const Run base = base_run(d, log_a, c, ws, L.cut);
+  cudaError_t e;
+
+  Run r = base;  // dq_i = sum_{j <= i} (dO_i . v_j) k_j: the state is the forward's, transposed
+  r.x = dO; r.Hx = H; r.y = v; r.Hy = H; r.z = k; r.Hz = Hq;
+  r.dy = d->d_v; r.dz = d->d_k;
+  r.start = S0; r.start_t = 1; r.fin = fin; r.fin_t = 1;
+  r.out = shared ? part : dq; r.out_f32 = shared;
+  if (dlog_a) { r.m = q; r.Hm = Hq; r.dots = dots_q; }
+  if ((e = full_run(r, s)) != cudaSuccess) return cuda_fail("linattn dq run", e);
+  if (shared && (e = gdn2::lin::launch_group_sum(part, dq, c, Hq, d->d_k, d->dtype_in, s)) != cudaSuccess)
+    return cuda_fail("linattn dq head sum", e);
+
+  r = base;  // dv_j = sum_{i >= j} (k_j . q_i) dO_i: the state is dLoss/dS
+  r.back = 1;
+  r.x = k; r.Hx = Hq; r.y = q; r.Hy = Hq; r.z = dO; r.Hz = H;
+  r.dy = d->d_k; r.dz = d->d_v;
+  r.start = dS_T; r.fin = dS0;
+  r.out = dv;
+  if ((e = full_run(r, s)) != cudaSuccess) return cuda_fail("linattn dv run", e);
+
+  r = base;  // dk_j = sum_{i >= j} (v_j . dO_i) q_i
+  r.back = 1;
+  r.x = v; r.Hx = H; r.y = dO; r.Hy = H; r.z = q; r.Hz = Hq;
+  r.dy = d->d_v; r.dz = d->d_k;
+  r.start = dS_T; r.start_t = 1;
+  r.out = shared ? part : dk; r.out_f32 = shared;
+  if (dlog_a) { r.m = k; r.Hm = Hq; r.dots = dots_k; }
+  if ((e = full_run(r, s)) != cudaSuccess) return cuda_fail("linattn dk run", e);
+  if (shared && (e = gdn2::lin::launch_group_sum(part, dk, c, Hq, d->d_k, d->dtype_in, s)) != cudaSuccess)
+    return cuda_fail("linattn dk head sum", e);
+  if (dlog_a) {
+    const int n = gdn2::lin::simt_slices(d->d_k);
+    e = gdn2::lin::launch_dlog_simt(dots_q, n, dots_k, n, fin, dS_T, d->d_k, d->d_v, c, dlog_a, d->dtype_in, s);
+    if (e != cudaSuccess) return cuda_fail("linattn dlog_a", e);
+  }
+  return GDN2_OK;
+}
+
+int check_bwd(const gdn2_linattn_dims *d, const void *log_a, const float *S0, const int32_t *cu, const void *dO,
+              const float *dS_T, void *dq, void *dk, void *dv, void *dlog_a, float *dS0) {
+  const int64_t T = tokens_of(d, cu != nullptr);
+  const void *rows[4] = {dO, dq, dk, dv};
+  int rc = check_tensors(T, rows, 4);
+  if (!rc) rc = check_log_a(d, T, log_a);
+  if (rc) return rc;
+  const bool head = (d->flags & GDN2_LINATTN_HEAD_DECAY) != 0;
+  if (head && dlog_a) return fail(GDN2_ERR_INVALID_ARG, "dlog_a must be NULL with GDN2_LINATTN_HEAD_DECAY");
+  if (!head && !dlog_a && T > 0) return fail(GDN2_ERR_INVALID_ARG, "dlog_a is NULL");
+  if (!aligned(dlog_a, d->dtype_in == GDN2_F32 ? 4 : 2)) return fail(GDN2_ERR_INVALID_ARG, "dlog_a is misaligned");
+  if (!aligned(S0, 16) || !aligned(dS_T, 16) || !aligned(dS0, 16))
+    return fail(GDN2_ERR_INVALID_ARG, "S0, dS_T and dS0 must be 16-byte aligned");
+  if (!aligned(cu, 4)) return fail(GDN2_ERR_INVALID_ARG, "cu_seqlens is misaligned");
+  return GDN2_OK;
+}
+
+int check_ckpt8(const void *x, const int8_t *codes, const uint8_t *scales, int64_t rows, int32_t cols, int32_t dtype) {
+  if (rows < 0 || cols < 1) return fail(GDN2_ERR_INVALID_ARG, "bad shape (rows=%lld cols=%d)", (long long)rows, cols);
+  if (dtype != GDN2_BF16 && dtype != GDN2_F32) return fail(GDN2_ERR_INVALID_ARG, "bad dtype=%d", dtype);
+  if (rows > ((int64_t)1 << 33) / ((cols + 31) / 32))
+    return fail(GDN2_ERR_UNSUPPORTED, "more than 2^33 blocks of 32 values");
+  if (rows > 0 && (!x || !codes || !scales)) return fail(GDN2_ERR_INVALID_ARG, "x, codes and scales must be non-NULL");
+  if (!aligned(x, 16) || !aligned(codes, 16))
+    return fail(GDN2_ERR_INVALID_ARG, "x and codes must be 16-byte aligned");
+  return GDN2_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn2_linattn_fwd_workspace_size(const gdn2_linattn_dims *dims, int32_t packed) {
+  clear_error();
+  if (check_dims(dims, true) || check_sizes(dims, packed != 0)) return 0;
+  const Cut c = make_cut(dims, nullptr, packed != 0);
+  return cut_layout(c, kHeader, (size_t)dims->d_k * dims->d_v).end;
+}
+
+int gdn2_linattn_fwd(const void *q, const void *k, const void *v, const void *log_a, const float *S0,
+                     const int32_t *cu_seqlens, void *o, float *S_T, const gdn2_linattn_dims *dims, void *workspace,
+                     size_t workspace_bytes, gdn2_stream_t stream) {
+  clear_error();
+  int rc = check_dims(dims, true);
+  if (!rc) rc = check_sizes(dims, cu_seqlens != nullptr);
+  if (rc) return rc;
+  const int64_t T = tokens_of(dims, cu_seqlens != nullptr);
+  const void *rows[4] = {q, k, v, o};
+  rc = check_tensors(T, rows, 4);
+  if (!rc) rc = check_log_a(dims, T, log_a);
+  if (rc) return rc;
+  if (!aligned(S0, 16) || !aligned(S_T, 16)) return fail(GDN2_ERR_INVALID_ARG, "S0 / S_T must be 16-byte aligned");
+  if (!aligned(cu_seqlens, 4)) return fail(GDN2_ERR_INVALID_ARG, "cu_seqlens is misaligned");
+  Cut c = make_cut(dims, cu_seqlens, cu_seqlens != nullptr);
+  const CutLayout L = cut_layout(c, kHeader, (size_t)dims->d_k * dims->d_v);
+  rc = check_workspace(workspace, workspace_bytes, L.end);
+  if (rc) return rc;
+  char *ws = static_cast<char *>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = prepare(c, ws, L, s);
+  if (e != cudaSuccess) return cuda_fail("linattn workspace", e);
+  Run r = base_run(dims, log_a, c, ws, L);
+  r.x = q; r.Hx = dims->n_qk_heads; r.y = k; r.Hy = dims->n_qk_heads; r.z = v; r.Hz = dims->n_heads;
+  r.dy = dims->d_k; r.dz = dims->d_v;
+  r.start = S0; r.fin = S_T; r.out = o;
+  if ((e = full_run(r, s)) != cudaSuccess) return cuda_fail("linattn run", e);
+  return GDN2_OK;
+}
+
+int gdn2_linattn_step(const void *q, const void *k, const void *v, const void *log_a, float *S, int32_t n_slots,
+                      const int32_t *state_idx, void *o, const gdn2_linattn_dims *dims, gdn2_stream_t stream) {
+  clear_error();
+  int rc = check_dims(dims, false);
+  if (!rc) rc = check_sizes(dims, false);
+  if (rc) return rc;
+  if (dims->seq_len != 1) return fail(GDN2_ERR_INVALID_ARG, "seq_len must be 1 (got %d)", dims->seq_len);
+  const void *rows[4] = {q, k, v, o};
+  rc = check_tensors(1, rows, 4);
+  if (!rc) rc = check_log_a(dims, 1, log_a);
+  if (rc) return rc;
+  if (!S || !aligned(S, 16)) return fail(GDN2_ERR_INVALID_ARG, "S must be non-NULL and 16-byte aligned");
+  if (state_idx && n_slots < 1) return fail(GDN2_ERR_INVALID_ARG, "n_slots must be at least 1 (got %d)", n_slots);
+  if (!aligned(state_idx, 4)) return fail(GDN2_ERR_INVALID_ARG, "state_idx is misaligned");
+  gdn2::lin::StepProblem p;
+  memset(&p, 0, sizeof(p));
+  p.q = q; p.k = k; p.v = v; p.log_a = log_a; p.S = S; p.state_idx = state_idx; p.o = o;
+  p.n_slots = n_slots; p.N = dims->n_seqs; p.H = dims->n_heads; p.Hqk = dims->n_qk_heads;
+  p.dk = dims->d_k; p.dv = dims->d_v;
+  p.per_head = (dims->flags & GDN2_LINATTN_HEAD_DECAY) != 0;
+  p.dtype_in = dims->dtype_in; p.dtype_out = dims->dtype_out;
+  const cudaError_t e = gdn2::lin::launch_step(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("linattn step launch", e);
+  return GDN2_OK;
+}
+
+size_t gdn2_linattn_bwd_workspace_size(const gdn2_linattn_dims *dims, int32_t packed) {
+  clear_error();
+  if (check_dims(dims, true) || check_sizes(dims, packed != 0)) return 0;
+  return bwd_layout(dims, make_cut(dims, nullptr, packed != 0), false).total;
+}
+
+int gdn2_linattn_bwd(const void *q, const void *k, const void *v, const void *log_a, const float *S0,
+                     const int32_t *cu_seqlens, const void *dO, const float *dS_T, void *dq, void *dk, void *dv,
+                     void *dlog_a, float *dS0, const gdn2_linattn_dims *dims, void *workspace, size_t workspace_bytes,
+                     gdn2_stream_t stream) {
+  clear_error();
+  int rc = check_dims(dims, true);
+  if (!rc) rc = check_sizes(dims, cu_seqlens != nullptr);
+  if (rc) return rc;
+  const void *rows[3] = {q, k, v};
+  rc = check_tensors(tokens_of(dims, cu_seqlens != nullptr), rows, 3);
+  if (!rc) rc = check_bwd(dims, log_a, S0, cu_seqlens, dO, dS_T, dq, dk, dv, dlog_a, dS0);
+  if (rc) return rc;
+  Cut c = make_cut(dims, cu_seqlens, cu_seqlens != nullptr);
+  const BwdLayout L = bwd_layout(dims, c, false);
+  rc = check_workspace(workspace, workspace_bytes, L.total);
+  if (rc) return rc;
+  char *ws = static_cast<char *>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = prepare(c, ws, L.cut, s);
+  if (e != cudaSuccess) return cuda_fail("linattn workspace", e);
+  return bwd_runs(q, k, v, log_a, S0, cu_seqlens, dO, dS_T, dq, dk, dv, dlog_a, dS0, dims, c, ws, L, s);
+}
+
+int gdn2_ckpt8_save(const void *x, int8_t *codes, uint8_t *scales, int64_t rows, int32_t cols, int32_t dtype,
+                    gdn2_stream_t stream) {
+  clear_error();
+  int rc = check_ckpt8(x, codes, scales, rows, cols, dtype);
+  if (rc || rows == 0) return rc;
+  const cudaError_t e = gdn2::launch_ckpt8_save(x, codes, scales, rows, cols, dtype, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GDN2_OK : cuda_fail("ckpt8 save launch", e);
+}
+
+int gdn2_ckpt8_restore(const int8_t *codes, const uint8_t *scales, void *x, int64_t rows, int32_t cols, int32_t dtype,
+                       gdn2_stream_t stream) {
+  clear_error();
+  int rc = check_ckpt8(x, codes, scales, rows, cols, dtype);
+  if (rc || rows == 0) return rc;
+  const cudaError_t e =
+      gdn2::launch_ckpt8_restore(codes, scales, x, rows, cols, dtype, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GDN2_OK : cuda_fail("ckpt8 restore launch", e);
+}
+
+size_t gdn2_linattn_bwd_ckpt8_workspace_size(const gdn2_linattn_dims *dims, int32_t packed) {
+  clear_error();
+  if (check_dims(dims, true) || check_sizes(dims, packed != 0)) return 0;
+  return bwd_layout(dims, make_cut(dims, nullptr, packed != 0), true).total;
+}
+
+int gdn2_linattn_bwd_ckpt8(const int8_t *q_codes, const uint8_t *q_scales, const int8_t *k_codes,
+                           const uint8_t *k_scales, const int8_t *v_codes, const uint8_t *v_scales, const void *log_a,
+                           const float *S0, const int32_t *cu_seqlens, const void *dO, const float *dS_T, void *dq,
+                           void *dk, void *dv, void *dlog_a, float *dS0, const gdn2_linattn_dims *dims, void *workspace,
+                           size_t workspace_bytes, gdn2_stream_t stream) {
+  clear_error();
+  int rc = check_dims(dims, true);
+  if (!rc) rc = check_sizes(dims, cu_seqlens != nullptr);
+  if (rc) return rc;
+  const int64_t T = tokens_of(dims, cu_seqlens != nullptr);
+  const void *rows[3] = {q_codes, k_codes, v_codes};
+  rc = check_tensors(T, rows, 3);
+  if (rc) return rc;
+  if (T > 0 && (!q_scales || !k_scales || !v_scales)) return fail(GDN2_ERR_INVALID_ARG, "a scales pointer is NULL");
+  rc = check_bwd(dims, log_a, S0, cu_seqlens, dO, dS_T, dq, dk, dv, dlog_a, dS0);
+  if (rc) return rc;
+  Cut c = make_cut(dims, cu_seqlens, cu_seqlens != nullptr);
+  const BwdLayout L = bwd_layout(dims, c, true);
+  rc = check_workspace(workspace, workspace_bytes, L.total);
+  if (rc) return rc;
+  char *ws = static_cast<char *>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = prepare(c, ws, L.cut, s);
+  if (e != cudaSuccess) return cuda_fail("linattn workspace", e);
+  const int8_t *codes[3] = {q_codes, k_codes, v_codes};
+  const uint8_t *scales[3] = {q_scales, k_scales, v_scales};
+  for (int i = 0; i < 3 && T > 0; ++i) {
+    e = gdn2::launch_ckpt8_restore(codes[i], scales[i], ws + L.off_restored[i],
+                                   T * (i < 2 ? dims->n_qk_heads : dims->n_heads), i < 2 ? dims->d_k : dims->d_v,
+                                   dims->dtype_in, s);
+    if (e != cudaSuccess) return cuda_fail("ckpt8 restore launch", e);
+  }
+  return bwd_runs(ws + L.off_restored[0], ws + L.off_restored[1], ws + L.off_restored[2], log_a, S0, cu_seqlens, dO,
+                  dS_T, dq, dk, dv, dlog_a, dS0, dims, c, ws, L, s);
+}
+
+}  // extern "C"

@@ -7,6 +7,7 @@ missing: there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -39,7 +40,11 @@ EXPORTED = ("gdn2_chunk_fwd", "gdn2_chunk_fwd_workspace_size", "gdn2_check_statu
             "gdn2_segment_correct", "gdn2_segment_correct_workspace_size",
             "gdn2_chunk_fwd_split_varlen", "gdn2_chunk_fwd_split_varlen_workspace_size",
             "gdn2_chunk_fwd_noalloc", "gdn2_chunk_fwd_noalloc_status", "gdn2_debug_timeout_once",
+            "gdn2_linattn_fwd", "gdn2_linattn_fwd_workspace_size", "gdn2_linattn_step", "gdn2_linattn_bwd",
+            "gdn2_linattn_bwd_workspace_size", "gdn2_ckpt8_save", "gdn2_ckpt8_restore", "gdn2_linattn_bwd_ckpt8",
+            "gdn2_linattn_bwd_ckpt8_workspace_size",
             "gdn2_last_error", "gdn2_version")
+LINATTN_HEAD_DECAY = 1
 DEBUG_CHUNK = 1
 DEBUG_DECODE = 2
 DEBUG_BWD = 3
@@ -48,6 +53,13 @@ DEBUG_BWD = 3
 class Dims(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int32), ("seq_len", ctypes.c_int32), ("n_heads", ctypes.c_int32),
                 ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32), ("chunk", ctypes.c_int32),
+                ("dtype_in", ctypes.c_int32), ("dtype_out", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("reserved", ctypes.c_int32)]
+
+
+class LinattnDims(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("seq_len", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("n_qk_heads", ctypes.c_int32), ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32),
                 ("dtype_in", ctypes.c_int32), ("dtype_out", ctypes.c_int32), ("flags", ctypes.c_uint32),
                 ("reserved", ctypes.c_int32)]
 
@@ -104,6 +116,19 @@ def _load():
     lib.gdn2_chunk_bwd.argtypes = [vp] * 17 + [ctypes.POINTER(Dims), vp, sz, vp]
     lib.gdn2_chunk_bwd_workspace_size.restype = sz
     lib.gdn2_chunk_bwd_workspace_size.argtypes = [ctypes.POINTER(Dims), ctypes.c_int32]
+    ld = ctypes.POINTER(LinattnDims)
+    for name, argtypes in (("fwd", [vp] * 8 + [ld, vp, sz, vp]), ("bwd", [vp] * 13 + [ld, vp, sz, vp]),
+                           ("bwd_ckpt8", [vp] * 16 + [ld, vp, sz, vp]),
+                           ("step", [vp] * 5 + [ctypes.c_int32, vp, vp, ld, vp])):
+        fn = getattr(lib, "gdn2_linattn_" + name)
+        fn.restype, fn.argtypes = ctypes.c_int, argtypes
+        if name != "step":
+            fn = getattr(lib, f"gdn2_linattn_{name}_workspace_size")
+            fn.restype, fn.argtypes = sz, [ld, ctypes.c_int32]
+    for name in ("save", "restore"):
+        fn = getattr(lib, "gdn2_ckpt8_" + name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = [vp, vp, vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, vp]
     lib.gdn2_last_error.restype = ctypes.c_char_p
     lib.gdn2_last_error.argtypes = []
     lib.gdn2_version.restype = ctypes.c_int
@@ -512,6 +537,220 @@ def _bwd_call(fn, ws_fn, q, k, v, log_a, b, w, dO, S0, dS_T, cu_seqlens, scalar_
     _check(rc)
     g["workspace"] = workspace
     return g
+
+
+# ---------------------------------------------------------------- linear attention, 8-bit checkpoints
+def _linattn_shape(q, k, v, log_a, cu_seqlens, dtype):
+    """(n_seqs, seq_len) of the token tensors, after checking that they fit together."""
+    if q.dim() != 3 and not (q.dim() == 4 and cu_seqlens is None):
+        raise ValueError("q must be [B, T, H_qk, d_k], or [T_tot, H_qk, d_k] (with cu_seqlens or as one sequence)")
+    if cu_seqlens is not None and (cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2):
+        raise TypeError("cu_seqlens must be int32 [N + 1]")
+    lead = tuple(q.shape[:-2])
+    if k.shape != q.shape:
+        raise ValueError(f"k {tuple(k.shape)} must be shaped like q {tuple(q.shape)}")
+    if tuple(v.shape[:-2]) != lead or v.dim() != q.dim():
+        raise ValueError(f"v {tuple(v.shape)} must be [..., H, d_v] over q's tokens {lead}")
+    H = v.shape[-2]
+    if log_a.dim() == 1:
+        if log_a.dtype != torch.float32 or log_a.numel() != H:
+            raise TypeError("a log_a per head must be fp32 [H]")
+    elif tuple(log_a.shape) != lead + (H,) or log_a.dtype != dtype:
+        raise ValueError(f"log_a must be {lead + (H,)} in {dtype}, or fp32 [H]")
+    if q.dim() == 4:
+        return q.shape[0], q.shape[1]
+    return (1 if cu_seqlens is None else cu_seqlens.numel() - 1), q.shape[0]
+
+
+def _linattn_dims(n, seq_len, q, v, log_a, dtype, out_dtype) -> LinattnDims:
+    return LinattnDims(int(n), int(seq_len), int(v.shape[-2]), int(q.shape[-2]), int(q.shape[-1]), int(v.shape[-1]),
+                       _dtype_code(dtype), _dtype_code(out_dtype), LINATTN_HEAD_DECAY if log_a.dim() == 1 else 0, 0)
+
+
+def _same(dtype, device, **tensors):
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+        if t.device != device:
+            raise ValueError(f"{name} lives on {t.device}, q on {device}")
+
+
+def _shaped(name, t, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
+
+
+def _workspace(nbytes, workspace, device):
+    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device) if workspace is None else workspace
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(device):
+    """Makes ``device`` current for a call: the launches and the plan follow the tensors."""
+    if device.type != "cuda":
+        raise ValueError("gdn2 tensors must live on a CUDA device")
+    return _HERE_ALREADY if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _nbytes(t: torch.Tensor) -> int:
+    return t.numel() * t.element_size()
+
+
+def linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_a: torch.Tensor,
+                S0: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None, *,
+                output_final_state: bool = True, o: Optional[torch.Tensor] = None,
+                S_T: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Linear attention with a decay per head through ``gdn2_linattn_fwd``:
+    S_t = exp(log_a_t) S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+
+    q, k: [B, T, H_qk, d_k] (equal lengths) or [T_tot, H_qk, d_k] with ``cu_seqlens`` (int32
+    [N+1] on the device); v: [.., H, d_v] with H a multiple of H_qk; log_a: [.., H] of v's dtype,
+    or fp32 [H] for one fixed decay per head.  S0: fp32 [N, H, d_k, d_v] or None.
+    Returns (o [.., H, d_v], S_T fp32 [N, H, d_k, d_v] or None).
+    """
+    N, seq_len = _linattn_shape(q, k, v, log_a, cu_seqlens, q.dtype)
+    dev = q.device
+    _same(q.dtype, dev, k=k, v=v, o=o)
+    _same(torch.float32, dev, S0=S0, S_T=S_T)
+    _same(None, dev, log_a=log_a, cu_seqlens=cu_seqlens, workspace=workspace)
+    state = (N, v.shape[-2], q.shape[-1], v.shape[-1])
+    dims = _linattn_dims(N, seq_len, q, v, log_a, q.dtype, q.dtype)
+    _shaped("S0", S0, state)
+    _shaped("S_T", S_T, state)
+    _shaped("o", o, v.shape)
+    if o is None:
+        o = torch.empty(v.shape, dtype=q.dtype, device=dev)
+    if S_T is None and output_final_state:
+        S_T = torch.empty(state, dtype=torch.float32, device=dev)
+    with _on(dev):
+        packed = 0 if cu_seqlens is None else 1
+        ws = _workspace(lib.gdn2_linattn_fwd_workspace_size(ctypes.byref(dims), packed), workspace, dev)
+        _check(lib.gdn2_linattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_a), _ptr(S0), _ptr(cu_seqlens), _ptr(o),
+                                    _ptr(S_T), ctypes.byref(dims), _ptr(ws), _nbytes(ws), _stream(dev)))
+    return o, S_T
+
+
+def linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_a: torch.Tensor, S: torch.Tensor,
+                 state_idx: Optional[torch.Tensor] = None, *, out_dtype: torch.dtype = torch.float32,
+                 o: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of linear attention through ``gdn2_linattn_step``; ``S`` is updated in place.
+
+    q, k: [N, H_qk, d_k]; v: [N, H, d_v]; log_a: [N, H] of v's dtype or fp32 [H].  S: fp32
+    [N, H, d_k, d_v], or with ``state_idx`` (int32 [N] on the device) a pool [P, H, d_k, d_v] of
+    which row n uses slot ``state_idx[n]``; an index outside [0, P) is a padding row.
+    Returns o [N, H, d_v].
+    """
+    if q.dim() != 3:
+        raise ValueError("q must be [N, H_qk, d_k]")
+    _linattn_shape(q, k, v, log_a, None, q.dtype)
+    dev, N = q.device, q.shape[0]
+    _same(q.dtype, dev, k=k, v=v)
+    _same(torch.float32, dev, S=S)
+    _same(None, dev, log_a=log_a, state_idx=state_idx, o=o)
+    if state_idx is not None and (state_idx.dtype != torch.int32 or state_idx.numel() != N):
+        raise TypeError("state_idx must be int32 with one entry per row")
+    _shaped("S", S, (N if state_idx is None else S.shape[0], v.shape[-2], q.shape[-1], v.shape[-1]))
+    if o is None:
+        o = torch.empty(v.shape, dtype=out_dtype, device=dev)
+    _shaped("o", o, v.shape)
+    if N == 0:
+        return o
+    dims = _linattn_dims(N, 1, q, v, log_a, q.dtype, o.dtype)
+    with _on(dev):
+        _check(lib.gdn2_linattn_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_a), _ptr(S), int(S.shape[0]), _ptr(state_idx),
+                                     _ptr(o), ctypes.byref(dims), _stream(dev)))
+    return o
+
+
+def _linattn_grads(q, k, v, log_a, dO, S0, dS_T, cu_seqlens, need_dS0, workspace, size_fn, call):
+    N, seq_len = _linattn_shape(q, k, v, log_a, cu_seqlens, dO.dtype)
+    dev = q.device
+    state = (N, v.shape[-2], q.shape[-1], v.shape[-1])
+    _same(torch.float32, dev, S0=S0, dS_T=dS_T)
+    _same(None, dev, log_a=log_a, cu_seqlens=cu_seqlens, dO=dO, workspace=workspace)
+    _shaped("dO", dO, v.shape)
+    _shaped("S0", S0, state)
+    _shaped("dS_T", dS_T, state)
+    dims = _linattn_dims(N, seq_len, q, v, log_a, dO.dtype, dO.dtype)
+    g = {"d" + name: torch.empty(t.shape, dtype=dO.dtype, device=dev) for name, t in (("q", q), ("k", k), ("v", v))}
+    g["dlog_a"] = torch.empty(log_a.shape, dtype=dO.dtype, device=dev) if log_a.dim() > 1 else None
+    g["dS0"] = torch.empty(state, dtype=torch.float32, device=dev) if need_dS0 else None
+    with _on(dev):
+        ws = _workspace(size_fn(ctypes.byref(dims), 0 if cu_seqlens is None else 1), workspace, dev)
+        _check(call(_ptr(log_a), _ptr(S0), _ptr(cu_seqlens), _ptr(dO), _ptr(dS_T), _ptr(g["dq"]), _ptr(g["dk"]),
+                    _ptr(g["dv"]), _ptr(g["dlog_a"]), _ptr(g["dS0"]), ctypes.byref(dims), _ptr(ws), _nbytes(ws),
+                    _stream(dev)))
+    g["workspace"] = ws
+    return g
+
+
+def linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_a: torch.Tensor, dO: torch.Tensor,
+                S0: Optional[torch.Tensor] = None, dS_T: Optional[torch.Tensor] = None,
+                cu_seqlens: Optional[torch.Tensor] = None, *, need_dS0: bool = True,
+                workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients through ``gdn2_linattn_bwd`` of  sum <dO, o> + <dS_T, S_T>  for ``linattn_fwd`` with
+    the same inputs.  Returns a dict with dq, dk (summed over the heads that share q and k), dv,
+    dlog_a (None for a decay per head) and dS0 (fp32, None unless ``need_dS0``)."""
+    _same(q.dtype, q.device, k=k, v=v, dO=dO)
+    return _linattn_grads(q, k, v, log_a, dO, S0, dS_T, cu_seqlens, need_dS0, workspace,
+                          lib.gdn2_linattn_bwd_workspace_size,
+                          lambda *rest: lib.gdn2_linattn_bwd(_ptr(q), _ptr(k), _ptr(v), *rest))
+
+
+def ckpt8_save(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+    """Keep ``x`` [.., n] (bf16 or fp32) in 8 bits through ``gdn2_ckpt8_save``: blocks of 32 values
+    along the last axis share a power-of-two scale.  Returns (codes int8 like x, scales uint8
+    [.., ceil(n / 32)])."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must have a last axis of at least one value")
+    dtype = _dtype_code(x.dtype)
+    shape = tuple(x.shape[:-1]) + ((x.shape[-1] + 31) // 32,)
+    codes = torch.empty(x.shape, dtype=torch.int8, device=x.device) if codes is None else codes
+    scales = torch.empty(shape, dtype=torch.uint8, device=x.device) if scales is None else scales
+    _ckpt8_shapes(codes, scales, x.shape, x.device)
+    with _on(x.device):
+        _check(lib.gdn2_ckpt8_save(_ptr(x), _ptr(codes), _ptr(scales), x.numel() // x.shape[-1], x.shape[-1],
+                                   dtype, _stream(x.device)))
+    return codes, scales
+
+
+def ckpt8_restore(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                  x: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values that a checkpoint of ``ckpt8_save`` stands for, through ``gdn2_ckpt8_restore``."""
+    x = torch.empty(codes.shape, dtype=dtype, device=codes.device) if x is None else x
+    _ckpt8_shapes(codes, scales, x.shape, x.device)
+    with _on(codes.device):
+        _check(lib.gdn2_ckpt8_restore(_ptr(codes), _ptr(scales), _ptr(x), codes.numel() // codes.shape[-1],
+                                      codes.shape[-1], _dtype_code(x.dtype), _stream(codes.device)))
+    return x
+
+
+def _ckpt8_shapes(codes, scales, shape, device):
+    _same(torch.int8, device, codes=codes)
+    _same(torch.uint8, device, scales=scales)
+    _shaped("codes", codes, shape)
+    if codes.dim() < 1 or codes.shape[-1] < 1:
+        raise ValueError("codes must have a last axis of at least one value")
+    _shaped("scales", scales, tuple(shape[:-1]) + ((shape[-1] + 31) // 32,))
+
+
+def linattn_bwd_ckpt8(q8, k8, v8, log_a: torch.Tensor, dO: torch.Tensor, S0: Optional[torch.Tensor] = None,
+                      dS_T: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None, *,
+                      need_dS0: bool = True, workspace: Optional[torch.Tensor] = None) -> dict:
+    """``linattn_bwd`` at the values that 8-bit checkpoints stand for, through
+    ``gdn2_linattn_bwd_ckpt8``: q8, k8, v8 are the (codes, scales) of ``ckpt8_save`` of q, k and v.
+    The gradients take dO's dtype."""
+    (q, qs), (k, ks), (v, vs) = q8, k8, v8
+    for codes, scales in (q8, k8, v8):
+        _ckpt8_shapes(codes, scales, codes.shape, q.device)
+    return _linattn_grads(q, k, v, log_a, dO, S0, dS_T, cu_seqlens, need_dS0, workspace,
+                          lib.gdn2_linattn_bwd_ckpt8_workspace_size,
+                          lambda *rest: lib.gdn2_linattn_bwd_ckpt8(_ptr(q), _ptr(qs), _ptr(k), _ptr(ks), _ptr(v),
+                                                                   _ptr(vs), *rest))
 
 
 def version() -> int:

@@ -442,6 +442,127 @@ int gdn2_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
 int gdn2_chunk_fwd_noalloc_status(gdn2_stream_t stream);
 
 /*
+ * Linear attention with a decay for each head: the delta rule's sibling without the erase, which
+ * hybrid stacks run beside it (retention, and state-space layers whose heads share q and k).  Per
+ * sequence and head, state S of d_k x d_v in fp32, for every token t:
+ *
+ *   S_t = a_t S_{t-1} + k_t v_t^T,   a_t = exp(log_a_t) in [0, 1],
+ *   o_t = S_t^T q_t.
+ *
+ * (The pages describe it as the decayed state before the delta rule's correction: neelmishra.
+ * github.io, "A retention curve you can calculate".)  No 1/sqrt(d_k) scale is applied.
+ *   n_heads     H, the heads of v, o, log_a and the state.
+ *   n_qk_heads  heads of q and k, a divisor of H: head h reads q and k head h / (H / n_qk_heads).
+ *               Their gradients are summed over the heads that share them.
+ *   seq_len     as in gdn2_dims.
+ *   flags       GDN2_LINATTN_HEAD_DECAY: log_a is fp32 [H], one fixed decay per head; else log_a is
+ *               [T_tot, H] of dtype_in.
+ * log_a <= 0; -infinity (a reset) is allowed, and log_a below -256 counts as -256 in the prompt and
+ * gradient calls (a factor of 0 in fp32).  Conventions otherwise as above.  Supported: d_k and d_v
+ * up to 128, bf16 or fp32.  d_k = d_v = 128 in bf16 runs on the tensor cores (bf16 products, fp32
+ * sums; the state is fp32 throughout and S_T and dS0 are computed to fp32 accuracy); everything
+ * else runs in fp32.
+ */
+enum gdn2_linattn_flags { GDN2_LINATTN_HEAD_DECAY = 1u };
+typedef struct gdn2_linattn_dims {
+  int32_t n_seqs;
+  int32_t seq_len;
+  int32_t n_heads;
+  int32_t n_qk_heads;
+  int32_t d_k;
+  int32_t d_v;
+  int32_t dtype_in;
+  int32_t dtype_out; /* dtype_in, except for gdn2_linattn_step's o */
+  uint32_t flags;
+  int32_t reserved;  /* must be 0 */
+} gdn2_linattn_dims;
+
+/*
+ * gdn2_linattn_fwd -- the prompt form over N sequences.
+ *   q, k         [T_tot, n_qk_heads, d_k] dtype_in
+ *   v            [T_tot, H, d_v] dtype_in
+ *   log_a        [T_tot, H] dtype_in, or fp32 [H] with GDN2_LINATTN_HEAD_DECAY
+ *   S0           [N, H, d_k, d_v] fp32 or NULL for zeros.  May alias S_T.
+ *   cu_seqlens   device int32 [N + 1] token offsets, or NULL: N sequences of seq_len tokens
+ *   o            [T_tot, H, d_v] dtype_out = dtype_in (written; rows outside every sequence stay)
+ *   S_T          [N, H, d_k, d_v] fp32 or NULL
+ *   workspace    at least gdn2_linattn_fwd_workspace_size(dims, cu_seqlens != NULL) bytes, 256-byte
+ *                aligned, uninitialised; one call at a time.  The size depends on the current
+ *                device's SM count: sequences much longer than the balanced share of tokens per SM
+ *                are cut into pieces that run side by side.
+ * gdn2_check_status(workspace) reports a timed-out wait.
+ * Errors: GDN2_ERR_INVALID_ARG, GDN2_ERR_UNSUPPORTED, GDN2_ERR_WORKSPACE, GDN2_ERR_CUDA.
+ */
+int gdn2_linattn_fwd(const void *q, const void *k, const void *v, const void *log_a, const float *S0,
+                     const int32_t *cu_seqlens, void *o, float *S_T, const gdn2_linattn_dims *dims,
+                     void *workspace, size_t workspace_bytes, gdn2_stream_t stream);
+/* Workspace bytes (0 if dims are invalid or unsupported); packed != 0: the call passes cu_seqlens. */
+size_t gdn2_linattn_fwd_workspace_size(const gdn2_linattn_dims *dims, int32_t packed);
+
+/*
+ * gdn2_linattn_step -- one token for each of N sequences, the states updated in place.
+ *   q, k [N, n_qk_heads, d_k], v [N, H, d_v], log_a [N, H] dtype_in (or fp32 [H])
+ *   S          [N, H, d_k, d_v] fp32; with state_idx [n_slots, H, d_k, d_v]
+ *   state_idx  device int32 [N] or NULL, as gdn2_decode_step_indexed: an entry outside
+ *              [0, n_slots) is a padding row (o row zero, no state touched); two rows naming one
+ *              slot race on it.
+ *   o          [N, H, d_v] dtype_out
+ * dims.seq_len must be 1.
+ * Errors: GDN2_ERR_INVALID_ARG, GDN2_ERR_UNSUPPORTED, GDN2_ERR_CUDA.
+ */
+int gdn2_linattn_step(const void *q, const void *k, const void *v, const void *log_a, float *S,
+                      int32_t n_slots, const int32_t *state_idx, void *o, const gdn2_linattn_dims *dims,
+                      gdn2_stream_t stream);
+
+/*
+ * gdn2_linattn_bwd -- the gradients of  sum_t <dO_t, o_t> + sum_n <dS_T[n], S_T[n]>  for
+ * gdn2_linattn_fwd with the same inputs.
+ *   dO              [T_tot, H, d_v] dtype_in
+ *   dS_T            [N, H, d_k, d_v] fp32 or NULL (zero)
+ *   dq, dk, dv      written, dtype_in, shaped like q, k, v
+ *   dlog_a          [T_tot, H] dtype_in; NULL with GDN2_LINATTN_HEAD_DECAY (fixed decays have no
+ *                   gradient here)
+ *   dS0             [N, H, d_k, d_v] fp32 or NULL to skip
+ *   workspace       at least gdn2_linattn_bwd_workspace_size bytes, as for gdn2_linattn_fwd
+ * Errors as gdn2_linattn_fwd.
+ */
+int gdn2_linattn_bwd(const void *q, const void *k, const void *v, const void *log_a, const float *S0,
+                     const int32_t *cu_seqlens, const void *dO, const float *dS_T, void *dq, void *dk,
+                     void *dv, void *dlog_a, float *dS0, const gdn2_linattn_dims *dims, void *workspace,
+                     size_t workspace_bytes, gdn2_stream_t stream);
+size_t gdn2_linattn_bwd_workspace_size(const gdn2_linattn_dims *dims, int32_t packed);
+
+/*
+ * 8-bit checkpoints: activations kept between a forward and its backward pass at 8.25 bits a value.
+ * Every row of x [rows, cols] is cut into blocks of 32 values (the last may be shorter) with one
+ * scale 2^e each, e the smallest integer >= -127 with max|x| <= 127 * 2^e:
+ *   codes   [rows, cols] int8: x / 2^e rounded to the nearest integer, ties to even (cut back to
+ *           +-63 where 64 * 2^e would overflow)
+ *   scales  [rows, ceil(cols / 32)] uint8: e + 127; 255 for a block with an infinity or a NaN,
+ *           which restores as NaN
+ * The error is at most 2^(e-1), below max|x| / 127.  A restored value code * 2^e is exact in bf16.
+ * dtype is x's (GDN2_BF16 or GDN2_F32).  x and codes are 16-byte aligned; rows may be 0.
+ * Errors: GDN2_ERR_INVALID_ARG, GDN2_ERR_UNSUPPORTED, GDN2_ERR_CUDA.
+ */
+int gdn2_ckpt8_save(const void *x, int8_t *codes, uint8_t *scales, int64_t rows, int32_t cols,
+                    int32_t dtype, gdn2_stream_t stream);
+int gdn2_ckpt8_restore(const int8_t *codes, const uint8_t *scales, void *x, int64_t rows, int32_t cols,
+                       int32_t dtype, gdn2_stream_t stream);
+
+/*
+ * gdn2_linattn_bwd_ckpt8 -- gdn2_linattn_bwd at the values that 8-bit checkpoints of q, k and v stand
+ * for: q and k saved as rows of d_k (codes [T_tot, n_qk_heads, d_k], scales [T_tot, n_qk_heads,
+ * ceil(d_k / 32)]), v as rows of d_v.  dtype_in is the type of dO and of the gradients.
+ */
+int gdn2_linattn_bwd_ckpt8(const int8_t *q_codes, const uint8_t *q_scales, const int8_t *k_codes,
+                           const uint8_t *k_scales, const int8_t *v_codes, const uint8_t *v_scales,
+                           const void *log_a, const float *S0, const int32_t *cu_seqlens, const void *dO,
+                           const float *dS_T, void *dq, void *dk, void *dv, void *dlog_a, float *dS0,
+                           const gdn2_linattn_dims *dims, void *workspace, size_t workspace_bytes,
+                           gdn2_stream_t stream);
+size_t gdn2_linattn_bwd_ckpt8_workspace_size(const gdn2_linattn_dims *dims, int32_t packed);
+
+/*
  * gdn2_debug_timeout_once -- test hook for the failure detection of the bounded
  * device-side waits; not for production use.  It arms a one-shot fault for the
  * next launch of the kernel named by `site`:
