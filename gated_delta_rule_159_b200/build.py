@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn2.so")
 
 SOURCES = ["api.cu", "decode.cu", "chunk_simt.cu", "chunk_tc.cu", "noalloc.cu", "bwd.cu", "bwd_tc.cu", "seqpar.cu",
-           "linattn.cu", "linattn_api.cu", "ckpt8.cu"]
+           "linattn.cu", "linattn_tc.cu", "linattn_api.cu", "ckpt8.cu"]
 HEADERS = ["common.cuh", "internal.h", "sm100_ptx.cuh", "tc_util.cuh", "linattn.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -1209,13 +1209,14 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   return fn;
 }
 
-// [T_tot][H][128] bf16 viewed as (channel, head, token); box 64 channels x 1 head x 64 tokens.
-bool make_map(CUtensorMap *m, const void *base, int64_t t_total, int H) {
+// [T_tot][H][128] bf16 viewed as (channel, head, token); box 64 channels x 1 head x
+// box_tokens tokens.
+bool make_map(CUtensorMap *m, const void *base, int64_t t_total, int H, uint32_t box_tokens = 64) {
   auto enc = get_encode();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)t_total};
   cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
-  cuuint32_t box[3] = {64, 1, 64};
+  cuuint32_t box[3] = {64, 1, box_tokens};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1275,8 +1276,8 @@ cudaError_t launch_gates_ck(const TcParams &P, int grid, cudaStream_t stream, bo
 
 }  // namespace
 
-bool make_row_tile_map(CUtensorMap *m, const void *base, int64_t t_total, int H) {
-  return make_map(m, base, t_total, H);
+bool make_row_tile_map(CUtensorMap *m, const void *base, int64_t t_total, int H, int box_tokens) {
+  return make_map(m, base, t_total, H, (uint32_t)box_tokens);
 }
 
 cudaError_t launch_chunk_tc(const ChunkProblem &p, cudaStream_t stream, const char **why) {

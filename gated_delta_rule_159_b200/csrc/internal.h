@@ -156,8 +156,8 @@ cudaError_t launch_chunk_simt(const ChunkProblem &p, cudaStream_t stream);
 // when the problem is outside what it handles.
 cudaError_t launch_chunk_tc(const ChunkProblem &p, cudaStream_t stream, const char **why);
 // Tensor map of a [t_total][H][128] bf16 tensor viewed as (channel, head, token): boxes of 64
-// channels x 1 head x 64 tokens with the 128-byte swizzle (the tile layout of the tensor-core
+// channels x 1 head x box_tokens tokens with the 128-byte swizzle (the tile layout of the tensor-core
 // kernels).  False when the driver entry point is missing or the geometry is rejected.
-bool make_row_tile_map(CUtensorMap *m, const void *base, int64_t t_total, int H);
+bool make_row_tile_map(CUtensorMap *m, const void *base, int64_t t_total, int H, int box_tokens = 64);
 
 }  // namespace gdn2

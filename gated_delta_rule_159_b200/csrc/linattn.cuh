@@ -81,6 +81,13 @@ __device__ __forceinline__ bool find_piece(const Cut &c, int g, Piece *p) {
   return true;
 }
 
+// Groups of chunks that dlog_a of the tensor-core runs is summed over, numbered from each piece's
+// start.  Slot of the group that starts at token t of piece g: pieces are in token order, so no two
+// share one.
+constexpr int kGroup = 4;
+__host__ __device__ inline int mark_slot(int g, int t) { return g + t / (kGroup * kChunk); }
+inline size_t mark_slots(const Cut &c) { return (size_t)c.n_pieces + (size_t)(c.t_total / (kGroup * kChunk)) + 1; }
+
 // log_a below this is a reset: e^-256 is 0 in fp32, and sums over a chunk stay finite.
 constexpr float kMinLog = -256.f;
 
@@ -112,6 +119,10 @@ struct Run {
   const void *m;
   int Hm;
   float *dots;
+  // Tensor-core runs: marks of the state behind every group of kGroup chunks, [slots][H][dy * dz]
+  // in the state warps' own order; the forward form writes them, the backward form multiplies its
+  // state at the same place with them into mark_dots [slots][H][8].  NULL: none.
+  float *marks, *mark_dots;
   Cut cut;
   int dtype;
 };
@@ -120,11 +131,17 @@ cudaError_t launch_plan(const Cut &c, int32_t *seg_off, cudaStream_t stream);
 cudaError_t launch_join(const Run &r, cudaStream_t stream);
 int simt_slices(int dz);
 cudaError_t launch_run_simt(const Run &r, cudaStream_t stream);
+// The run on the tensor cores (linattn_tc.cu): bf16, dy = dz = 128.  `terms`: bf16 values that
+// stand for a weighted row of y in the state's update, 3 (24 bits) or 2.
+cudaError_t launch_run_tc(const Run &r, int terms, int32_t *status, cudaStream_t stream);
 // dlog_a of the fp32 runs: dots_q (of dq with q), dots_k (of dk with k), and <S_T, dS_T> (S_T
 // may be NULL with dS_T).
 cudaError_t launch_dlog_simt(const float *dots_q, int nq, const float *dots_k, int nk, const float *S_T,
                              const float *dS_T, int dk, int dv, const Cut &c, void *dlog, int dtype,
                              cudaStream_t stream);
+// dlog_a of the tensor-core runs (linattn_tc.cu).
+cudaError_t launch_dlog_tc(const float *dots_q, const float *dots_k, const float *mark_dots, const Cut &c, void *dlog,
+                           cudaStream_t stream);
 // out[t, g, :] = sum over the heads of group g of part[t, h, :]
 cudaError_t launch_group_sum(const float *part, void *out, const Cut &c, int Hg, int d, int dtype,
                              cudaStream_t stream);

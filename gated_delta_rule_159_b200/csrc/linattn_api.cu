@@ -135,19 +135,24 @@ int check_log_a(const gdn2_linattn_dims *d, int64_t tokens, const void *log_a) {
 
 int cuda_fail(const char *what, cudaError_t e) { return fail(GDN2_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e)); }
 
-// A run, with its cut sequences' piece states and join first.
-cudaError_t full_run(Run r, cudaStream_t s) {
+// A run, with its cut sequences' piece states and join first.  The runs whose state can be a result
+// (the forward's, dv's) take it to the tensor cores in three bf16 terms, whether or not this call
+// asks for it: out must not depend on that.  The others only feed it to bf16 products: two terms.
+cudaError_t full_run(Run r, int terms, int32_t *status, bool tc, cudaStream_t s) {
   cudaError_t e;
+  auto launch = [&](const Run &run) {
+    return tc ? gdn2::lin::launch_run_tc(run, terms, status, s) : gdn2::lin::launch_run_simt(run, s);
+  };
   if (has_cuts(r.cut)) {
     Run first = r;
     first.state_only = 1;
     first.m = nullptr;
-    if ((e = gdn2::lin::launch_run_simt(first, s)) != cudaSuccess) return e;
+    if ((e = launch(first)) != cudaSuccess) return e;
     if ((e = gdn2::lin::launch_join(r, s)) != cudaSuccess) return e;
   } else {
     r.piece_state = nullptr;
   }
-  return gdn2::lin::launch_run_simt(r, s);
+  return launch(r);
 }
 
 cudaError_t prepare(Cut &c, char *ws, const CutLayout &L, cudaStream_t s) {
@@ -173,21 +178,25 @@ Run base_run(const gdn2_linattn_dims *d, const void *log_a, const Cut &c, char *
   return r;
 }
 
-// gdn2_linattn_bwd's workspace: header, the cut, the final state (for dlog_a with dS_T), the
-// per-head parts of dq and dk where heads share q and k (one buffer, used twice), the dots.
+// gdn2_linattn_bwd's workspace: header, the cut, for dlog_a the final state (fp32 runs) or the marks
+// (tensor-core runs), the per-head parts of dq and dk where heads share q and k (one buffer, used
+// twice), the dots.
 struct BwdLayout {
   CutLayout cut;
-  size_t off_fin, off_part, off_dq, off_dk, off_restored[3], total;
+  size_t off_fin, off_marks, off_mark_dots, off_part, off_dq, off_dk, off_restored[3], total;
 };
 BwdLayout bwd_layout(const gdn2_linattn_dims *d, const Cut &c, bool ckpt8) {
   BwdLayout L;
   const size_t state = (size_t)d->d_k * d->d_v, T = (size_t)c.t_total, H = d->n_heads;
-  const bool dlog = !(d->flags & GDN2_LINATTN_HEAD_DECAY);
+  const bool dlog = !(d->flags & GDN2_LINATTN_HEAD_DECAY), tc = tensor_core(d);
+  const size_t slots = dlog && tc ? gdn2::lin::mark_slots(c) * H : 0;
   L.cut = cut_layout(c, kHeader, state);
   L.off_fin = L.cut.end;
-  L.off_part = L.off_fin + (dlog ? up256((size_t)d->n_seqs * H * state * sizeof(float)) : 0);
+  L.off_marks = L.off_fin + (dlog && !tc ? up256((size_t)d->n_seqs * H * state * sizeof(float)) : 0);
+  L.off_mark_dots = L.off_marks + slots * state * sizeof(float);
+  L.off_part = L.off_mark_dots + up256(slots * 8 * sizeof(float));
   L.off_dq = L.off_part + (d->n_qk_heads < d->n_heads ? up256(T * H * d->d_k * sizeof(float)) : 0);
-  const size_t dots = dlog ? up256(T * H * gdn2::lin::simt_slices(d->d_k) * sizeof(float)) : 0;
+  const size_t dots = dlog ? up256(T * H * (tc ? 1 : gdn2::lin::simt_slices(d->d_k)) * sizeof(float)) : 0;
   L.off_dk = L.off_dq + dots;
   L.total = L.off_dk + dots;
   const size_t es = d->dtype_in == GDN2_BF16 ? 2 : 4;
@@ -200,14 +209,17 @@ BwdLayout bwd_layout(const gdn2_linattn_dims *d, const Cut &c, bool ckpt8) {
 }
 
 int bwd_runs(const void *q, const void *k, const void *v, const void *log_a, const float *S0,
-             const int32_t *cu, const void *dO, const float *dS_T, void *dq, void *dk, void *dv, void *dlog_a,
+             const void *dO, const float *dS_T, void *dq, void *dk, void *dv, void *dlog_a,
              float *dS0, const gdn2_linattn_dims *d, Cut c, char *ws, const BwdLayout &L, cudaStream_t s) {
-  (void)cu;
+  const bool tc = tensor_core(d);
+  int32_t *status = reinterpret_cast<int32_t *>(ws);
   const int H = d->n_heads, Hq = d->n_qk_heads;
   const bool shared = Hq < H;
   float *part = reinterpret_cast<float *>(ws + L.off_part);
   float *dots_q = reinterpret_cast<float *>(ws + L.off_dq), *dots_k = reinterpret_cast<float *>(ws + L.off_dk);
-  float *fin = dlog_a && dS_T ? reinterpret_cast<float *>(ws + L.off_fin) : nullptr;
+  float *fin = dlog_a && dS_T && !tc ? reinterpret_cast<float *>(ws + L.off_fin) : nullptr;
+  float *marks = tc ? reinterpret_cast<float *>(ws + L.off_marks) : nullptr;
+  float *mark_dots = tc ? reinterpret_cast<float *>(ws + L.off_mark_dots) : nullptr;
   const Run base = base_run(d, log_a, c, ws, L.cut);
   cudaError_t e;
 
@@ -216,8 +228,8 @@ int bwd_runs(const void *q, const void *k, const void *v, const void *log_a, con
   r.dy = d->d_v; r.dz = d->d_k;
   r.start = S0; r.start_t = 1; r.fin = fin; r.fin_t = 1;
   r.out = shared ? part : dq; r.out_f32 = shared;
-  if (dlog_a) { r.m = q; r.Hm = Hq; r.dots = dots_q; }
-  if ((e = full_run(r, s)) != cudaSuccess) return cuda_fail("linattn dq run", e);
+  if (dlog_a) { r.m = q; r.Hm = Hq; r.dots = dots_q; r.marks = marks; }
+  if ((e = full_run(r, 2, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dq run", e);
   if (shared && (e = gdn2::lin::launch_group_sum(part, dq, c, Hq, d->d_k, d->dtype_in, s)) != cudaSuccess)
     return cuda_fail("linattn dq head sum", e);
 
@@ -227,7 +239,7 @@ int bwd_runs(const void *q, const void *k, const void *v, const void *log_a, con
   r.dy = d->d_k; r.dz = d->d_v;
   r.start = dS_T; r.fin = dS0;
   r.out = dv;
-  if ((e = full_run(r, s)) != cudaSuccess) return cuda_fail("linattn dv run", e);
+  if ((e = full_run(r, 3, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dv run", e);
 
   r = base;  // dk_j = sum_{i >= j} (v_j . dO_i) q_i
   r.back = 1;
@@ -235,13 +247,14 @@ int bwd_runs(const void *q, const void *k, const void *v, const void *log_a, con
   r.dy = d->d_v; r.dz = d->d_k;
   r.start = dS_T; r.start_t = 1;
   r.out = shared ? part : dk; r.out_f32 = shared;
-  if (dlog_a) { r.m = k; r.Hm = Hq; r.dots = dots_k; }
-  if ((e = full_run(r, s)) != cudaSuccess) return cuda_fail("linattn dk run", e);
+  if (dlog_a) { r.m = k; r.Hm = Hq; r.dots = dots_k; r.marks = marks; r.mark_dots = mark_dots; }
+  if ((e = full_run(r, 2, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dk run", e);
   if (shared && (e = gdn2::lin::launch_group_sum(part, dk, c, Hq, d->d_k, d->dtype_in, s)) != cudaSuccess)
     return cuda_fail("linattn dk head sum", e);
   if (dlog_a) {
     const int n = gdn2::lin::simt_slices(d->d_k);
-    e = gdn2::lin::launch_dlog_simt(dots_q, n, dots_k, n, fin, dS_T, d->d_k, d->d_v, c, dlog_a, d->dtype_in, s);
+    e = tc ? gdn2::lin::launch_dlog_tc(dots_q, dots_k, mark_dots, c, dlog_a, s)
+           : gdn2::lin::launch_dlog_simt(dots_q, n, dots_k, n, fin, dS_T, d->d_k, d->d_v, c, dlog_a, d->dtype_in, s);
     if (e != cudaSuccess) return cuda_fail("linattn dlog_a", e);
   }
   return GDN2_OK;
@@ -312,7 +325,7 @@ int gdn2_linattn_fwd(const void *q, const void *k, const void *v, const void *lo
   r.x = q; r.Hx = dims->n_qk_heads; r.y = k; r.Hy = dims->n_qk_heads; r.z = v; r.Hz = dims->n_heads;
   r.dy = dims->d_k; r.dz = dims->d_v;
   r.start = S0; r.fin = S_T; r.out = o;
-  if ((e = full_run(r, s)) != cudaSuccess) return cuda_fail("linattn run", e);
+  if ((e = full_run(r, 3, reinterpret_cast<int32_t *>(ws), tensor_core(dims), s)) != cudaSuccess) return cuda_fail("linattn run", e);
   return GDN2_OK;
 }
 
@@ -368,7 +381,7 @@ int gdn2_linattn_bwd(const void *q, const void *k, const void *v, const void *lo
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = prepare(c, ws, L.cut, s);
   if (e != cudaSuccess) return cuda_fail("linattn workspace", e);
-  return bwd_runs(q, k, v, log_a, S0, cu_seqlens, dO, dS_T, dq, dk, dv, dlog_a, dS0, dims, c, ws, L, s);
+  return bwd_runs(q, k, v, log_a, S0, dO, dS_T, dq, dk, dv, dlog_a, dS0, dims, c, ws, L, s);
 }
 
 int gdn2_ckpt8_save(const void *x, int8_t *codes, uint8_t *scales, int64_t rows, int32_t cols, int32_t dtype,
@@ -428,7 +441,7 @@ int gdn2_linattn_bwd_ckpt8(const int8_t *q_codes, const uint8_t *q_scales, const
                                    dims->dtype_in, s);
     if (e != cudaSuccess) return cuda_fail("ckpt8 restore launch", e);
   }
-  return bwd_runs(ws + L.off_restored[0], ws + L.off_restored[1], ws + L.off_restored[2], log_a, S0, cu_seqlens, dO,
+  return bwd_runs(ws + L.off_restored[0], ws + L.off_restored[1], ws + L.off_restored[2], log_a, S0, dO,
                   dS_T, dq, dk, dv, dlog_a, dS0, dims, c, ws, L, s);
 }
 

@@ -1,0 +1,670 @@
+// linattn_tc.cu -- one run of linear attention with a decay per head on the tensor cores
+// (d_k = d_v = 128, bf16): out_t = sum_j e^{|L_t - L_j|..} (x_t . y_j) z_j + (state part), chunks of
+// 128 tokens, a CTA per (piece, head) that walks its chunks in order (last first when BACK).
+//
+// Per chunk, with D the matrix of decays inside the chunk (0 outside the triangle), w_j the decay
+// from token j to the chunk's far end, f_i the decay from its near end to token i, g the chunk's:
+//   G = X Y^T,  P = bf16(G o D)           (rows = tokens; P becomes a TMEM operand)
+//   out = P Z + f o (X S)                 (two accumulators, joined in fp32 by the epilogue)
+//   S <- g S + (w o Y)^T Z                (S in fp32 registers; the increment in TMEM)
+// The state is exact to fp32: w o Y goes to the tensor cores as a sum of NT bf16 values (3 give 24
+// bits, 2 give 16, for runs whose state only feeds bf16 products), Z is bf16 already.
+//
+// Memory is what bounds it: 4 tiles of 32 KB a chunk, 128 KB against 1.9 us of 6.6 TB/s / 148 SMs;
+// the products take 6 x 512 tensor cycles.  Roles, so that loads, products and the two CUDA-core
+// groups run side by side on two stages of tiles: warp 0 loads, warp 1 issues the products, warp
+// 2 sums the decays, warp 3 stores, warps 4-7 own a token row a thread (P and the epilogue), warps
+// 8-15 own the state.  Tiles are reused in place, which is what makes two stages fit: the first
+// part of w o Y overwrites Y once X Y^T is done, the second X, the third the bf16 state; the out
+// tile is staged in Y's place after the increment.
+#include <cstring>
+
+#include "linattn.cuh"
+#include "tc_util.cuh"
+
+namespace gdn2 {
+namespace lin {
+namespace {
+
+using namespace gdn2::tc;
+
+constexpr int D = 128;
+constexpr int C = kChunk;
+constexpr int kThreads = 512;
+constexpr uint32_t kTile = C * D * 2;       // 32 KB, two column blocks of 64
+constexpr uint32_t kBlock = kTile / 2;
+constexpr uint32_t kStage = 3 * kTile;
+constexpr uint32_t OFF_X = 0, OFF_Y = kTile, OFF_Z = 2 * kTile;
+constexpr uint32_t OFF_S = 2 * kStage;      // the bf16 state, [dz][dy]
+constexpr uint32_t OFF_MISC = OFF_S + kTile;
+// per stage: the decay from each token to the edge of its 32-token block (log2, as a float and its
+// bf16 remainder), 2^(block total - that), the four block totals
+constexpr uint32_t DEC_HI = 0, DEC_LO = 512, DEC_BETA = 768, DEC_TOT = 1280, DEC_BYTES = 1296;
+constexpr uint32_t MISC_BAR = 2 * DEC_BYTES;
+enum {
+  BAR_XY = 0,       // + stage: X and Y loaded
+  BAR_Z = 2,        // + stage: Z loaded
+  BAR_DEC = 4,      // + stage: decays summed
+  BAR_FREE = 6,     // + stage: nothing uses the stage any more
+  BAR_G = 8,        // G done
+  BAR_XS,           // X S done
+  BAR_P,            // P written
+  BAR_PZ,           // P Z done
+  BAR_W,            // w o Y written
+  BAR_U,            // increment done
+  BAR_S,            // bf16 state written
+  BAR_OREAD,        // accumulators of out read
+  BAR_STAGED,       // out tile staged
+  BAR_DRAIN,
+  N_BARS
+};
+constexpr uint32_t MISC_TMEM = MISC_BAR + N_BARS * 8, MISC_ABORT = MISC_TMEM + 4;
+constexpr uint32_t MISC_BYTES = MISC_ABORT + 4;
+constexpr uint32_t kSmemBytes = OFF_MISC + MISC_BYTES;
+static_assert(kSmemBytes <= 232448, "shared memory over the sm_100 limit per CTA");
+constexpr uint32_t TM_G = 0, TM_PZ = 128, TM_XS = 256, TM_U = 384;  // TMEM columns; P overwrites G
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr float kLog2 = 1.4426950408889634f;
+
+struct TcRun {
+  Run r;
+  CUtensorMap tm_x, tm_y, tm_z, tm_o;
+  int32_t *status;
+  uint64_t wait_ns;
+  int dbg_skip;
+};
+
+__device__ __forceinline__ uint64_t kmaj(uint32_t base, int kk) {
+  return ptx::sdesc_sw128(base + (uint32_t)(kk >> 2) * kBlock + (uint32_t)(kk & 3) * 32u, 16, 1024);
+}
+__device__ __forceinline__ uint64_t mnmaj(uint32_t base, int kk) {
+  return ptx::sdesc_sw128(base + (uint32_t)kk * 2048u, kBlock, 1024);
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+template <bool BACK, int NT>
+__global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_constant__ TcRun P) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const Run &r = P.r;
+  const uint32_t sb = ptx::smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int H = r.cut.H, unit = blockIdx.x, h = unit % H;
+  Piece pc;
+  if (!find_piece(r.cut, unit / H, &pc)) return;
+  const bool only = r.state_only != 0;
+  if (only && (pc.count < 2 || pc.s == (BACK ? 0 : pc.count - 1))) return;
+  if (sb & 1023u) {  // the swizzled tiles need it; dynamic shared memory starts on it
+    if (tid == 0) atomicExch(P.status, kStatusTimeout);
+    return;
+  }
+  const int nch = (pc.len + C - 1) / C;
+  auto bar = [&](int b) { return sb + OFF_MISC + MISC_BAR + 8u * (uint32_t)b; };
+  auto dec = [&](int s) { return sb + OFF_MISC + (uint32_t)s * DEC_BYTES; };
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + MISC_ABORT);
+  auto wait = [&](int b, uint32_t parity) { return wait_bar(bar(b), parity & 1u, abort_flag, P.status, P.wait_ns); };
+  // the same for whole warps, which stay together whether or not it gives up
+  auto wait_warp = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+  // tokens of the k-th chunk walked: its number and how many rows it has
+  auto chunk_no = [&](int k) { return BACK ? nch - 1 - k : k; };
+  auto rows_of = [&](int k) { return min(C, pc.len - chunk_no(k) * C); };
+
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(bar(BAR_XY + s), 1);
+      ptx::mbar_init(bar(BAR_Z + s), 1);
+      ptx::mbar_init(bar(BAR_DEC + s), 1);
+      ptx::mbar_init(bar(BAR_FREE + s), 1);
+    }
+    ptx::mbar_init(bar(BAR_G), 1);
+    ptx::mbar_init(bar(BAR_XS), 1);
+    ptx::mbar_init(bar(BAR_P), 128);
+    ptx::mbar_init(bar(BAR_PZ), 1);
+    ptx::mbar_init(bar(BAR_W), 256);
+    ptx::mbar_init(bar(BAR_U), 1);
+    ptx::mbar_init(bar(BAR_S), 256);
+    ptx::mbar_init(bar(BAR_OREAD), 128);
+    ptx::mbar_init(bar(BAR_STAGED), 128);
+    ptx::mbar_init(bar(BAR_DRAIN), 1);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(sb + OFF_MISC + MISC_TMEM, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tm = *reinterpret_cast<volatile uint32_t *>(smem + OFF_MISC + MISC_TMEM);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loads
+    if (lane == 0) {
+      const int hx = h / (H / r.Hx), hy = h / (H / r.Hy), hz = h / (H / r.Hz);
+      int issued = 0;
+      for (int k = 0; k < nch; ++k) {
+        const int s = k & 1, t0 = pc.t0 + chunk_no(k) * C;
+        if (k >= 2 && !wait(BAR_FREE + s, (uint32_t)(k >> 1) + 1u)) break;
+        const uint32_t st = sb + (uint32_t)s * kStage;
+        ptx::mbar_arrive_expect_tx(bar(BAR_XY + s), only ? kTile : 2 * kTile);
+        issued = k + 1;
+        if (P.dbg_skip && blockIdx.x == 0) break;
+        for (int b = 0; b < 2; ++b) {
+          if (!only) ptx::tma_load_3d(st + OFF_X + b * kBlock, &P.tm_x, b * 64, hx, t0, bar(BAR_XY + s));
+          ptx::tma_load_3d(st + OFF_Y + b * kBlock, &P.tm_y, b * 64, hy, t0, bar(BAR_XY + s));
+        }
+        ptx::mbar_arrive_expect_tx(bar(BAR_Z + s), kTile);
+        for (int b = 0; b < 2; ++b) ptx::tma_load_3d(st + OFF_Z + b * kBlock, &P.tm_z, b * 64, hz, t0, bar(BAR_Z + s));
+      }
+      // every load has to land before the CTA leaves, whether or not somebody waited for it
+      for (int k = max(0, issued - 2); k < issued; ++k) {
+        drain_bar(bar(BAR_XY + (k & 1)), (uint32_t)(k >> 1) & 1u, P.wait_ns);
+        if (!(P.dbg_skip && blockIdx.x == 0)) drain_bar(bar(BAR_Z + (k & 1)), (uint32_t)(k >> 1) & 1u, P.wait_ns);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t idKK = ptx::idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idKN = ptx::idesc_bf16(128, 128, false, true);
+      constexpr uint32_t idNN = ptx::idesc_bf16(128, 128, true, true);
+      for (int k = 0; k < nch; ++k) {
+        const int s = k & 1;
+        const uint32_t st = sb + (uint32_t)s * kStage, par = (uint32_t)(k >> 1);
+        if (!wait(BAR_XY + s, par)) break;
+        if (!only) {
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) ptx::umma_bf16(tm + TM_G, kmaj(st + OFF_X, kk), kmaj(st + OFF_Y, kk), idKK, kk > 0);
+          ptx::umma_commit(bar(BAR_G));
+          if (!wait(BAR_S, (uint32_t)k)) break;
+          if (k && !wait(BAR_OREAD, (uint32_t)k + 1u)) break;
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            ptx::umma_bf16(tm + TM_XS, kmaj(st + OFF_X, kk), kmaj(sb + OFF_S, kk), idKK, kk > 0);
+          ptx::umma_commit(bar(BAR_XS));
+        }
+        if (!wait(BAR_Z + s, par) || !wait(BAR_W, (uint32_t)k)) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int part = 0; part < NT; ++part) {
+          const uint32_t b = part == 0 ? st + OFF_Y : part == 1 ? st + OFF_X : sb + OFF_S;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            ptx::umma_bf16(tm + TM_U, mnmaj(st + OFF_Z, kk), mnmaj(b, kk), idNN, part + kk > 0);
+        }
+        ptx::umma_commit(bar(BAR_U));
+        if (only) {
+          ptx::umma_commit(bar(BAR_FREE + s));
+          continue;
+        }
+        if (!wait(BAR_P, (uint32_t)k)) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          ptx::umma_bf16_ts(tm + TM_PZ, tm + TM_G + kk * 8, mnmaj(st + OFF_Z, kk), idKN, kk > 0);
+        ptx::umma_commit(bar(BAR_PZ));
+      }
+      ptx::umma_commit(bar(BAR_DRAIN));  // all products, before the tensor memory is freed
+      drain_bar(bar(BAR_DRAIN), 0u, P.wait_ns);
+    }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- decays
+    // Lane l sums tokens 4 l .. 4 l + 3 in fp64 (a chunk may hold resets beside weak decays); 8
+    // lanes are a block of 32 tokens.  Forward, `edge` of token i is the log2 decay from its
+    // block's start to it, itself included; backward, from it to the block's end, itself not.
+    const float fixed = r.per_head ? static_cast<const float *>(r.log_a)[h] : 0.f;
+    const __nv_bfloat16 *la = static_cast<const __nv_bfloat16 *>(r.log_a);
+    double logs = 0.0;
+    for (int k = 0; k < nch; ++k) {
+      const int s = k & 1, c0 = chunk_no(k) * C, rows = rows_of(k);
+      float a[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 4 * lane + j;
+        a[j] = i >= rows ? 0.f : r.per_head ? fixed : __bfloat162float(la[(size_t)(pc.t0 + c0 + i) * H + h]);
+        a[j] = fmaxf(a[j], kMinLog);
+      }
+      double own[4];  // inclusive sums inside the lane
+      own[0] = a[0];
+#pragma unroll
+      for (int j = 1; j < 4; ++j) own[j] = own[j - 1] + (double)a[j];
+      double incl = own[3];
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) {
+        const double up = __shfl_up_sync(0xffffffffu, incl, d, 8);
+        if ((lane & 7) >= d) incl += up;
+      }
+      const double total = __shfl_sync(0xffffffffu, incl, 7, 8), before = incl - own[3];
+      if (k >= 2 && !wait_warp(BAR_FREE + s, (uint32_t)(k >> 1) + 1u)) break;
+      float hi[4], beta[4];
+      uint32_t lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const double in = before + own[j];
+        const double edge = (BACK ? total - in : in) * (double)kLog2, rest = (BACK ? in : total - in) * (double)kLog2;
+        hi[j] = (float)edge;
+        lo[j] = bf16_bits((float)(edge - (double)hi[j]));
+        beta[j] = ptx::ex2((float)rest);
+      }
+      const uint32_t at = dec(s);
+      sts_v4(at + DEC_HI + 16 * lane, make_uint4(__float_as_uint(hi[0]), __float_as_uint(hi[1]), __float_as_uint(hi[2]),
+                                                 __float_as_uint(hi[3])));
+      sts_v2(at + DEC_LO + 8 * lane, make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16));
+      sts_v4(at + DEC_BETA + 16 * lane, make_uint4(__float_as_uint(beta[0]), __float_as_uint(beta[1]),
+                                                   __float_as_uint(beta[2]), __float_as_uint(beta[3])));
+      if ((lane & 7) == 0) sts_f32(at + DEC_TOT + (lane >> 3) * 4, (float)(total * (double)kLog2));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(BAR_DEC + s));
+      if (only) {
+        logs += __shfl_sync(0xffffffffu, total, 0) + __shfl_sync(0xffffffffu, total, 8) +
+                __shfl_sync(0xffffffffu, total, 16) + __shfl_sync(0xffffffffu, total, 24);
+      }
+    }
+    if (only && lane == 0) r.piece_log[unit] = logs;
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- stores
+    if (lane == 0 && !only) {
+      for (int k = 0; k < nch; ++k) {
+        const int s = k & 1;
+        if (!wait(BAR_STAGED, (uint32_t)k)) break;
+        if (!r.out_f32 && rows_of(k) == C) {
+          const uint32_t src = sb + (uint32_t)s * kStage + OFF_Y;
+          const int t0 = pc.t0 + chunk_no(k) * C;
+          for (int b = 0; b < 2; ++b) ptx::tma_store_3d(&P.tm_o, src + b * kBlock, b * 64, h, t0);
+          ptx::bulk_commit_group();
+          ptx::bulk_wait_group_read0();
+        }
+        ptx::mbar_arrive(bar(BAR_FREE + s));
+      }
+      ptx::bulk_wait_group0();
+    }
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- P and out: a token row a thread
+    if (!only) {
+      const int wq = warp & 3, row = wq * 32 + lane;
+      const uint32_t lanes = tm + ((uint32_t)(wq * 32) << 16);
+      for (int k = 0; k < nch; ++k) {
+        const int s = k & 1, rows = rows_of(k);
+        const uint32_t at = dec(s);
+        const size_t tok = (size_t)pc.t0 + (size_t)chunk_no(k) * C + row;
+        const __nv_bfloat16 *m = nullptr;
+        if (r.m && row < rows) {
+          m = static_cast<const __nv_bfloat16 *>(r.m) + (tok * r.Hm + h / (H / r.Hm)) * D;
+          prefetch_l2(m);
+          prefetch_l2(m + 64);
+        }
+        if (!wait_warp(BAR_DEC + s, (uint32_t)(k >> 1))) break;
+        const float edge = lds_f32(at + DEC_HI + row * 4), edge_lo = bf16_value(lds_u16(at + DEC_LO + row * 2));
+        const float4 tot = lds_f4(at + DEC_TOT);
+        const float tots[4] = {tot.x, tot.y, tot.z, tot.w};
+        float near = edge;  // log2 f_i: from the chunk's near end
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (BACK ? b > wq : b < wq) near += tots[b];
+        const float f = ptx::ex2(near);
+        if (!wait_warp(BAR_G, (uint32_t)k)) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb) {
+          uint32_t out[16];
+          if (BACK ? cb < wq : cb > wq) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) out[j] = 0u;
+          } else {
+            uint32_t g[32];
+            ptx::tmem_ld32(lanes + TM_G + cb * 32, g);
+            if (cb == wq) {
+              // both tokens in one block: the decay between them, pair by pair
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int j4 = 0; j4 < 8; ++j4) {
+                const float4 e = lds_f4(at + DEC_HI + cb * 128 + j4 * 16);
+                const uint2 l = lds_v2(at + DEC_LO + cb * 64 + j4 * 8);
+                const float eh[4] = {e.x, e.y, e.z, e.w};
+                const float el[4] = {bf16_value((uint16_t)l.x), bf16_value((uint16_t)(l.x >> 16)),
+                                     bf16_value((uint16_t)l.y), bf16_value((uint16_t)(l.y >> 16))};
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int j = j4 * 4 + i;
+                  const float w = ptx::ex2((edge - eh[i]) + (edge_lo - el[i]));
+                  const bool in = (BACK ? j >= lane : j <= lane) && cb * 32 + j < rows;
+                  v[i] = in ? w * __uint_as_float(g[j]) : 0.f;
+                }
+                out[2 * j4] = pack_bf16x2(v[0], v[1]);
+                out[2 * j4 + 1] = pack_bf16x2(v[2], v[3]);
+              }
+            } else {
+              // through the edges of the two blocks: a row factor times a column factor, both <= 1
+              float between = edge;
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                if (BACK ? (b > wq && b < cb) : (b > cb && b < wq)) between += tots[b];
+              const float alpha = ptx::ex2(between);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int j4 = 0; j4 < 8; ++j4) {
+                const float4 be = lds_f4(at + DEC_BETA + cb * 128 + j4 * 16);
+                float v[4] = {alpha * be.x * __uint_as_float(g[4 * j4]), alpha * be.y * __uint_as_float(g[4 * j4 + 1]),
+                              alpha * be.z * __uint_as_float(g[4 * j4 + 2]),
+                              alpha * be.w * __uint_as_float(g[4 * j4 + 3])};
+                if (BACK && rows < C)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    if (cb * 32 + j4 * 4 + i >= rows) v[i] = 0.f;
+                out[2 * j4] = pack_bf16x2(v[0], v[1]);
+                out[2 * j4 + 1] = pack_bf16x2(v[2], v[3]);
+              }
+            }
+          }
+          // columns 16 cb .. are G columns of block cb / 2, read already
+          ptx::tmem_st16(lanes + TM_G + cb * 16, out);
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(BAR_P));
+
+        if (!wait_warp(BAR_XS, (uint32_t)k) || !wait_warp(BAR_U, (uint32_t)k) || !wait_warp(BAR_PZ, (uint32_t)k)) break;
+        ptx::tc_fence_after();
+        float dot = 0.f;
+        const bool whole = rows == C && !r.out_f32;
+        const uint32_t dst = sb + (uint32_t)s * kStage + OFF_Y;
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb) {
+          uint4 mw[4];
+          if (m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mw[j] = *reinterpret_cast<const uint4 *>(m + cb * 32 + 8 * j);
+          uint32_t u[32], v[32];
+          ptx::tmem_ld32(lanes + TM_PZ + cb * 32, u);
+          ptx::tmem_ld32(lanes + TM_XS + cb * 32, v);
+          ptx::tmem_wait_ld();
+          if (cb == 3) {  // the accumulators are in registers
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bar(BAR_OREAD));
+          }
+          float o[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = fmaf(f, __uint_as_float(v[j]), __uint_as_float(u[j]));
+          if (m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t w[4] = {mw[j].x, mw[j].y, mw[j].z, mw[j].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 b = unpack_bf16x2(w[i]);
+                dot = fmaf(b.x, o[8 * j + 2 * i], fmaf(b.y, o[8 * j + 2 * i + 1], dot));
+              }
+            }
+          if (r.out_f32) {
+            if (row < rows) {
+              float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(r.out) + (tok * H + h) * D + cb * 32);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) p[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint4 w = pack8(o + 8 * j, 1.f);
+              if (whole)
+                sts_v4(dst + (uint32_t)(cb >> 1) * kBlock + swz(row, (uint32_t)((cb & 1) * 4 + j)), w);
+              else if (row < rows)
+                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(r.out) + (tok * H + h) * D + cb * 32 + 8 * j) = w;
+            }
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(bar(BAR_STAGED));
+        if (m) r.dots[tok * H + h] = dot;
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- state: warp -> 32 z rows x 64 y columns
+    const int wq = warp & 3, half = (warp - 8) >> 2, zrow = wq * 32 + lane;
+    const int stid = tid - 256;
+    const uint32_t lanes = tm + ((uint32_t)(wq * 32) << 16) + TM_U + half * 64;
+    float S[64];
+    {
+      const float *start = nullptr;
+      bool st = false;
+      if (!only) {
+        if (r.piece_state && pc.count > 1) {
+          start = r.piece_state + (size_t)unit * D * D;
+        } else if (r.start) {
+          start = r.start + ((size_t)pc.n * H + h) * D * D;
+          st = r.start_t;
+        }
+      }
+      if (!start) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) S[j] = 0.f;
+      } else if (!st) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) S[j] = start[(half * 64 + j) * D + zrow];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float4 v = *reinterpret_cast<const float4 *>(start + zrow * D + half * 64 + 4 * j);
+          S[4 * j] = v.x; S[4 * j + 1] = v.y; S[4 * j + 2] = v.z; S[4 * j + 3] = v.w;
+        }
+      }
+    }
+    auto write_state = [&]() {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sts_v4(sb + OFF_S + half * kBlock + swz(zrow, (uint32_t)j), pack8(S + 8 * j, 1.f));
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(bar(BAR_S));
+    };
+    // marks of this thread's part of the state at the end of group `g` of chunks
+    auto mark_unit = [&](int g) { return (size_t)mark_slot(unit / H, pc.t0 + g * kGroup * C) * H + h; };
+    auto ends_group = [&](int no) { return (no + 1) % kGroup == 0 || no == nch - 1; };
+    if (!only && nch > 0) write_state();
+    bool ok = true;
+    for (int k = 0; k < nch && ok; ++k) {
+      const int s = k & 1, rows = rows_of(k);
+      if (BACK && r.mark_dots && !only) {
+        const int no = chunk_no(k);
+        if (ends_group(no)) {
+          const size_t mu = mark_unit(no / kGroup);
+          const float4 *mark = reinterpret_cast<const float4 *>(r.marks + mu * (D * D)) + stid;
+          float dot = 0.f;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float4 v = mark[j * 256];
+            dot = fmaf(v.x, S[4 * j], fmaf(v.y, S[4 * j + 1], fmaf(v.z, S[4 * j + 2], fmaf(v.w, S[4 * j + 3], dot))));
+          }
+#pragma unroll
+          for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+          if (lane == 0) r.mark_dots[mu * 8 + (warp - 8)] = dot;
+        }
+        if (no % kGroup == 1 && no > kGroup) {  // the next group's mark, two chunks ahead
+          const char *next = reinterpret_cast<const char *>(r.marks + mark_unit(no / kGroup - 1) * (D * D)) + stid * 256;
+          prefetch_l2(next);
+          prefetch_l2(next + 128);
+        }
+      }
+      const uint32_t st = sb + (uint32_t)s * kStage, par = (uint32_t)(k >> 1);
+      ok = wait_warp(BAR_DEC + s, par) && wait_warp(BAR_XY + s, par) && (rows == C || wait_warp(BAR_Z + s, par));
+      // Y is free to be overwritten after X Y^T, X and the bf16 state after X S
+      if (ok && !only) ok = wait_warp(BAR_G, (uint32_t)k) && wait_warp(BAR_XS, (uint32_t)k);
+      if (!ok) break;
+      const float4 tot = lds_f4(dec(s) + DEC_TOT);
+      const float tots[4] = {tot.x, tot.y, tot.z, tot.w};
+      const float g = ptx::ex2((tot.x + tot.y) + (tot.z + tot.w));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int t = i * 16 + (stid >> 4);
+        const uint32_t c = (uint32_t)(stid & 15), off = (c >> 3) * kBlock + swz(t, c & 7u);
+        float far = 0.f;  // from the edge of the token's block to the chunk's far end
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (BACK ? b < (i >> 1) : b > (i >> 1)) far += tots[b];
+        const bool in = t < rows;
+        const float w = lds_f32(dec(s) + DEC_BETA + t * 4) * ptx::ex2(far);
+        const uint4 y = lds_v4(st + OFF_Y + off);
+        const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
+        uint32_t part[3][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 v = unpack_bf16x2(yw[j]);
+          v.x = in ? v.x * w : 0.f;
+          v.y = in ? v.y * w : 0.f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            part[n][j] = pack_bf16x2(v.x, v.y);
+            const float2 b = unpack_bf16x2(part[n][j]);
+            v.x -= b.x;
+            v.y -= b.y;
+          }
+        }
+        sts_v4(st + OFF_Y + off, make_uint4(part[0][0], part[0][1], part[0][2], part[0][3]));
+        sts_v4(st + OFF_X + off, make_uint4(part[1][0], part[1][1], part[1][2], part[1][3]));
+        if constexpr (NT == 3) sts_v4(sb + OFF_S + off, make_uint4(part[2][0], part[2][1], part[2][2], part[2][3]));
+        // rows behind the sequence: their Z meets zero weights, which a NaN would outlive
+        if (!in) sts_v4(st + OFF_Z + off, make_uint4(0u, 0u, 0u, 0u));
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(bar(BAR_W));
+      ok = wait_warp(BAR_U, (uint32_t)k);
+      if (!ok) break;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t u[32];
+        ptx::tmem_ld32(lanes + c * 32, u);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) S[c * 32 + j] = fmaf(g, S[c * 32 + j], __uint_as_float(u[j]));
+      }
+      ptx::tc_fence_before();
+      if (!only && k + 1 < nch) write_state();
+      if (!BACK && r.marks && !only && ends_group(k)) {
+        float4 *mark = reinterpret_cast<float4 *>(r.marks + mark_unit(k / kGroup) * (D * D)) + stid;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) mark[j * 256] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+      }
+    }
+    float *dst = nullptr;
+    bool dt = false;
+    if (only) {
+      dst = r.piece_state + (size_t)unit * D * D;
+    } else if (r.fin && pc.s == (BACK ? 0 : pc.count - 1)) {
+      dst = r.fin + ((size_t)pc.n * H + h) * D * D;
+      dt = r.fin_t;
+    }
+    if (dst && ok) {
+      if (!dt) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) dst[(half * 64 + j) * D + zrow] = S[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          *reinterpret_cast<float4 *>(dst + zrow * D + half * 64 + 4 * j) =
+              make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+      }
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tm, 512);
+  }
+}
+
+// dlog_a_t = sum_{t <= i in the group} (q_i . dq_i - k_i . dk_i) + <S, dLoss/dS> behind the group.  The dots carry
+// bf16 products whose errors would add up along a sequence; the marks' product starts each group afresh.
+// A warp per group of kGroup chunks, 16 tokens a lane.
+constexpr int kDlogWarps = 4;
+__global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *dots_q, const float *dots_k,
+                                                                  const float *mark_dots, Cut c, __nv_bfloat16 *dlog) {
+  constexpr int kTokens = kGroup * C, kEach = kTokens / 32;
+  const int H = c.H, unit = blockIdx.x, h = unit % H, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Piece pc;
+  if (!find_piece(c, unit / H, &pc)) return;
+  for (int g = blockIdx.y * kDlogWarps + warp; g * kTokens < pc.len; g += gridDim.y * kDlogWarps) {
+    const size_t t0 = (size_t)pc.t0 + (size_t)g * kTokens;
+    const int cnt = min(kTokens, pc.len - g * kTokens), first = lane * kEach;
+    float v[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const size_t at = (t0 + first + j) * H + h;
+      v[j] = first + j < cnt ? dots_q[at] - dots_k[at] : 0.f;
+    }
+#pragma unroll
+    for (int j = kEach - 2; j >= 0; --j) v[j] += v[j + 1];
+    const float own = v[0];
+    float incl = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const float down = __shfl_down_sync(0xffffffffu, incl, d);
+      if (lane + d < 32) incl += down;
+    }
+    const float *end = mark_dots + ((size_t)mark_slot(unit / H, (int)t0) * H + h) * 8;
+    float behind = incl - own;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) behind += end[w];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (first + j < cnt) dlog[(t0 + first + j) * H + h] = __float2bfloat16_rn(v[j] + behind);
+  }
+}
+
+template <bool BACK, int NT>
+cudaError_t launch_t(const TcRun &P, cudaStream_t s) {
+  auto kern = run_tc_kernel<BACK, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)((int64_t)P.r.cut.n_pieces * P.r.cut.H), kThreads, kSmemBytes, s>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_run_tc(const Run &r, int terms, int32_t *status, cudaStream_t s) {
+  TcRun P;
+  memset(&P, 0, sizeof(P));
+  P.r = r;
+  P.status = status;
+  P.wait_ns = kWaitNs;
+  const int64_t T = r.cut.t_total;
+  if (T > 0) {
+    bool ok = make_row_tile_map(&P.tm_y, r.y, T, r.Hy, C) && make_row_tile_map(&P.tm_z, r.z, T, r.Hz, C);
+    if (ok && !r.state_only) ok = make_row_tile_map(&P.tm_x, r.x, T, r.Hx, C);
+    if (ok && !r.state_only && !r.out_f32) ok = make_row_tile_map(&P.tm_o, r.out, T, r.cut.H, C);
+    if (!ok) return cudaErrorInvalidValue;
+  }
+  uint64_t hook_ns = 0;
+  if (take_debug_timeout(GDN2_DEBUG_LINATTN, &hook_ns)) {
+    P.dbg_skip = 1;
+    P.wait_ns = hook_ns;
+  }
+  if (r.back) return terms == 3 ? launch_t<true, 3>(P, s) : launch_t<true, 2>(P, s);
+  return terms == 3 ? launch_t<false, 3>(P, s) : launch_t<false, 2>(P, s);
+}
+
+cudaError_t launch_dlog_tc(const float *dots_q, const float *dots_k, const float *mark_dots, const Cut &c, void *dlog,
+                           cudaStream_t s) {
+  if (c.t_total == 0) return cudaSuccess;
+  const int64_t groups = (int64_t)c.t_total / (kGroup * C * kDlogWarps) + 1;  // of the longest piece, at most
+  const dim3 grid((unsigned)((int64_t)c.n_pieces * c.H), (unsigned)(groups < 16 ? groups : 16));
+  dlog_tc_kernel<<<grid, 32 * kDlogWarps, 0, s>>>(dots_q, dots_k, mark_dots, c, static_cast<__nv_bfloat16 *>(dlog));
+  return cudaGetLastError();
+}
+
+}  // namespace lin
+}  // namespace gdn2

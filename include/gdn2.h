@@ -570,7 +570,8 @@ size_t gdn2_linattn_bwd_ckpt8_workspace_size(const gdn2_linattn_dims *dims, int3
  *                      built on it),
  *   GDN2_DEBUG_DECODE  the streaming decode kernel (d_k = d_v = 128),
  *   GDN2_DEBUG_BWD     the reverse kernel of gdn2_chunk_bwd (its checkpointing
- *                      forward runs normally).
+ *                      forward runs normally),
+ *   GDN2_DEBUG_LINATTN the tensor-core run of the linear-attention calls.
  * In that launch every bounded wait uses the limit `wait_ns` instead of 1 s, and
  * the first CTA announces the bytes of its first load group to its mbarrier but
  * issues none of the copies, so its wait runs out: the kernel records
@@ -583,7 +584,12 @@ size_t gdn2_linattn_bwd_ckpt8_workspace_size(const gdn2_linattn_dims *dims, int3
  * Errors: GDN2_ERR_INVALID_ARG for an unknown site or wait_ns outside
  * [1000, 10^10].
  */
-enum gdn2_debug_site { GDN2_DEBUG_CHUNK = 1, GDN2_DEBUG_DECODE = 2, GDN2_DEBUG_BWD = 3 };
+enum gdn2_debug_site {
+  GDN2_DEBUG_CHUNK = 1,
+  GDN2_DEBUG_DECODE = 2,
+  GDN2_DEBUG_BWD = 3,
+  GDN2_DEBUG_LINATTN = 4
+};
 int gdn2_debug_timeout_once(int32_t site, uint64_t wait_ns);
 
 /* Thread-local description of the last non-zero status on this thread ("" if none). */
