@@ -10,13 +10,15 @@
 // The state is exact to fp32: w o Y goes to the tensor cores as a sum of NT bf16 values (3 give 24
 // bits, 2 give 16, for runs whose state only feeds bf16 products), Z is bf16 already.
 //
-// Memory is what bounds it: 4 tiles of 32 KB a chunk, 128 KB against 1.9 us of 6.6 TB/s / 148 SMs;
-// the products take 6 x 512 tensor cycles.  Roles, so that loads, products and the two CUDA-core
-// groups run side by side on two stages of tiles: warp 0 loads, warp 1 issues the products, warp
-// 2 sums the decays, warp 3 stores, warps 4-7 own a token row a thread (P and the epilogue), warps
-// 8-15 own the state.  Tiles are reused in place, which is what makes two stages fit: the first
-// part of w o Y overwrites Y once X Y^T is done, the second X, the third the bf16 state; the out
-// tile is staged in Y's place after the increment.
+// Memory is what bounds it: 4 tiles of 32 KB a chunk, 128 KB against 2.9 us of 6.6 TB/s / 148 SMs;
+// the products take 6 x 512 tensor cycles.  One chain runs through the chunks: the state, its bf16
+// copy, X S; the update waits for nothing but the previous one.  Roles, side by side: warp 0 loads;
+// warp 1 issues the state's products (X S, the update), warp 3 the rows' (G, P Z); warp 2 sums the
+// decays and stores; warps 4-7 own a token row a thread (P, f o X S as the start of P Z's
+// accumulator, out); warps 8-15 own the state and weight Y.  What fits two stages of Y and Z into
+// shared memory: X has one, the first bf16 term of w o Y overwrites Y once X Y^T is done, the other
+// terms pass through a ring of 32-token slices, and out is staged in Y's place after the update.
+// Loops are kept rolled: unrolled, the roles together ran out of the instruction cache.
 #include <cstring>
 
 #include "linattn.cuh"
@@ -33,30 +35,34 @@ constexpr int C = kChunk;
 constexpr int kThreads = 512;
 constexpr uint32_t kTile = C * D * 2;       // 32 KB, two column blocks of 64
 constexpr uint32_t kBlock = kTile / 2;
-constexpr uint32_t kStage = 3 * kTile;
-constexpr uint32_t OFF_X = 0, OFF_Y = kTile, OFF_Z = 2 * kTile;
-constexpr uint32_t OFF_S = 2 * kStage;      // the bf16 state, [dz][dy]
-constexpr uint32_t OFF_MISC = OFF_S + kTile;
+constexpr int kSlice = 32;                  // tokens of a slice of w o Y
+constexpr uint32_t kSliceTile = kSlice * D * 2, kSliceBlock = kSliceTile / 2;
+constexpr uint32_t OFF_X = 0, OFF_Y = kTile, OFF_Z = 3 * kTile;  // Y, Z: two stages
+constexpr uint32_t OFF_S = 5 * kTile;       // the bf16 state, [dz][dy]
+constexpr uint32_t OFF_W = 6 * kTile;       // the ring
+constexpr uint32_t OFF_MISC = 7 * kTile;
 // per stage: the decay from each token to the edge of its 32-token block (log2, as a float and its
 // bf16 remainder), 2^(block total - that), the four block totals
 constexpr uint32_t DEC_HI = 0, DEC_LO = 512, DEC_BETA = 768, DEC_TOT = 1280, DEC_BYTES = 1296;
 constexpr uint32_t MISC_BAR = 2 * DEC_BYTES;
 enum {
-  BAR_XY = 0,       // + stage: X and Y loaded
+  BAR_Y = 0,        // + stage: Y loaded
   BAR_Z = 2,        // + stage: Z loaded
   BAR_DEC = 4,      // + stage: decays summed
-  BAR_FREE = 6,     // + stage: nothing uses the stage any more
-  BAR_G = 8,        // G done
+  BAR_FREE = 6,     // + stage: nothing uses Y and Z any more
+  BAR_FULL = 8,     // + slot: a slice of w o Y written
+  BAR_EMPTY = 12,   // + slot: its products done
+  BAR_X = 16,       // X loaded
+  BAR_XFREE,        // X Y^T and X S done
+  BAR_G,            // X Y^T done
   BAR_XS,           // X S done
-  BAR_P,            // P written
+  BAR_P,            // P written, f o X S in place
   BAR_PZ,           // P Z done
-  BAR_W,            // w o Y written
   BAR_U,            // increment done
   BAR_S,            // bf16 state written
-  BAR_OREAD,        // accumulators of out read
   BAR_STAGED,       // out tile staged
-  BAR_DRAIN,
-  N_BARS
+  BAR_DRAIN,        // + 0, 1
+  N_BARS = BAR_DRAIN + 2
 };
 constexpr uint32_t MISC_TMEM = MISC_BAR + N_BARS * 8, MISC_ABORT = MISC_TMEM + 4;
 constexpr uint32_t MISC_BYTES = MISC_ABORT + 4;
@@ -77,8 +83,8 @@ struct TcRun {
 __device__ __forceinline__ uint64_t kmaj(uint32_t base, int kk) {
   return ptx::sdesc_sw128(base + (uint32_t)(kk >> 2) * kBlock + (uint32_t)(kk & 3) * 32u, 16, 1024);
 }
-__device__ __forceinline__ uint64_t mnmaj(uint32_t base, int kk) {
-  return ptx::sdesc_sw128(base + (uint32_t)kk * 2048u, kBlock, 1024);
+__device__ __forceinline__ uint64_t mnmaj(uint32_t base, int kk, uint32_t block = kBlock) {
+  return ptx::sdesc_sw128(base + (uint32_t)kk * 2048u, block, 1024);
 }
 __device__ __forceinline__ float lds_f32(uint32_t a) {
   float v;
@@ -95,6 +101,7 @@ __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefe
 
 template <bool BACK, int NT>
 __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_constant__ TcRun P) {
+  constexpr int SLOTS = NT == 3 ? 2 : 4;  // of the ring: NT - 1 slice tiles each
   extern __shared__ __align__(1024) uint8_t smem[];
   const Run &r = P.r;
   const uint32_t sb = ptx::smem_u32(smem);
@@ -121,22 +128,10 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
 
   if (tid == 0) {
     *abort_flag = 0;
-    for (int s = 0; s < 2; ++s) {
-      ptx::mbar_init(bar(BAR_XY + s), 1);
-      ptx::mbar_init(bar(BAR_Z + s), 1);
-      ptx::mbar_init(bar(BAR_DEC + s), 1);
-      ptx::mbar_init(bar(BAR_FREE + s), 1);
+    for (int b = 0; b < N_BARS; ++b) {
+      const bool rows = b == BAR_P || b == BAR_STAGED, state = b == BAR_S || (b >= BAR_FULL && b < BAR_EMPTY);
+      ptx::mbar_init(bar(b), rows ? 4 : state ? 8 : b == BAR_XFREE ? 2 : 1);
     }
-    ptx::mbar_init(bar(BAR_G), 1);
-    ptx::mbar_init(bar(BAR_XS), 1);
-    ptx::mbar_init(bar(BAR_P), 128);
-    ptx::mbar_init(bar(BAR_PZ), 1);
-    ptx::mbar_init(bar(BAR_W), 256);
-    ptx::mbar_init(bar(BAR_U), 1);
-    ptx::mbar_init(bar(BAR_S), 256);
-    ptx::mbar_init(bar(BAR_OREAD), 128);
-    ptx::mbar_init(bar(BAR_STAGED), 128);
-    ptx::mbar_init(bar(BAR_DRAIN), 1);
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
@@ -152,95 +147,142 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
       const int hx = h / (H / r.Hx), hy = h / (H / r.Hy), hz = h / (H / r.Hz);
-      int issued = 0;
+      const bool skip = P.dbg_skip && blockIdx.x == 0;
+      int k_yz = 0, k_x = 0;  // loads asked for
       for (int k = 0; k < nch; ++k) {
         const int s = k & 1, t0 = pc.t0 + chunk_no(k) * C;
         if (k >= 2 && !wait(BAR_FREE + s, (uint32_t)(k >> 1) + 1u)) break;
-        const uint32_t st = sb + (uint32_t)s * kStage;
-        ptx::mbar_arrive_expect_tx(bar(BAR_XY + s), only ? kTile : 2 * kTile);
-        issued = k + 1;
-        if (P.dbg_skip && blockIdx.x == 0) break;
-        for (int b = 0; b < 2; ++b) {
-          if (!only) ptx::tma_load_3d(st + OFF_X + b * kBlock, &P.tm_x, b * 64, hx, t0, bar(BAR_XY + s));
-          ptx::tma_load_3d(st + OFF_Y + b * kBlock, &P.tm_y, b * 64, hy, t0, bar(BAR_XY + s));
-        }
+        ptx::mbar_arrive_expect_tx(bar(BAR_Y + s), kTile);
+        k_yz = k + 1;
+        if (skip) break;
+        for (int b = 0; b < 2; ++b)
+          ptx::tma_load_3d(sb + OFF_Y + s * kTile + b * kBlock, &P.tm_y, b * 64, hy, t0, bar(BAR_Y + s));
         ptx::mbar_arrive_expect_tx(bar(BAR_Z + s), kTile);
-        for (int b = 0; b < 2; ++b) ptx::tma_load_3d(st + OFF_Z + b * kBlock, &P.tm_z, b * 64, hz, t0, bar(BAR_Z + s));
+        for (int b = 0; b < 2; ++b)
+          ptx::tma_load_3d(sb + OFF_Z + s * kTile + b * kBlock, &P.tm_z, b * 64, hz, t0, bar(BAR_Z + s));
+        if (only) continue;
+        if (k >= 1 && !wait(BAR_XFREE, (uint32_t)k + 1u)) break;
+        ptx::mbar_arrive_expect_tx(bar(BAR_X), kTile);
+        k_x = k + 1;
+        for (int b = 0; b < 2; ++b) ptx::tma_load_3d(sb + OFF_X + b * kBlock, &P.tm_x, b * 64, hx, t0, bar(BAR_X));
+        if (k + 1 < nch)
+          for (int b = 0; b < 2; ++b) ptx::tma_prefetch_3d(&P.tm_x, b * 64, hx, pc.t0 + chunk_no(k + 1) * C);
       }
       // every load has to land before the CTA leaves, whether or not somebody waited for it
-      for (int k = max(0, issued - 2); k < issued; ++k) {
-        drain_bar(bar(BAR_XY + (k & 1)), (uint32_t)(k >> 1) & 1u, P.wait_ns);
-        if (!(P.dbg_skip && blockIdx.x == 0)) drain_bar(bar(BAR_Z + (k & 1)), (uint32_t)(k >> 1) & 1u, P.wait_ns);
+      for (int k = max(0, k_yz - 2); k < k_yz; ++k) {
+        drain_bar(bar(BAR_Y + (k & 1)), (uint32_t)(k >> 1) & 1u, P.wait_ns);
+        if (!skip) drain_bar(bar(BAR_Z + (k & 1)), (uint32_t)(k >> 1) & 1u, P.wait_ns);
       }
+      if (k_x) drain_bar(bar(BAR_X), (uint32_t)(k_x - 1) & 1u, P.wait_ns);
     }
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- products
+    // ---------------------------------------------------------------- the state's products
     if (lane == 0) {
       constexpr uint32_t idKK = ptx::idesc_bf16(128, 128, false, false);
-      constexpr uint32_t idKN = ptx::idesc_bf16(128, 128, false, true);
       constexpr uint32_t idNN = ptx::idesc_bf16(128, 128, true, true);
-      for (int k = 0; k < nch; ++k) {
+      bool ok = true;
+      for (int k = 0; k < nch && ok; ++k) {
         const int s = k & 1;
-        const uint32_t st = sb + (uint32_t)s * kStage, par = (uint32_t)(k >> 1);
-        if (!wait(BAR_XY + s, par)) break;
+        const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile, z = sb + OFF_Z + (uint32_t)s * kTile;
         if (!only) {
-          ptx::tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) ptx::umma_bf16(tm + TM_G, kmaj(st + OFF_X, kk), kmaj(st + OFF_Y, kk), idKK, kk > 0);
-          ptx::umma_commit(bar(BAR_G));
-          if (!wait(BAR_S, (uint32_t)k)) break;
-          if (k && !wait(BAR_OREAD, (uint32_t)k + 1u)) break;
+          // the state's copy, and the last X S read
+          if (!wait(BAR_X, (uint32_t)k) || !wait(BAR_S, (uint32_t)k) || (k && !wait(BAR_P, (uint32_t)k + 1u))) break;
           ptx::tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            ptx::umma_bf16(tm + TM_XS, kmaj(st + OFF_X, kk), kmaj(sb + OFF_S, kk), idKK, kk > 0);
+            ptx::umma_bf16(tm + TM_XS, kmaj(sb + OFF_X, kk), kmaj(sb + OFF_S, kk), idKK, kk > 0);
           ptx::umma_commit(bar(BAR_XS));
+          ptx::umma_commit(bar(BAR_XFREE));
         }
-        if (!wait(BAR_Z + s, par) || !wait(BAR_W, (uint32_t)k)) break;
-        ptx::tc_fence_after();
+        if (!wait(BAR_Z + s, (uint32_t)(k >> 1))) break;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int n = 4 * k + i, slot = n % SLOTS, b = BACK ? i : 3 - i;
+          ok = wait(BAR_FULL + slot, (uint32_t)(n / SLOTS));
+          if (!ok) break;
+          ptx::tc_fence_after();
 #pragma unroll
-        for (int part = 0; part < NT; ++part) {
-          const uint32_t b = part == 0 ? st + OFF_Y : part == 1 ? st + OFF_X : sb + OFF_S;
+          for (int part = 0; part < NT; ++part)
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            ptx::umma_bf16(tm + TM_U, mnmaj(st + OFF_Z, kk), mnmaj(b, kk), idNN, part + kk > 0);
+            for (int kk = 0; kk < 2; ++kk) {
+              const uint32_t w = sb + OFF_W + (uint32_t)(slot * (NT - 1) + part - 1) * kSliceTile;
+              ptx::umma_bf16(tm + TM_U, mnmaj(z, 2 * b + kk),
+                             part == 0 ? mnmaj(y, 2 * b + kk) : mnmaj(w, kk, kSliceBlock), idNN,
+                             (i > 0) | (part + kk > 0));
+            }
+          ptx::umma_commit(bar(BAR_EMPTY + slot));
         }
+        if (!ok) break;
         ptx::umma_commit(bar(BAR_U));
-        if (only) {
-          ptx::umma_commit(bar(BAR_FREE + s));
-          continue;
-        }
-        if (!wait(BAR_P, (uint32_t)k)) break;
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          ptx::umma_bf16_ts(tm + TM_PZ, tm + TM_G + kk * 8, mnmaj(st + OFF_Z, kk), idKN, kk > 0);
-        ptx::umma_commit(bar(BAR_PZ));
+        if (only) ptx::umma_commit(bar(BAR_FREE + s));
       }
       ptx::umma_commit(bar(BAR_DRAIN));  // all products, before the tensor memory is freed
       drain_bar(bar(BAR_DRAIN), 0u, P.wait_ns);
     }
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- the rows' products
+    if (lane == 0 && !only) {
+      constexpr uint32_t idKK = ptx::idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idKN = ptx::idesc_bf16(128, 128, false, true);
+      for (int k = 0; k < nch; ++k) {
+        const int s = k & 1;
+        const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile, z = sb + OFF_Z + (uint32_t)s * kTile;
+        if (!wait(BAR_X, (uint32_t)k) || !wait(BAR_Y + s, (uint32_t)(k >> 1))) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) ptx::umma_bf16(tm + TM_G, kmaj(sb + OFF_X, kk), kmaj(y, kk), idKK, kk > 0);
+        ptx::umma_commit(bar(BAR_G));
+        ptx::umma_commit(bar(BAR_XFREE));
+        if (!wait(BAR_Z + s, (uint32_t)(k >> 1)) || !wait(BAR_P, (uint32_t)k)) break;
+        if (rows_of(k) < C && !wait(BAR_U, (uint32_t)k)) break;  // Z's rows behind the sequence cleared
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) ptx::umma_bf16_ts(tm + TM_PZ, tm + TM_G + kk * 8, mnmaj(z, kk), idKN, 1u);
+        ptx::umma_commit(bar(BAR_PZ));
+      }
+      ptx::umma_commit(bar(BAR_DRAIN + 1));
+      drain_bar(bar(BAR_DRAIN + 1), 0u, P.wait_ns);
+    }
   } else if (warp == 2) {
-    // ---------------------------------------------------------------- decays
+    // ---------------------------------------------------------------- decays and stores
     // Lane l sums tokens 4 l .. 4 l + 3 in fp64 (a chunk may hold resets beside weak decays); 8
     // lanes are a block of 32 tokens.  Forward, `edge` of token i is the log2 decay from its
     // block's start to it, itself included; backward, from it to the block's end, itself not.
     const float fixed = r.per_head ? static_cast<const float *>(r.log_a)[h] : 0.f;
     const __nv_bfloat16 *la = static_cast<const __nv_bfloat16 *>(r.log_a);
-    double logs = 0.0;
-    for (int k = 0; k < nch; ++k) {
-      const int s = k & 1, c0 = chunk_no(k) * C, rows = rows_of(k);
-      float a[4];
+    auto load = [&](int k, float (&a)[4]) {
+      const int c0 = chunk_no(k) * C, rows = rows_of(k);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = 4 * lane + j;
         a[j] = i >= rows ? 0.f : r.per_head ? fixed : __bfloat162float(la[(size_t)(pc.t0 + c0 + i) * H + h]);
-        a[j] = fmaxf(a[j], kMinLog);
       }
+    };
+    // chunk k's out tile; the stage is free once it has been read
+    auto store = [&](int k) {
+      if (only) return wait_warp(BAR_FREE + (k & 1), (uint32_t)(k >> 1));
+      if (!wait_warp(BAR_STAGED, (uint32_t)k)) return false;
+      if (lane == 0) {
+        if (!r.out_f32 && rows_of(k) == C) {
+          const uint32_t src = sb + OFF_Y + (uint32_t)(k & 1) * kTile;
+          const int t0 = pc.t0 + chunk_no(k) * C;
+          for (int b = 0; b < 2; ++b) ptx::tma_store_3d(&P.tm_o, src + b * kBlock, b * 64, h, t0);
+          ptx::bulk_commit_group();
+          ptx::bulk_wait_group_read0();
+        }
+        ptx::mbar_arrive(bar(BAR_FREE + (k & 1)));
+      }
+      return true;
+    };
+    double logs = 0.0;
+    float a[4];
+    if (nch > 0) load(0, a);
+    bool ok = true;
+    for (int k = 0; k < nch; ++k) {
       double own[4];  // inclusive sums inside the lane
-      own[0] = a[0];
 #pragma unroll
-      for (int j = 1; j < 4; ++j) own[j] = own[j - 1] + (double)a[j];
+      for (int j = 0; j < 4; ++j) own[j] = (double)fmaxf(a[j], kMinLog) + (j ? own[j - 1] : 0.0);
+      if (k + 1 < nch) load(k + 1, a);
       double incl = own[3];
 #pragma unroll
       for (int d = 1; d < 8; d <<= 1) {
@@ -248,7 +290,6 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         if ((lane & 7) >= d) incl += up;
       }
       const double total = __shfl_sync(0xffffffffu, incl, 7, 8), before = incl - own[3];
-      if (k >= 2 && !wait_warp(BAR_FREE + s, (uint32_t)(k >> 1) + 1u)) break;
       float hi[4], beta[4];
       uint32_t lo[4];
 #pragma unroll
@@ -259,7 +300,9 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         lo[j] = bf16_bits((float)(edge - (double)hi[j]));
         beta[j] = ptx::ex2((float)rest);
       }
-      const uint32_t at = dec(s);
+      if (k >= 2) ok = store(k - 2);
+      if (!ok) break;
+      const uint32_t at = dec(k & 1);
       sts_v4(at + DEC_HI + 16 * lane, make_uint4(__float_as_uint(hi[0]), __float_as_uint(hi[1]), __float_as_uint(hi[2]),
                                                  __float_as_uint(hi[3])));
       sts_v2(at + DEC_LO + 8 * lane, make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16));
@@ -267,29 +310,17 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
                                                    __float_as_uint(beta[2]), __float_as_uint(beta[3])));
       if ((lane & 7) == 0) sts_f32(at + DEC_TOT + (lane >> 3) * 4, (float)(total * (double)kLog2));
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(BAR_DEC + s));
+      if (lane == 0) ptx::mbar_arrive(bar(BAR_DEC + (k & 1)));
       if (only) {
         logs += __shfl_sync(0xffffffffu, total, 0) + __shfl_sync(0xffffffffu, total, 8) +
                 __shfl_sync(0xffffffffu, total, 16) + __shfl_sync(0xffffffffu, total, 24);
       }
     }
-    if (only && lane == 0) r.piece_log[unit] = logs;
-  } else if (warp == 3) {
-    // ---------------------------------------------------------------- stores
-    if (lane == 0 && !only) {
-      for (int k = 0; k < nch; ++k) {
-        const int s = k & 1;
-        if (!wait(BAR_STAGED, (uint32_t)k)) break;
-        if (!r.out_f32 && rows_of(k) == C) {
-          const uint32_t src = sb + (uint32_t)s * kStage + OFF_Y;
-          const int t0 = pc.t0 + chunk_no(k) * C;
-          for (int b = 0; b < 2; ++b) ptx::tma_store_3d(&P.tm_o, src + b * kBlock, b * 64, h, t0);
-          ptx::bulk_commit_group();
-          ptx::bulk_wait_group_read0();
-        }
-        ptx::mbar_arrive(bar(BAR_FREE + s));
-      }
-      ptx::bulk_wait_group0();
+    if (only) {
+      if (lane == 0) r.piece_log[unit] = logs;
+    } else {
+      for (int k = max(0, nch - 2); k < nch && ok; ++k) ok = store(k);
+      if (lane == 0) ptx::bulk_wait_group0();
     }
   } else if (warp < 8) {
     // ---------------------------------------------------------------- P and out: a token row a thread
@@ -308,16 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         }
         if (!wait_warp(BAR_DEC + s, (uint32_t)(k >> 1))) break;
         const float edge = lds_f32(at + DEC_HI + row * 4), edge_lo = bf16_value(lds_u16(at + DEC_LO + row * 2));
-        const float4 tot = lds_f4(at + DEC_TOT);
-        const float tots[4] = {tot.x, tot.y, tot.z, tot.w};
-        float near = edge;  // log2 f_i: from the chunk's near end
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (BACK ? b > wq : b < wq) near += tots[b];
-        const float f = ptx::ex2(near);
+        float near = edge;  // log2 f_i: to the chunk's near end
         if (!wait_warp(BAR_G, (uint32_t)k)) break;
         ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int cb = 0; cb < 4; ++cb) {
           uint32_t out[16];
           if (BACK ? cb < wq : cb > wq) {
@@ -350,21 +375,18 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
             } else {
               // through the edges of the two blocks: a row factor times a column factor, both <= 1
               float between = edge;
-#pragma unroll
-              for (int b = 0; b < 4; ++b)
-                if (BACK ? (b > wq && b < cb) : (b > cb && b < wq)) between += tots[b];
+              for (int b = BACK ? wq + 1 : cb + 1; b < (BACK ? cb : wq); ++b) between += lds_f32(at + DEC_TOT + b * 4);
               const float alpha = ptx::ex2(between);
+              near += lds_f32(at + DEC_TOT + cb * 4);
+              const int last = BACK ? rows - cb * 32 : 32;  // columns behind the sequence are cut off
               ptx::tmem_wait_ld();
 #pragma unroll
               for (int j4 = 0; j4 < 8; ++j4) {
                 const float4 be = lds_f4(at + DEC_BETA + cb * 128 + j4 * 16);
-                float v[4] = {alpha * be.x * __uint_as_float(g[4 * j4]), alpha * be.y * __uint_as_float(g[4 * j4 + 1]),
-                              alpha * be.z * __uint_as_float(g[4 * j4 + 2]),
-                              alpha * be.w * __uint_as_float(g[4 * j4 + 3])};
-                if (BACK && rows < C)
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    if (cb * 32 + j4 * 4 + i >= rows) v[i] = 0.f;
+                const float v[4] = {j4 * 4 < last ? alpha * be.x * __uint_as_float(g[4 * j4]) : 0.f,
+                                    j4 * 4 + 1 < last ? alpha * be.y * __uint_as_float(g[4 * j4 + 1]) : 0.f,
+                                    j4 * 4 + 2 < last ? alpha * be.z * __uint_as_float(g[4 * j4 + 2]) : 0.f,
+                                    j4 * 4 + 3 < last ? alpha * be.w * __uint_as_float(g[4 * j4 + 3]) : 0.f};
                 out[2 * j4] = pack_bf16x2(v[0], v[1]);
                 out[2 * j4 + 1] = pack_bf16x2(v[2], v[3]);
               }
@@ -373,32 +395,42 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
           // columns 16 cb .. are G columns of block cb / 2, read already
           ptx::tmem_st16(lanes + TM_G + cb * 16, out);
         }
+        const float f = ptx::ex2(near);
+        if (!wait_warp(BAR_XS, (uint32_t)k)) break;
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int cb = 0; cb < 4; ++cb) {
+          uint32_t v[32];
+          ptx::tmem_ld32(lanes + TM_XS + cb * 32, v);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(f * __uint_as_float(v[j]));
+          ptx::tmem_st32(lanes + TM_PZ + cb * 32, v);
+        }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(bar(BAR_P));
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_P));
 
-        if (!wait_warp(BAR_XS, (uint32_t)k) || !wait_warp(BAR_U, (uint32_t)k) || !wait_warp(BAR_PZ, (uint32_t)k)) break;
+        if (!wait_warp(BAR_U, (uint32_t)k) || !wait_warp(BAR_PZ, (uint32_t)k)) break;
         ptx::tc_fence_after();
         float dot = 0.f;
         const bool whole = rows == C && !r.out_f32;
-        const uint32_t dst = sb + (uint32_t)s * kStage + OFF_Y;
-#pragma unroll
+        const uint32_t dst = sb + OFF_Y + (uint32_t)s * kTile;
+#pragma unroll 1
         for (int cb = 0; cb < 4; ++cb) {
           uint4 mw[4];
           if (m)
 #pragma unroll
             for (int j = 0; j < 4; ++j) mw[j] = *reinterpret_cast<const uint4 *>(m + cb * 32 + 8 * j);
-          uint32_t u[32], v[32];
-          ptx::tmem_ld32(lanes + TM_PZ + cb * 32, u);
-          ptx::tmem_ld32(lanes + TM_XS + cb * 32, v);
-          ptx::tmem_wait_ld();
-          if (cb == 3) {  // the accumulators are in registers
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(bar(BAR_OREAD));
-          }
           float o[32];
+          {
+            uint32_t u[32];
+            ptx::tmem_ld32(lanes + TM_PZ + cb * 32, u);
+            ptx::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = fmaf(f, __uint_as_float(v[j]), __uint_as_float(u[j]));
+            for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(u[j]);
+          }
           if (m)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -427,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
           }
         }
         ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(bar(BAR_STAGED));
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_STAGED));
         if (m) r.dots[tok * H + h] = dot;
       }
     }
@@ -466,7 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
 #pragma unroll
       for (int j = 0; j < 8; ++j) sts_v4(sb + OFF_S + half * kBlock + swz(zrow, (uint32_t)j), pack8(S + 8 * j, 1.f));
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(bar(BAR_S));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(BAR_S));
     };
     // marks of this thread's part of the state at the end of group `g` of chunks
     auto mark_unit = [&](int g) { return (size_t)mark_slot(unit / H, pc.t0 + g * kGroup * C) * H + h; };
@@ -496,48 +530,60 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
           prefetch_l2(next + 128);
         }
       }
-      const uint32_t st = sb + (uint32_t)s * kStage, par = (uint32_t)(k >> 1);
-      ok = wait_warp(BAR_DEC + s, par) && wait_warp(BAR_XY + s, par) && (rows == C || wait_warp(BAR_Z + s, par));
-      // Y is free to be overwritten after X Y^T, X and the bf16 state after X S
-      if (ok && !only) ok = wait_warp(BAR_G, (uint32_t)k) && wait_warp(BAR_XS, (uint32_t)k);
+      const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile, par = (uint32_t)(k >> 1);
+      ok = wait_warp(BAR_DEC + s, par) && wait_warp(BAR_Y + s, par) && (rows == C || wait_warp(BAR_Z + s, par));
+      if (ok && !only) ok = wait_warp(BAR_G, (uint32_t)k);  // Y may be overwritten
       if (!ok) break;
       const float4 tot = lds_f4(dec(s) + DEC_TOT);
-      const float tots[4] = {tot.x, tot.y, tot.z, tot.w};
       const float g = ptx::ex2((tot.x + tot.y) + (tot.z + tot.w));
+      float far = 0.f;  // from the edge of the tokens' block to the chunk's far end
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int b = BACK ? i : 3 - i, n = 4 * k + i, slot = n % SLOTS;
+        const float wb = ptx::ex2(far);
+        far += lds_f32(dec(s) + DEC_TOT + b * 4);
+        const int t = stid >> 4;  // rows t and t + 16 of the slice
+        const uint32_t c = (uint32_t)(stid & 15), in_row = swz(t, c & 7u);
+        const uint32_t to = y + (c >> 3) * kBlock + (uint32_t)b * (kSlice * 128) + in_row;
+        const uint32_t ring = sb + OFF_W + (uint32_t)slot * (NT - 1) * kSliceTile + (c >> 3) * kSliceBlock + in_row;
+        uint4 yv[2] = {lds_v4(to), lds_v4(to + 2048)};
+        const uint32_t be = dec(s) + DEC_BETA + (b * kSlice + t) * 4;
+        const float w[2] = {wb * lds_f32(be), wb * lds_f32(be + 64)};
+        if (n >= SLOTS) ok = wait_warp(BAR_EMPTY + slot, (uint32_t)(n / SLOTS) + 1u);
+        if (!ok) break;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int t = i * 16 + (stid >> 4);
-        const uint32_t c = (uint32_t)(stid & 15), off = (c >> 3) * kBlock + swz(t, c & 7u);
-        float far = 0.f;  // from the edge of the token's block to the chunk's far end
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (BACK ? b < (i >> 1) : b > (i >> 1)) far += tots[b];
-        const bool in = t < rows;
-        const float w = lds_f32(dec(s) + DEC_BETA + t * 4) * ptx::ex2(far);
-        const uint4 y = lds_v4(st + OFF_Y + off);
-        const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
-        uint32_t part[3][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float2 v = unpack_bf16x2(yw[j]);
-          v.x = in ? v.x * w : 0.f;
-          v.y = in ? v.y * w : 0.f;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            part[n][j] = pack_bf16x2(v.x, v.y);
-            const float2 b = unpack_bf16x2(part[n][j]);
-            v.x -= b.x;
-            v.y -= b.y;
+        for (int q = 0; q < 2; ++q) {
+          if (b * kSlice + t + 16 * q >= rows) {
+            // rows behind the sequence: their Z meets zero weights, which a NaN would outlive
+            yv[q] = make_uint4(0u, 0u, 0u, 0u);
+            sts_v4(to + (OFF_Z - OFF_Y) + q * 2048, yv[q]);
           }
+          const uint32_t yw[4] = {yv[q].x, yv[q].y, yv[q].z, yv[q].w};
+          uint32_t part[3][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float2 v = unpack_bf16x2(yw[j]);
+            v.x *= w[q];
+            v.y *= w[q];
+#pragma unroll
+            for (int p = 0; p < NT; ++p) {
+              part[p][j] = pack_bf16x2(v.x, v.y);
+              if (p + 1 < NT) {
+                v.x -= __uint_as_float(part[p][j] << 16);
+                v.y -= __uint_as_float(part[p][j] & 0xffff0000u);
+              }
+            }
+          }
+          sts_v4(to + q * 2048, make_uint4(part[0][0], part[0][1], part[0][2], part[0][3]));
+#pragma unroll
+          for (int p = 1; p < NT; ++p)
+            sts_v4(ring + (p - 1) * kSliceTile + q * 2048, make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]));
         }
-        sts_v4(st + OFF_Y + off, make_uint4(part[0][0], part[0][1], part[0][2], part[0][3]));
-        sts_v4(st + OFF_X + off, make_uint4(part[1][0], part[1][1], part[1][2], part[1][3]));
-        if constexpr (NT == 3) sts_v4(sb + OFF_S + off, make_uint4(part[2][0], part[2][1], part[2][2], part[2][3]));
-        // rows behind the sequence: their Z meets zero weights, which a NaN would outlive
-        if (!in) sts_v4(st + OFF_Z + off, make_uint4(0u, 0u, 0u, 0u));
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_FULL + slot));
       }
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(bar(BAR_W));
+      if (!ok) break;
       ok = wait_warp(BAR_U, (uint32_t)k);
       if (!ok) break;
       ptx::tc_fence_after();
@@ -550,7 +596,11 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         for (int j = 0; j < 32; ++j) S[c * 32 + j] = fmaf(g, S[c * 32 + j], __uint_as_float(u[j]));
       }
       ptx::tc_fence_before();
-      if (!only && k + 1 < nch) write_state();
+      if (!only && k + 1 < nch) {
+        ok = wait_warp(BAR_XS, (uint32_t)k);  // the last copy has been read
+        if (!ok) break;
+        write_state();
+      }
       if (!BACK && r.marks && !only && ends_group(k)) {
         float4 *mark = reinterpret_cast<float4 *>(r.marks + mark_unit(k / kGroup) * (D * D)) + stid;
 #pragma unroll
