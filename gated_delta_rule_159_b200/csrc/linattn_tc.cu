@@ -11,14 +11,14 @@
 // bits, 2 give 16, for runs whose state only feeds bf16 products), Z is bf16 already.
 //
 // Memory is what bounds it: 4 tiles of 32 KB a chunk, 128 KB against 2.9 us of 6.6 TB/s / 148 SMs;
-// the products take 6 x 512 tensor cycles.  One chain runs through the chunks: the state, its bf16
-// copy, X S; the update waits for nothing but the previous one.  Roles, side by side: warp 0 loads;
-// warp 1 issues the state's products (X S, the update), warp 3 the rows' (G, P Z); warp 2 sums the
-// decays and stores; warps 4-7 own a token row a thread (P, f o X S as the start of P Z's
-// accumulator, out); warps 8-15 own the state and weight Y.  What fits two stages of Y and Z into
-// shared memory: X has one, the first bf16 term of w o Y overwrites Y once X Y^T is done, the other
-// terms pass through a ring of 32-token slices, and out is staged in Y's place after the update.
-// Loops are kept rolled: unrolled, the roles together ran out of the instruction cache.
+// the products take 6 x 512 tensor cycles.  One chain runs through the chunks: the state and its
+// update; everything else runs beside it.  Roles: warp 0 loads; warp 1 issues the state's products
+// (X S, the update), warp 3 the rows' (G, P Z); warp 2 sums the decays; warps 4-7 own a token row a
+// thread (P, out); warps 8-15 own the state and weight Y.  What fits two stages of Y and Z into shared memory: X has one, the first bf16 term of w o Y
+// overwrites Y once X Y^T is done, the other terms pass through a ring of 32-token slices, and
+// out is staged in Y's place after the update.
+// Instruction issue comes next: the loops stay rolled (unrolled, the roles together ran out of the
+// instruction cache) and the fp32 arithmetic goes by pairs.
 #include <cstring>
 
 #include "linattn.cuh"
@@ -49,18 +49,20 @@ enum {
   BAR_Y = 0,        // + stage: Y loaded
   BAR_Z = 2,        // + stage: Z loaded
   BAR_DEC = 4,      // + stage: decays summed
-  BAR_FREE = 6,     // + stage: nothing uses Y and Z any more
-  BAR_FULL = 8,     // + slot: a slice of w o Y written
-  BAR_EMPTY = 12,   // + slot: its products done
-  BAR_X = 16,       // X loaded
+  BAR_FREE = 6,     // + stage: nothing uses Y, Z and the decays any more
+  BAR_G = 8,        // + stage: X Y^T done (two: the next may be done before the state warps look)
+  BAR_FULL = 10,    // + slot: a slice of w o Y written
+  BAR_EMPTY = 14,   // + slot: its products done
+  BAR_X = 18,       // X loaded
   BAR_XFREE,        // X Y^T and X S done
-  BAR_G,            // X Y^T done
   BAR_XS,           // X S done
-  BAR_P,            // P written, f o X S in place
+  BAR_P,            // P written
   BAR_PZ,           // P Z done
   BAR_U,            // increment done
   BAR_S,            // bf16 state written
+  BAR_OREAD,        // X S and P Z read
   BAR_STAGED,       // out tile staged
+  BAR_CLEAN,        // Y's and Z's rows behind the sequence cleared
   BAR_DRAIN,        // + 0, 1
   N_BARS = BAR_DRAIN + 2
 };
@@ -80,12 +82,14 @@ struct TcRun {
   int dbg_skip;
 };
 
-__device__ __forceinline__ uint64_t kmaj(uint32_t base, int kk) {
-  return ptx::sdesc_sw128(base + (uint32_t)(kk >> 2) * kBlock + (uint32_t)(kk & 3) * 32u, 16, 1024);
+// Tiles of two column blocks as operands: rows x K (kmaj), K x rows (mnmaj), and the steps from one
+// K = 16 product to the next, in the descriptors' 16-byte units.
+__device__ __forceinline__ uint64_t kmaj(uint32_t base) { return ptx::sdesc_sw128(base, 16, 1024); }
+__device__ __forceinline__ uint64_t mnmaj(uint32_t base, uint32_t block = kBlock) {
+  return ptx::sdesc_sw128(base, block, 1024);
 }
-__device__ __forceinline__ uint64_t mnmaj(uint32_t base, int kk, uint32_t block = kBlock) {
-  return ptx::sdesc_sw128(base + (uint32_t)kk * 2048u, block, 1024);
-}
+__device__ __forceinline__ uint64_t k_step(int kk) { return (uint64_t)((kk >> 2) * (kBlock >> 4) + (kk & 3) * 2); }
+constexpr uint64_t kMnStep = 2048 >> 4;
 __device__ __forceinline__ float lds_f32(uint32_t a) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
@@ -98,6 +102,34 @@ __device__ __forceinline__ float4 lds_f4(uint32_t a) {
 }
 
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 pair(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
+// The two fp32 values cut (not rounded) to bf16, in place and packed.
+__device__ __forceinline__ float2 cut2(float2 v) {
+  return pair(__float_as_uint(v.x) & 0xffff0000u, __float_as_uint(v.y) & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t pack_cut(float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); }
+// One copy of the waiting loop for all waits: some thirty inlined ones filled the instruction cache.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status,
+                                       uint64_t limit_ns) {
+  return wait_bar(bar, parity, abort_flag, status, limit_ns);
+}
 
 template <bool BACK, int NT>
 __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_constant__ TcRun P) {
@@ -119,9 +151,14 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
   auto bar = [&](int b) { return sb + OFF_MISC + MISC_BAR + 8u * (uint32_t)b; };
   auto dec = [&](int s) { return sb + OFF_MISC + (uint32_t)s * DEC_BYTES; };
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + MISC_ABORT);
-  auto wait = [&](int b, uint32_t parity) { return wait_bar(bar(b), parity & 1u, abort_flag, P.status, P.wait_ns); };
+  auto wait = [&](int b, uint32_t parity) {
+    return ptx::mbar_try_wait(bar(b), parity & 1u) || wait_long(bar(b), parity & 1u, abort_flag, P.status, P.wait_ns);
+  };
   // the same for whole warps, which stay together whether or not it gives up
-  auto wait_warp = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+  auto wait_warp = [&](int b, uint32_t parity) {
+    return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar(b), parity & 1u)) ||
+           __all_sync(0xffffffffu, wait_long(bar(b), parity & 1u, abort_flag, P.status, P.wait_ns));
+  };
   // tokens of the k-th chunk walked: its number and how many rows it has
   auto chunk_no = [&](int k) { return BACK ? nch - 1 - k : k; };
   auto rows_of = [&](int k) { return min(C, pc.len - chunk_no(k) * C); };
@@ -129,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
   if (tid == 0) {
     *abort_flag = 0;
     for (int b = 0; b < N_BARS; ++b) {
-      const bool rows = b == BAR_P || b == BAR_STAGED, state = b == BAR_S || (b >= BAR_FULL && b < BAR_EMPTY);
+      const bool rows = b == BAR_P || b == BAR_OREAD || b == BAR_STAGED;
+      const bool state = b == BAR_S || b == BAR_CLEAN || (b >= BAR_FULL && b < BAR_EMPTY);
       ptx::mbar_init(bar(b), rows ? 4 : state ? 8 : b == BAR_XFREE ? 2 : 1);
     }
     ptx::fence_mbar_init();
@@ -186,11 +224,11 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile, z = sb + OFF_Z + (uint32_t)s * kTile;
         if (!only) {
           // the state's copy, and the last X S read
-          if (!wait(BAR_X, (uint32_t)k) || !wait(BAR_S, (uint32_t)k) || (k && !wait(BAR_P, (uint32_t)k + 1u))) break;
+          if (!wait(BAR_X, (uint32_t)k) || !wait(BAR_S, (uint32_t)k) || (k && !wait(BAR_OREAD, (uint32_t)k + 1u))) break;
           ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int kk = 0; kk < 8; ++kk)
-            ptx::umma_bf16(tm + TM_XS, kmaj(sb + OFF_X, kk), kmaj(sb + OFF_S, kk), idKK, kk > 0);
+            ptx::umma_bf16(tm + TM_XS, kmaj(sb + OFF_X) + k_step(kk), kmaj(sb + OFF_S) + k_step(kk), idKK, kk > 0);
           ptx::umma_commit(bar(BAR_XS));
           ptx::umma_commit(bar(BAR_XFREE));
         }
@@ -201,15 +239,15 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
           ok = wait(BAR_FULL + slot, (uint32_t)(n / SLOTS));
           if (!ok) break;
           ptx::tc_fence_after();
+          const uint64_t zd = mnmaj(z + (uint32_t)b * (kSlice * 128)), yd = mnmaj(y + (uint32_t)b * (kSlice * 128));
+          const uint64_t wd = mnmaj(sb + OFF_W + (uint32_t)(slot * (NT - 1)) * kSliceTile, kSliceBlock);
 #pragma unroll
           for (int part = 0; part < NT; ++part)
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              const uint32_t w = sb + OFF_W + (uint32_t)(slot * (NT - 1) + part - 1) * kSliceTile;
-              ptx::umma_bf16(tm + TM_U, mnmaj(z, 2 * b + kk),
-                             part == 0 ? mnmaj(y, 2 * b + kk) : mnmaj(w, kk, kSliceBlock), idNN,
+            for (int kk = 0; kk < 2; ++kk)
+              ptx::umma_bf16(tm + TM_U, zd + kk * kMnStep,
+                             (part == 0 ? yd : wd + (uint64_t)(part - 1) * (kSliceTile >> 4)) + kk * kMnStep, idNN,
                              (i > 0) | (part + kk > 0));
-            }
           ptx::umma_commit(bar(BAR_EMPTY + slot));
         }
         if (!ok) break;
@@ -228,16 +266,19 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         const int s = k & 1;
         const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile, z = sb + OFF_Z + (uint32_t)s * kTile;
         if (!wait(BAR_X, (uint32_t)k) || !wait(BAR_Y + s, (uint32_t)(k >> 1))) break;
+        if (rows_of(k) < C && !wait(BAR_CLEAN, 0u)) break;
         ptx::tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) ptx::umma_bf16(tm + TM_G, kmaj(sb + OFF_X, kk), kmaj(y, kk), idKK, kk > 0);
-        ptx::umma_commit(bar(BAR_G));
+#pragma unroll 1
+        for (int kk = 0; kk < 8; ++kk)
+          ptx::umma_bf16(tm + TM_G, kmaj(sb + OFF_X) + k_step(kk), kmaj(y) + k_step(kk), idKK, kk > 0);
+        ptx::umma_commit(bar(BAR_G + s));
         ptx::umma_commit(bar(BAR_XFREE));
         if (!wait(BAR_Z + s, (uint32_t)(k >> 1)) || !wait(BAR_P, (uint32_t)k)) break;
-        if (rows_of(k) < C && !wait(BAR_U, (uint32_t)k)) break;  // Z's rows behind the sequence cleared
+        if (k && !wait(BAR_OREAD, (uint32_t)k + 1u)) break;
         ptx::tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) ptx::umma_bf16_ts(tm + TM_PZ, tm + TM_G + kk * 8, mnmaj(z, kk), idKN, 1u);
+#pragma unroll 1
+        for (int kk = 0; kk < 8; ++kk)
+          ptx::umma_bf16_ts(tm + TM_PZ, tm + TM_G + kk * 8, mnmaj(z) + kk * kMnStep, idKN, kk > 0);
         ptx::umma_commit(bar(BAR_PZ));
       }
       ptx::umma_commit(bar(BAR_DRAIN + 1));
@@ -278,7 +319,12 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
     float a[4];
     if (nch > 0) load(0, a);
     bool ok = true;
-    for (int k = 0; k < nch; ++k) {
+    // the last two rounds only store
+    for (int k = 0; k < (only ? nch : nch + 2) && ok; ++k) {
+      if (k >= nch) {
+        if (k >= 2) ok = store(k - 2);
+        continue;
+      }
       double own[4];  // inclusive sums inside the lane
 #pragma unroll
       for (int j = 0; j < 4; ++j) own[j] = (double)fmaxf(a[j], kMinLog) + (j ? own[j - 1] : 0.0);
@@ -316,23 +362,20 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
                 __shfl_sync(0xffffffffu, total, 16) + __shfl_sync(0xffffffffu, total, 24);
       }
     }
-    if (only) {
-      if (lane == 0) r.piece_log[unit] = logs;
-    } else {
-      for (int k = max(0, nch - 2); k < nch && ok; ++k) ok = store(k);
-      if (lane == 0) ptx::bulk_wait_group0();
-    }
+    if (only && lane == 0) r.piece_log[unit] = logs;
+    if (!only && lane == 0) ptx::bulk_wait_group0();
   } else if (warp < 8) {
     // ---------------------------------------------------------------- P and out: a token row a thread
     if (!only) {
       const int wq = warp & 3, row = wq * 32 + lane;
       const uint32_t lanes = tm + ((uint32_t)(wq * 32) << 16);
       for (int k = 0; k < nch; ++k) {
-        const int s = k & 1, rows = rows_of(k);
+        const int s = k & 1;
         const uint32_t at = dec(s);
+        const bool in = row < rows_of(k);
         const size_t tok = (size_t)pc.t0 + (size_t)chunk_no(k) * C + row;
         const __nv_bfloat16 *m = nullptr;
-        if (r.m && row < rows) {
+        if (r.m && in) {
           m = static_cast<const __nv_bfloat16 *>(r.m) + (tok * r.Hm + h / (H / r.Hm)) * D;
           prefetch_l2(m);
           prefetch_l2(m + 64);
@@ -340,7 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         if (!wait_warp(BAR_DEC + s, (uint32_t)(k >> 1))) break;
         const float edge = lds_f32(at + DEC_HI + row * 4), edge_lo = bf16_value(lds_u16(at + DEC_LO + row * 2));
         float near = edge;  // log2 f_i: to the chunk's near end
-        if (!wait_warp(BAR_G, (uint32_t)k)) break;
+        for (int b = BACK ? wq + 1 : 0; b < (BACK ? 4 : wq); ++b) near += lds_f32(at + DEC_TOT + b * 4);
+        const float f = ptx::ex2(near);
+        if (!wait_warp(BAR_G + s, (uint32_t)(k >> 1))) break;
         ptx::tc_fence_after();
 #pragma unroll 1
         for (int cb = 0; cb < 4; ++cb) {
@@ -353,115 +398,102 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
             ptx::tmem_ld32(lanes + TM_G + cb * 32, g);
             if (cb == wq) {
               // both tokens in one block: the decay between them, pair by pair
+              const float2 minus = make_float2(-1.f, -1.f), e2 = make_float2(edge, edge);
               ptx::tmem_wait_ld();
 #pragma unroll
               for (int j4 = 0; j4 < 8; ++j4) {
                 const float4 e = lds_f4(at + DEC_HI + cb * 128 + j4 * 16);
                 const uint2 l = lds_v2(at + DEC_LO + cb * 64 + j4 * 8);
-                const float eh[4] = {e.x, e.y, e.z, e.w};
-                const float el[4] = {bf16_value((uint16_t)l.x), bf16_value((uint16_t)(l.x >> 16)),
-                                     bf16_value((uint16_t)l.y), bf16_value((uint16_t)(l.y >> 16))};
-                float v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int j = j4 * 4 + i;
-                  const float w = ptx::ex2((edge - eh[i]) + (edge_lo - el[i]));
-                  const bool in = (BACK ? j >= lane : j <= lane) && cb * 32 + j < rows;
-                  v[i] = in ? w * __uint_as_float(g[j]) : 0.f;
+                for (int i = 0; i < 2; ++i) {
+                  const int j = j4 * 4 + 2 * i;
+                  const uint32_t lw = i ? l.y : l.x;
+                  const float2 eh = i ? make_float2(e.z, e.w) : make_float2(e.x, e.y);
+                  const float2 d = fma2(eh, minus, e2);
+                  const float2 w = make_float2(ptx::ex2(d.x + (edge_lo - __uint_as_float(lw << 16))),
+                                               ptx::ex2(d.y + (edge_lo - __uint_as_float(lw & 0xffff0000u))));
+                  const float2 v = mul2(w, pair(g[j], g[j + 1]));
+                  out[2 * j4 + i] = pack_bf16x2((BACK ? j >= lane : j <= lane) ? v.x : 0.f,
+                                                (BACK ? j + 1 >= lane : j + 1 <= lane) ? v.y : 0.f);
                 }
-                out[2 * j4] = pack_bf16x2(v[0], v[1]);
-                out[2 * j4 + 1] = pack_bf16x2(v[2], v[3]);
               }
             } else {
               // through the edges of the two blocks: a row factor times a column factor, both <= 1
               float between = edge;
               for (int b = BACK ? wq + 1 : cb + 1; b < (BACK ? cb : wq); ++b) between += lds_f32(at + DEC_TOT + b * 4);
               const float alpha = ptx::ex2(between);
-              near += lds_f32(at + DEC_TOT + cb * 4);
-              const int last = BACK ? rows - cb * 32 : 32;  // columns behind the sequence are cut off
+              const float2 a2 = make_float2(alpha, alpha);
               ptx::tmem_wait_ld();
 #pragma unroll
               for (int j4 = 0; j4 < 8; ++j4) {
                 const float4 be = lds_f4(at + DEC_BETA + cb * 128 + j4 * 16);
-                const float v[4] = {j4 * 4 < last ? alpha * be.x * __uint_as_float(g[4 * j4]) : 0.f,
-                                    j4 * 4 + 1 < last ? alpha * be.y * __uint_as_float(g[4 * j4 + 1]) : 0.f,
-                                    j4 * 4 + 2 < last ? alpha * be.z * __uint_as_float(g[4 * j4 + 2]) : 0.f,
-                                    j4 * 4 + 3 < last ? alpha * be.w * __uint_as_float(g[4 * j4 + 3]) : 0.f};
-                out[2 * j4] = pack_bf16x2(v[0], v[1]);
-                out[2 * j4 + 1] = pack_bf16x2(v[2], v[3]);
+                const float2 v = mul2(mul2(a2, make_float2(be.x, be.y)), pair(g[4 * j4], g[4 * j4 + 1]));
+                const float2 u = mul2(mul2(a2, make_float2(be.z, be.w)), pair(g[4 * j4 + 2], g[4 * j4 + 3]));
+                out[2 * j4] = pack_bf16x2(v.x, v.y);
+                out[2 * j4 + 1] = pack_bf16x2(u.x, u.y);
               }
             }
           }
           // columns 16 cb .. are G columns of block cb / 2, read already
           ptx::tmem_st16(lanes + TM_G + cb * 16, out);
         }
-        const float f = ptx::ex2(near);
-        if (!wait_warp(BAR_XS, (uint32_t)k)) break;
-        ptx::tc_fence_after();
-#pragma unroll 1
-        for (int cb = 0; cb < 4; ++cb) {
-          uint32_t v[32];
-          ptx::tmem_ld32(lanes + TM_XS + cb * 32, v);
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(f * __uint_as_float(v[j]));
-          ptx::tmem_st32(lanes + TM_PZ + cb * 32, v);
-        }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(BAR_P));
-
-        if (!wait_warp(BAR_U, (uint32_t)k) || !wait_warp(BAR_PZ, (uint32_t)k)) break;
-        ptx::tc_fence_after();
-        float dot = 0.f;
-        const bool whole = rows == C && !r.out_f32;
+        const float2 f2 = make_float2(f, f);
+        float2 dot = make_float2(0.f, 0.f);
+        const bool whole = rows_of(k) == C && !r.out_f32;
         const uint32_t dst = sb + OFF_Y + (uint32_t)s * kTile;
+        if (!wait_warp(BAR_XS, (uint32_t)k) || !wait_warp(BAR_PZ, (uint32_t)k) || !wait_warp(BAR_U, (uint32_t)k)) break;
+        ptx::tc_fence_after();
 #pragma unroll 1
-        for (int cb = 0; cb < 4; ++cb) {
-          uint4 mw[4];
+        for (int cb = 0; cb < 8; ++cb) {
+          uint4 mw[2];
           if (m)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mw[j] = *reinterpret_cast<const uint4 *>(m + cb * 32 + 8 * j);
-          float o[32];
-          {
-            uint32_t u[32];
-            ptx::tmem_ld32(lanes + TM_PZ + cb * 32, u);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(u[j]);
+            for (int j = 0; j < 2; ++j) mw[j] = *reinterpret_cast<const uint4 *>(m + cb * 16 + 8 * j);
+          uint32_t u[16], v[16];
+          ptx::tmem_ld16(lanes + TM_PZ + cb * 16, u);
+          ptx::tmem_ld16(lanes + TM_XS + cb * 16, v);
+          ptx::tmem_wait_ld();
+          if (cb == 7) {  // the accumulators are in registers
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BAR_OREAD));
           }
+          float2 o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = fma2(f2, pair(v[2 * j], v[2 * j + 1]), pair(u[2 * j], u[2 * j + 1]));
           if (m)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
               const uint32_t w[4] = {mw[j].x, mw[j].y, mw[j].z, mw[j].w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 b = unpack_bf16x2(w[i]);
-                dot = fmaf(b.x, o[8 * j + 2 * i], fmaf(b.y, o[8 * j + 2 * i + 1], dot));
-              }
+              for (int i = 0; i < 4; ++i) dot = fma2(pair(w[i] << 16, w[i] & 0xffff0000u), o[4 * j + i], dot);
             }
-          if (r.out_f32) {
-            if (row < rows) {
-              float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(r.out) + (tok * H + h) * D + cb * 32);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) p[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint4 w = pack8(o + 8 * j, 1.f);
-              if (whole)
-                sts_v4(dst + (uint32_t)(cb >> 1) * kBlock + swz(row, (uint32_t)((cb & 1) * 4 + j)), w);
-              else if (row < rows)
-                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(r.out) + (tok * H + h) * D + cb * 32 + 8 * j) = w;
+          for (int j = 0; j < 2; ++j) {
+            const uint4 w = make_uint4(pack_bf16x2(o[4 * j].x, o[4 * j].y), pack_bf16x2(o[4 * j + 1].x, o[4 * j + 1].y),
+                                       pack_bf16x2(o[4 * j + 2].x, o[4 * j + 2].y),
+                                       pack_bf16x2(o[4 * j + 3].x, o[4 * j + 3].y));
+            const size_t at_out = (tok * H + h) * D + cb * 16 + 8 * j;
+            if (whole) {
+              sts_v4(dst + (uint32_t)(cb >> 2) * kBlock + swz(row, (uint32_t)((cb & 3) * 2 + j)), w);
+            } else if (in && r.out_f32) {
+              float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(r.out) + at_out);
+              p[0] = make_float4(o[4 * j].x, o[4 * j].y, o[4 * j + 1].x, o[4 * j + 1].y);
+              p[1] = make_float4(o[4 * j + 2].x, o[4 * j + 2].y, o[4 * j + 3].x, o[4 * j + 3].y);
+            } else if (in) {
+              *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(r.out) + at_out) = w;
             }
           }
+          __syncwarp();
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(BAR_STAGED));
-        if (m) r.dots[tok * H + h] = dot;
+        if (m) r.dots[tok * H + h] = dot.x + dot.y;
       }
     }
   } else {
@@ -532,7 +564,19 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
       }
       const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile, par = (uint32_t)(k >> 1);
       ok = wait_warp(BAR_DEC + s, par) && wait_warp(BAR_Y + s, par) && (rows == C || wait_warp(BAR_Z + s, par));
-      if (ok && !only) ok = wait_warp(BAR_G, (uint32_t)k);  // Y may be overwritten
+      if (ok && rows < C) {
+        // rows behind the sequence meet zero weights, which a NaN would outlive
+        for (int t = stid >> 4; t < C; t += 16)
+          if (t >= rows) {
+            const uint32_t to = y + (uint32_t)(stid >> 3 & 1) * kBlock + swz(t, (uint32_t)(stid & 7));
+            sts_v4(to, make_uint4(0u, 0u, 0u, 0u));
+            sts_v4(to + (OFF_Z - OFF_Y), make_uint4(0u, 0u, 0u, 0u));
+          }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_CLEAN));
+      }
+      if (ok && !only) ok = wait_warp(BAR_G + s, (uint32_t)(k >> 1));  // Y may be overwritten
       if (!ok) break;
       const float4 tot = lds_f4(dec(s) + DEC_TOT);
       const float g = ptx::ex2((tot.x + tot.y) + (tot.z + tot.w));
@@ -546,32 +590,24 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         const uint32_t c = (uint32_t)(stid & 15), in_row = swz(t, c & 7u);
         const uint32_t to = y + (c >> 3) * kBlock + (uint32_t)b * (kSlice * 128) + in_row;
         const uint32_t ring = sb + OFF_W + (uint32_t)slot * (NT - 1) * kSliceTile + (c >> 3) * kSliceBlock + in_row;
-        uint4 yv[2] = {lds_v4(to), lds_v4(to + 2048)};
+        const uint4 yv[2] = {lds_v4(to), lds_v4(to + 2048)};
         const uint32_t be = dec(s) + DEC_BETA + (b * kSlice + t) * 4;
         const float w[2] = {wb * lds_f32(be), wb * lds_f32(be + 64)};
         if (n >= SLOTS) ok = wait_warp(BAR_EMPTY + slot, (uint32_t)(n / SLOTS) + 1u);
         if (!ok) break;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          if (b * kSlice + t + 16 * q >= rows) {
-            // rows behind the sequence: their Z meets zero weights, which a NaN would outlive
-            yv[q] = make_uint4(0u, 0u, 0u, 0u);
-            sts_v4(to + (OFF_Z - OFF_Y) + q * 2048, yv[q]);
-          }
           const uint32_t yw[4] = {yv[q].x, yv[q].y, yv[q].z, yv[q].w};
+          const float2 w2 = make_float2(w[q], w[q]), minus = make_float2(-1.f, -1.f);
           uint32_t part[3][4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float2 v = unpack_bf16x2(yw[j]);
-            v.x *= w[q];
-            v.y *= w[q];
+            // the first terms are cut, the last rounded: 8 bits each, the signs all the same
+            float2 v = mul2(pair(yw[j] << 16, yw[j] & 0xffff0000u), w2);
 #pragma unroll
             for (int p = 0; p < NT; ++p) {
-              part[p][j] = pack_bf16x2(v.x, v.y);
-              if (p + 1 < NT) {
-                v.x -= __uint_as_float(part[p][j] << 16);
-                v.y -= __uint_as_float(part[p][j] & 0xffff0000u);
-              }
+              part[p][j] = p + 1 < NT ? pack_cut(v) : pack_bf16x2(v.x, v.y);
+              if (p + 1 < NT) v = fma2(cut2(v), minus, v);
             }
           }
           sts_v4(to + q * 2048, make_uint4(part[0][0], part[0][1], part[0][2], part[0][3]));
@@ -593,7 +629,12 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         ptx::tmem_ld32(lanes + c * 32, u);
         ptx::tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[c * 32 + j] = fmaf(g, S[c * 32 + j], __uint_as_float(u[j]));
+        for (int j = 0; j < 16; ++j) {
+          float *p = S + c * 32 + 2 * j;
+          const float2 v = fma2(make_float2(g, g), make_float2(p[0], p[1]), pair(u[2 * j], u[2 * j + 1]));
+          p[0] = v.x;
+          p[1] = v.y;
+        }
       }
       ptx::tc_fence_before();
       if (!only && k + 1 < nch) {
