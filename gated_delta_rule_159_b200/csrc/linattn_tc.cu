@@ -51,9 +51,10 @@ enum {
   BAR_DEC = 4,      // + stage: decays summed
   BAR_FREE = 6,     // + stage: nothing uses Y, Z and the decays any more
   BAR_G = 8,        // + stage: X Y^T done (two: the next may be done before the state warps look)
-  BAR_FULL = 10,    // + slot: a slice of w o Y written
-  BAR_EMPTY = 14,   // + slot: its products done
-  BAR_X = 18,       // X loaded
+  BAR_STAGED = 10,  // + stage: out tile staged (two: the next may be staged before the storing warp looks)
+  BAR_FULL = 12,    // + slot: a slice of w o Y written
+  BAR_EMPTY = 16,   // + slot: its products done
+  BAR_X = 20,       // X loaded
   BAR_XFREE,        // X Y^T and X S done
   BAR_XS,           // X S done
   BAR_P,            // P written
@@ -61,7 +62,6 @@ enum {
   BAR_U,            // increment done
   BAR_S,            // bf16 state written
   BAR_OREAD,        // X S and P Z read
-  BAR_STAGED,       // out tile staged
   BAR_CLEAN,        // Y's and Z's rows behind the sequence cleared
   BAR_DRAIN,        // + 0, 1
   N_BARS = BAR_DRAIN + 2
@@ -72,6 +72,7 @@ constexpr uint32_t kSmemBytes = OFF_MISC + MISC_BYTES;
 static_assert(kSmemBytes <= 232448, "shared memory over the sm_100 limit per CTA");
 constexpr uint32_t TM_G = 0, TM_PZ = 128, TM_XS = 256, TM_U = 384;  // TMEM columns; P overwrites G
 constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint32_t kSleepNs = 20000;  // between two looks at the clock: busy waits take issue slots from the workers
 constexpr float kLog2 = 1.4426950408889634f;
 
 struct TcRun {
@@ -128,7 +129,17 @@ __device__ __forceinline__ uint32_t pack_cut(float2 v) { return __byte_perm(__fl
 // One copy of the waiting loop for all waits: some thirty inlined ones filled the instruction cache.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status,
                                        uint64_t limit_ns) {
-  return wait_bar(bar, parity, abort_flag, status, limit_ns);
+  if (*abort_flag) return false;
+  const uint64_t t0 = global_timer_ns();
+  while (!ptx::mbar_try_wait_for(bar, parity, kSleepNs)) {
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      *abort_flag = 1;
+      atomicExch(status, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
 }
 
 template <bool BACK, int NT>
@@ -137,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
   extern __shared__ __align__(1024) uint8_t smem[];
   const Run &r = P.r;
   const uint32_t sb = ptx::smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int H = r.cut.H, unit = blockIdx.x, h = unit % H;
   Piece pc;
   if (!find_piece(r.cut, unit / H, &pc)) return;
@@ -166,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
   if (tid == 0) {
     *abort_flag = 0;
     for (int b = 0; b < N_BARS; ++b) {
-      const bool rows = b == BAR_P || b == BAR_OREAD || b == BAR_STAGED;
+      const bool rows = b == BAR_P || b == BAR_OREAD || b == BAR_STAGED || b == BAR_STAGED + 1;
       const bool state = b == BAR_S || b == BAR_CLEAN || (b >= BAR_FULL && b < BAR_EMPTY);
       ptx::mbar_init(bar(b), rows ? 4 : state ? 8 : b == BAR_XFREE ? 2 : 1);
     }
@@ -179,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tm = *reinterpret_cast<volatile uint32_t *>(smem + OFF_MISC + MISC_TMEM);
+  const uint32_t tm = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(smem + OFF_MISC + MISC_TMEM), 0);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
@@ -215,7 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- the state's products
-    if (lane == 0) {
+    {
+      const bool lead = ptx::elect_one();
       constexpr uint32_t idKK = ptx::idesc_bf16(128, 128, false, false);
       constexpr uint32_t idNN = ptx::idesc_bf16(128, 128, true, true);
       bool ok = true;
@@ -224,19 +236,19 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile, z = sb + OFF_Z + (uint32_t)s * kTile;
         if (!only) {
           // the state's copy, and the last X S read
-          if (!wait(BAR_X, (uint32_t)k) || !wait(BAR_S, (uint32_t)k) || (k && !wait(BAR_OREAD, (uint32_t)k + 1u))) break;
+          if (!wait_warp(BAR_X, (uint32_t)k) || !wait_warp(BAR_S, (uint32_t)k) || (k && !wait_warp(BAR_OREAD, (uint32_t)k + 1u))) break;
           ptx::tc_fence_after();
 #pragma unroll 1
           for (int kk = 0; kk < 8; ++kk)
-            ptx::umma_bf16(tm + TM_XS, kmaj(sb + OFF_X) + k_step(kk), kmaj(sb + OFF_S) + k_step(kk), idKK, kk > 0);
-          ptx::umma_commit(bar(BAR_XS));
-          ptx::umma_commit(bar(BAR_XFREE));
+            ptx::umma_bf16_if(lead, tm + TM_XS, kmaj(sb + OFF_X) + k_step(kk), kmaj(sb + OFF_S) + k_step(kk), idKK, kk > 0);
+          ptx::umma_commit_if(lead, bar(BAR_XS));
+          ptx::umma_commit_if(lead, bar(BAR_XFREE));
         }
-        if (!wait(BAR_Z + s, (uint32_t)(k >> 1))) break;
+        if (!wait_warp(BAR_Z + s, (uint32_t)(k >> 1))) break;
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
           const int n = 4 * k + i, slot = n % SLOTS, b = BACK ? i : 3 - i;
-          ok = wait(BAR_FULL + slot, (uint32_t)(n / SLOTS));
+          ok = wait_warp(BAR_FULL + slot, (uint32_t)(n / SLOTS));
           if (!ok) break;
           ptx::tc_fence_after();
           const uint64_t zd = mnmaj(z + (uint32_t)b * (kSlice * 128)), yd = mnmaj(y + (uint32_t)b * (kSlice * 128));
@@ -245,43 +257,44 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
           for (int part = 0; part < NT; ++part)
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
-              ptx::umma_bf16(tm + TM_U, zd + kk * kMnStep,
+              ptx::umma_bf16_if(lead, tm + TM_U, zd + kk * kMnStep,
                              (part == 0 ? yd : wd + (uint64_t)(part - 1) * (kSliceTile >> 4)) + kk * kMnStep, idNN,
                              (i > 0) | (part + kk > 0));
-          ptx::umma_commit(bar(BAR_EMPTY + slot));
+          ptx::umma_commit_if(lead, bar(BAR_EMPTY + slot));
         }
         if (!ok) break;
-        ptx::umma_commit(bar(BAR_U));
-        if (only) ptx::umma_commit(bar(BAR_FREE + s));
+        ptx::umma_commit_if(lead, bar(BAR_U));
+        if (only) ptx::umma_commit_if(lead, bar(BAR_FREE + s));
       }
-      ptx::umma_commit(bar(BAR_DRAIN));  // all products, before the tensor memory is freed
+      ptx::umma_commit_if(lead, bar(BAR_DRAIN));  // all products, before the tensor memory is freed
       drain_bar(bar(BAR_DRAIN), 0u, P.wait_ns);
     }
   } else if (warp == 3) {
     // ---------------------------------------------------------------- the rows' products
-    if (lane == 0 && !only) {
+    if (!only) {
+      const bool lead = ptx::elect_one();
       constexpr uint32_t idKK = ptx::idesc_bf16(128, 128, false, false);
       constexpr uint32_t idKN = ptx::idesc_bf16(128, 128, false, true);
       for (int k = 0; k < nch; ++k) {
         const int s = k & 1;
         const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile, z = sb + OFF_Z + (uint32_t)s * kTile;
-        if (!wait(BAR_X, (uint32_t)k) || !wait(BAR_Y + s, (uint32_t)(k >> 1))) break;
-        if (rows_of(k) < C && !wait(BAR_CLEAN, 0u)) break;
+        if (!wait_warp(BAR_X, (uint32_t)k) || !wait_warp(BAR_Y + s, (uint32_t)(k >> 1))) break;
+        if (rows_of(k) < C && !wait_warp(BAR_CLEAN, 0u)) break;
         ptx::tc_fence_after();
 #pragma unroll 1
         for (int kk = 0; kk < 8; ++kk)
-          ptx::umma_bf16(tm + TM_G, kmaj(sb + OFF_X) + k_step(kk), kmaj(y) + k_step(kk), idKK, kk > 0);
-        ptx::umma_commit(bar(BAR_G + s));
-        ptx::umma_commit(bar(BAR_XFREE));
-        if (!wait(BAR_Z + s, (uint32_t)(k >> 1)) || !wait(BAR_P, (uint32_t)k)) break;
-        if (k && !wait(BAR_OREAD, (uint32_t)k + 1u)) break;
+          ptx::umma_bf16_if(lead, tm + TM_G, kmaj(sb + OFF_X) + k_step(kk), kmaj(y) + k_step(kk), idKK, kk > 0);
+        ptx::umma_commit_if(lead, bar(BAR_G + s));
+        ptx::umma_commit_if(lead, bar(BAR_XFREE));
+        if (!wait_warp(BAR_Z + s, (uint32_t)(k >> 1)) || !wait_warp(BAR_P, (uint32_t)k)) break;
+        if (k && !wait_warp(BAR_OREAD, (uint32_t)k + 1u)) break;
         ptx::tc_fence_after();
 #pragma unroll 1
         for (int kk = 0; kk < 8; ++kk)
-          ptx::umma_bf16_ts(tm + TM_PZ, tm + TM_G + kk * 8, mnmaj(z) + kk * kMnStep, idKN, kk > 0);
-        ptx::umma_commit(bar(BAR_PZ));
+          ptx::umma_bf16_ts_if(lead, tm + TM_PZ, tm + TM_G + kk * 8, mnmaj(z) + kk * kMnStep, idKN, kk > 0);
+        ptx::umma_commit_if(lead, bar(BAR_PZ));
       }
-      ptx::umma_commit(bar(BAR_DRAIN + 1));
+      ptx::umma_commit_if(lead, bar(BAR_DRAIN + 1));
       drain_bar(bar(BAR_DRAIN + 1), 0u, P.wait_ns);
     }
   } else if (warp == 2) {
@@ -302,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
     // chunk k's out tile; the stage is free once it has been read
     auto store = [&](int k) {
       if (only) return wait_warp(BAR_FREE + (k & 1), (uint32_t)(k >> 1));
-      if (!wait_warp(BAR_STAGED, (uint32_t)k)) return false;
+      if (!wait_warp(BAR_STAGED + (k & 1), (uint32_t)(k >> 1))) return false;
       if (lane == 0) {
         if (!r.out_f32 && rows_of(k) == C) {
           const uint32_t src = sb + OFF_Y + (uint32_t)(k & 1) * kTile;
@@ -492,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(BAR_STAGED));
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_STAGED + s));
         if (m) r.dots[tok * H + h] = dot.x + dot.y;
       }
     }
