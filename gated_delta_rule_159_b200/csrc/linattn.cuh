@@ -85,11 +85,13 @@ __device__ __forceinline__ bool find_piece(const Cut &c, int g, Piece *p) {
 // start.  Slot of the group that starts at token t of piece g: pieces are in token order, so no two
 // share one.
 constexpr int kGroup = 4;
+constexpr int kMarkDots = 8;  // partial products a mark, one of each state warp
 __host__ __device__ inline int mark_slot(int g, int t) { return g + t / (kGroup * kChunk); }
 inline size_t mark_slots(const Cut &c) { return (size_t)c.n_pieces + (size_t)(c.t_total / (kGroup * kChunk)) + 1; }
 
-// log_a below this is a reset: e^-256 is 0 in fp32, and sums over a chunk stay finite.
-constexpr float kMinLog = -256.f;
+// log_a below this is a reset: e^-104 is 0 in fp32, and sums over a chunk stay finite and fine enough
+// (32 resets come to 4800 in log2, a float's step there is 2^-11).
+constexpr float kMinLog = -104.f;
 
 // One run over all (piece, head) units:
 //   forward:   out_t = sum_{j <= t} e^{L_t - L_j} (x_t . y_j) z_j + e^{L_t} start^T x_t
@@ -115,13 +117,13 @@ struct Run {
   double *piece_log;     // [n_pieces * H]
   int state_only;        // write piece_state and piece_log, no out
   // For the gradient of log_a: partial dots of every out row with the row of m (Hm heads, dz
-  // columns) over the columns of one slice, [slices][T, H]; NULL: none.
+  // columns) over the columns of one slice (the tensor-core runs have two), [slices][T, H]; NULL: none.
   const void *m;
   int Hm;
   float *dots;
   // Tensor-core runs: marks of the state behind every group of kGroup chunks, [slots][H][dy * dz]
   // in the state warps' own order; the forward form writes them, the backward form multiplies its
-  // state at the same place with them into mark_dots [slots][H][8].  NULL: none.
+  // state at the same place with them into mark_dots [slots][H][kMarkDots].  NULL: none.
   float *marks, *mark_dots;
   Cut cut;
   int dtype;
@@ -132,7 +134,7 @@ cudaError_t launch_join(const Run &r, cudaStream_t stream);
 int simt_slices(int dz);
 cudaError_t launch_run_simt(const Run &r, cudaStream_t stream);
 // The run on the tensor cores (linattn_tc.cu): bf16, dy = dz = 128.  `terms`: bf16 values that
-// stand for a weighted row of y in the state's update, 3 (24 bits) or 2.
+// stand for a weighted row of y in the state's update, 4 (26 bits) or 2 (17).
 cudaError_t launch_run_tc(const Run &r, int terms, int32_t *status, cudaStream_t stream);
 // dlog_a of the fp32 runs: dots_q (of dq with q), dots_k (of dk with k), and <S_T, dS_T> (S_T
 // may be NULL with dS_T).

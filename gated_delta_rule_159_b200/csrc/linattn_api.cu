@@ -136,7 +136,7 @@ int check_log_a(const gdn2_linattn_dims *d, int64_t tokens, const void *log_a) {
 int cuda_fail(const char *what, cudaError_t e) { return fail(GDN2_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e)); }
 
 // A run, with its cut sequences' piece states and join first.  The runs whose state can be a result
-// (the forward's, dv's) take it to the tensor cores in three bf16 terms, whether or not this call
+// (the forward's, dv's) take it to the tensor cores in four bf16 terms, whether or not this call
 // asks for it: out must not depend on that.  The others only feed it to bf16 products: two terms.
 cudaError_t full_run(Run r, int terms, int32_t *status, bool tc, cudaStream_t s) {
   cudaError_t e;
@@ -194,9 +194,9 @@ BwdLayout bwd_layout(const gdn2_linattn_dims *d, const Cut &c, bool ckpt8) {
   L.off_fin = L.cut.end;
   L.off_marks = L.off_fin + (dlog && !tc ? up256((size_t)d->n_seqs * H * state * sizeof(float)) : 0);
   L.off_mark_dots = L.off_marks + slots * state * sizeof(float);
-  L.off_part = L.off_mark_dots + up256(slots * 8 * sizeof(float));
+  L.off_part = L.off_mark_dots + up256(slots * gdn2::lin::kMarkDots * sizeof(float));
   L.off_dq = L.off_part + (d->n_qk_heads < d->n_heads ? up256(T * H * d->d_k * sizeof(float)) : 0);
-  const size_t dots = dlog ? up256(T * H * (tc ? 1 : gdn2::lin::simt_slices(d->d_k)) * sizeof(float)) : 0;
+  const size_t dots = dlog ? up256(T * H * (tc ? 2 : gdn2::lin::simt_slices(d->d_k)) * sizeof(float)) : 0;
   L.off_dk = L.off_dq + dots;
   L.total = L.off_dk + dots;
   const size_t es = d->dtype_in == GDN2_BF16 ? 2 : 4;
@@ -239,7 +239,7 @@ int bwd_runs(const void *q, const void *k, const void *v, const void *log_a, con
   r.dy = d->d_k; r.dz = d->d_v;
   r.start = dS_T; r.fin = dS0;
   r.out = dv;
-  if ((e = full_run(r, 3, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dv run", e);
+  if ((e = full_run(r, 4, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dv run", e);
 
   r = base;  // dk_j = sum_{i >= j} (v_j . dO_i) q_i
   r.back = 1;
@@ -325,7 +325,7 @@ int gdn2_linattn_fwd(const void *q, const void *k, const void *v, const void *lo
   r.x = q; r.Hx = dims->n_qk_heads; r.y = k; r.Hy = dims->n_qk_heads; r.z = v; r.Hz = dims->n_heads;
   r.dy = dims->d_k; r.dz = dims->d_v;
   r.start = S0; r.fin = S_T; r.out = o;
-  if ((e = full_run(r, 3, reinterpret_cast<int32_t *>(ws), tensor_core(dims), s)) != cudaSuccess) return cuda_fail("linattn run", e);
+  if ((e = full_run(r, 4, reinterpret_cast<int32_t *>(ws), tensor_core(dims), s)) != cudaSuccess) return cuda_fail("linattn run", e);
   return GDN2_OK;
 }
 

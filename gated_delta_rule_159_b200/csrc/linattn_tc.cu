@@ -5,20 +5,25 @@
 // Per chunk, with D the matrix of decays inside the chunk (0 outside the triangle), w_j the decay
 // from token j to the chunk's far end, f_i the decay from its near end to token i, g the chunk's:
 //   G = X Y^T,  P = bf16(G o D)           (rows = tokens; P becomes a TMEM operand)
-//   out = P Z + f o (X S)                 (two accumulators, joined in fp32 by the epilogue)
-//   S <- g S + (w o Y)^T Z                (S in fp32 registers; the increment in TMEM)
-// The state is exact to fp32: w o Y goes to the tensor cores as a sum of NT bf16 values (3 give 24
-// bits, 2 give 16, for runs whose state only feeds bf16 products), Z is bf16 already.
+//   out = P Z + f o (X S)
+//   S <- g S + (w o Y)^T Z                (S is the fp32 accumulator itself)
+// Where the chunk's decay stays above 2^-32, D_ij = f_i / f_j is not needed: out = f o (X S + P' Z)
+// with P' = bf16(G_ij / f_j), one accumulator and one product a weight.  And S is kept as 2^rho S
+// for as long as rho <= 32, so that the update of one chunk follows the last one's without a pass
+// over the accumulator; only past that is it scaled back.  Chunks of stronger decay (resets) take
+// D block by block and scale S every time.
+// The state is exact to fp32: w o Y goes to the tensor cores as a sum of NT bf16 values (4 give 26
+// bits, 2 give 17, for runs whose state only feeds bf16 products), Z is bf16 already.
 //
 // Memory is what bounds it: 4 tiles of 32 KB a chunk, 128 KB against 2.9 us of 6.6 TB/s / 148 SMs;
-// the products take 6 x 512 tensor cycles.  One chain runs through the chunks: the state and its
-// update; everything else runs beside it.  Roles: warp 0 loads; warp 1 issues the state's products
-// (X S, the update), warp 3 the rows' (G, P Z); warp 2 sums the decays; warps 4-7 own a token row a
-// thread (P, out); warps 8-15 own the state and weight Y.  What fits two stages of Y and Z into shared memory: X has one, the first bf16 term of w o Y
-// overwrites Y once X Y^T is done, the other terms pass through a ring of 32-token slices, and
-// out is staged in Y's place after the update.
-// Instruction issue comes next: the loops stay rolled (unrolled, the roles together ran out of the
-// instruction cache) and the fp32 arithmetic goes by pairs.
+// the products take 5 x 512 (NT = 2) or 7 x 512 tensor cycles.  What costs time is the chains of
+// short steps on the CUDA cores, so they run side by side, each a group of warps of its own: warp 0
+// loads; warp 1 issues the state's products, warp 3 the rows' (G, X S, P Z); warp 2 sums the decays
+// and stores; warps 4-11 own half a token row a thread (P, out); warps 12-19 copy the state to bf16
+// for X S (and scale it); warps 20-27 weight Y, transposed into tensor memory: with w o Y in shared
+// memory (every term written, and read with Z) that memory's 128 bytes a cycle were short.  X has
+// one tile, Y and Z two stages.  The loops stay rolled: unrolled, the roles together ran out of
+// the instruction cache.
 #include <cstring>
 
 #include "linattn.cuh"
@@ -32,36 +37,44 @@ using namespace gdn2::tc;
 
 constexpr int D = 128;
 constexpr int C = kChunk;
-constexpr int kThreads = 512;
+constexpr int kRows0 = 4, kState0 = 12, kWeigh0 = 20;  // first warps of the groups of 8
+constexpr int kThreads = 32 * 28;
 constexpr uint32_t kTile = C * D * 2;       // 32 KB, two column blocks of 64
 constexpr uint32_t kBlock = kTile / 2;
-constexpr int kSlice = 32;                  // tokens of a slice of w o Y
-constexpr uint32_t kSliceTile = kSlice * D * 2, kSliceBlock = kSliceTile / 2;
 constexpr uint32_t OFF_X = 0, OFF_Y = kTile, OFF_Z = 3 * kTile;  // Y, Z: two stages
-constexpr uint32_t OFF_S = 5 * kTile;       // the bf16 state, [dz][dy]
-constexpr uint32_t OFF_W = 6 * kTile;       // the ring
+constexpr uint32_t OFF_S = 5 * kTile;       // the bf16 state, [dy][dz]
+constexpr uint32_t OFF_O = 6 * kTile;       // out
 constexpr uint32_t OFF_MISC = 7 * kTile;
-// per stage: the decay from each token to the edge of its 32-token block (log2, as a float and its
-// bf16 remainder), 2^(block total - that), the four block totals
-constexpr uint32_t DEC_HI = 0, DEC_LO = 512, DEC_BETA = 768, DEC_TOT = 1280, DEC_BYTES = 1296;
-constexpr uint32_t MISC_BAR = 2 * DEC_BYTES;
+// For the rows, mild chunks: f and 1 / f of each token, and 1; others: the decay from each token to
+// the edge of its 32-token block (log2), 2^(block total - that), the four block totals (not above
+// 0).  For the state (two stages): for each pair of tokens their weights as three bf16 pairs, then
+// 2^-rho and the factor that scales the accumulator back (1: none).
+constexpr uint32_t DEC_EDGE = 0, DEC_BETA = 512, DEC_TOT = 1024, DEC_W = 1040, DEC_G = 64 * 12, DEC_STAGE = 64 * 12 + 16;
+constexpr uint32_t MISC_BAR = DEC_W + 2 * DEC_STAGE;
+constexpr long long kMild = 32ll << 32;  // 2^-32, in the decays' units
+// A waiter must not look so late that the phase after next is over: where nothing else keeps it, a
+// barrier of each parity of the chunk does.
 enum {
   BAR_Y = 0,        // + stage: Y loaded
   BAR_Z = 2,        // + stage: Z loaded
-  BAR_DEC = 4,      // + stage: decays summed
-  BAR_FREE = 6,     // + stage: nothing uses Y, Z and the decays any more
-  BAR_G = 8,        // + stage: X Y^T done (two: the next may be done before the state warps look)
-  BAR_STAGED = 10,  // + stage: out tile staged (two: the next may be staged before the storing warp looks)
-  BAR_FULL = 12,    // + slot: a slice of w o Y written
-  BAR_EMPTY = 16,   // + slot: its products done
-  BAR_X = 20,       // X loaded
-  BAR_XFREE,        // X Y^T and X S done
-  BAR_XS,           // X S done
-  BAR_P,            // P written
+  BAR_FREE = 4,     // + stage: nothing uses Y and Z any more
+  BAR_DEC = 6,      // + stage: the state's weights there
+  BAR_WFREE = 8,    // + stage: and used
+  BAR_FULL = 10,    // + slot: a slice of w o Y written
+  BAR_EMPTY = 12,   // + slot: its products done
+  BAR_ROWDEC = 14,  // the rows' decays there
+  BAR_ROWFREE,      // and used
+  BAR_X,            // X loaded
+  BAR_XS,           // X S done, X and the state's copy free
+  BAR_G,            // X Y^T done
+  BAR_P,            // P written (and X S scaled)
   BAR_PZ,           // P Z done
-  BAR_U,            // increment done
-  BAR_S,            // bf16 state written
-  BAR_OREAD,        // X S and P Z read
+  BAR_OREAD,        // out read
+  BAR_STAGED,       // out tile staged
+  BAR_OFREE,        // and stored
+  BAR_S,            // the state's copy written
+  BAR_SREAD,        // the state read (and scaled)
+  BAR_U,            // update done
   BAR_CLEAN,        // Y's and Z's rows behind the sequence cleared
   BAR_DRAIN,        // + 0, 1
   N_BARS = BAR_DRAIN + 2
@@ -70,7 +83,8 @@ constexpr uint32_t MISC_TMEM = MISC_BAR + N_BARS * 8, MISC_ABORT = MISC_TMEM + 4
 constexpr uint32_t MISC_BYTES = MISC_ABORT + 4;
 constexpr uint32_t kSmemBytes = OFF_MISC + MISC_BYTES;
 static_assert(kSmemBytes <= 232448, "shared memory over the sm_100 limit per CTA");
-constexpr uint32_t TM_G = 0, TM_PZ = 128, TM_XS = 256, TM_U = 384;  // TMEM columns; P overwrites G
+constexpr uint32_t TM_G = 0, TM_OUT = 128, TM_S = 256, TM_W = 384;  // TMEM columns; TM_W: two slices of w o Y
+constexpr uint32_t TM_P = TM_G + 32;  // P takes the place of the middle half of G
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint32_t kSleepNs = 20000;  // between two looks at the clock: busy waits take issue slots from the workers
 constexpr float kLog2 = 1.4426950408889634f;
@@ -121,11 +135,26 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 __device__ __forceinline__ float2 pair(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
-// The two fp32 values cut (not rounded) to bf16, in place and packed.
-__device__ __forceinline__ float2 cut2(float2 v) {
-  return pair(__float_as_uint(v.x) & 0xffff0000u, __float_as_uint(v.y) & 0xffff0000u);
+__device__ __forceinline__ __nv_bfloat162 bf2(uint32_t w) { return *reinterpret_cast<__nv_bfloat162 *>(&w); }
+__device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t *>(&v); }
+// bf16 pairs whose sum is (w0 + w1 + w2) y to 26 bits (NT = 4) or (w0 + w1) y to 17 (NT = 2): the
+// product of two bf16 is the rounded one and a remainder that bf16 holds exactly.  Joining the
+// remainder and the next product in one term takes seven more operations than a fourth product on
+// the tensor cores, which have the time.
+template <int NT>
+__device__ __forceinline__ void weigh(__nv_bfloat162 y, __nv_bfloat162 w0, __nv_bfloat162 w1, __nv_bfloat162 w2,
+                                      uint32_t (&part)[NT]) {
+  const __nv_bfloat162 hi = __hmul2_rn(w0, y), lo = __hfma2(w0, y, __hneg2(hi));
+  part[0] = bits(hi);
+  if constexpr (NT == 2) {
+    part[1] = bits(__hfma2(w1, y, lo));
+  } else {
+    const __nv_bfloat162 q = __hmul2_rn(w1, y);
+    part[1] = bits(lo);
+    part[2] = bits(q);
+    part[3] = bits(__hfma2(w2, y, __hfma2(w1, y, __hneg2(q))));
+  }
 }
-__device__ __forceinline__ uint32_t pack_cut(float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); }
 // One copy of the waiting loop for all waits: some thirty inlined ones filled the instruction cache.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status,
                                        uint64_t limit_ns) {
@@ -144,7 +173,8 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile i
 
 template <bool BACK, int NT>
 __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_constant__ TcRun P) {
-  constexpr int SLOTS = NT == 3 ? 2 : 4;  // of the ring: NT - 1 slice tiles each
+  constexpr int SLICE = 128 / NT;     // tokens of a slice of w o Y: NT terms in 64 columns, two slots
+  constexpr int SLICES = C / SLICE;
   extern __shared__ __align__(1024) uint8_t smem[];
   const Run &r = P.r;
   const uint32_t sb = ptx::smem_u32(smem);
@@ -160,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
   }
   const int nch = (pc.len + C - 1) / C;
   auto bar = [&](int b) { return sb + OFF_MISC + MISC_BAR + 8u * (uint32_t)b; };
-  auto dec = [&](int s) { return sb + OFF_MISC + (uint32_t)s * DEC_BYTES; };
+  const uint32_t dec = sb + OFF_MISC;
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + OFF_MISC + MISC_ABORT);
   auto wait = [&](int b, uint32_t parity) {
     return ptx::mbar_try_wait(bar(b), parity & 1u) || wait_long(bar(b), parity & 1u, abort_flag, P.status, P.wait_ns);
@@ -177,9 +207,11 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
   if (tid == 0) {
     *abort_flag = 0;
     for (int b = 0; b < N_BARS; ++b) {
-      const bool rows = b == BAR_P || b == BAR_OREAD || b == BAR_STAGED || b == BAR_STAGED + 1;
-      const bool state = b == BAR_S || b == BAR_CLEAN || (b >= BAR_FULL && b < BAR_EMPTY);
-      ptx::mbar_init(bar(b), rows ? 4 : state ? 8 : b == BAR_XFREE ? 2 : 1);
+      const bool group = b == BAR_P || b == BAR_OREAD || b == BAR_STAGED || b == BAR_ROWFREE || b == BAR_S ||
+                         b == BAR_SREAD || b == BAR_CLEAN || b == BAR_FULL || b == BAR_FULL + 1;
+      const bool two = b == BAR_WFREE || b == BAR_WFREE + 1;                      // groups
+      const bool both = (b == BAR_FREE || b == BAR_FREE + 1) && !only;           // issuers
+      ptx::mbar_init(bar(b), group ? 8 : two ? 16 : both ? 2 : 1);
     }
     ptx::fence_mbar_init();
   }
@@ -210,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         for (int b = 0; b < 2; ++b)
           ptx::tma_load_3d(sb + OFF_Z + s * kTile + b * kBlock, &P.tm_z, b * 64, hz, t0, bar(BAR_Z + s));
         if (only) continue;
-        if (k >= 1 && !wait(BAR_XFREE, (uint32_t)k + 1u)) break;
+        if (k >= 1 && !wait(BAR_XS, (uint32_t)k + 1u)) break;
         ptx::mbar_arrive_expect_tx(bar(BAR_X), kTile);
         k_x = k + 1;
         for (int b = 0; b < 2; ++b) ptx::tma_load_3d(sb + OFF_X + b * kBlock, &P.tm_x, b * 64, hx, t0, bar(BAR_X));
@@ -226,49 +258,33 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- the state's products
-    {
-      const bool lead = ptx::elect_one();
-      constexpr uint32_t idKK = ptx::idesc_bf16(128, 128, false, false);
-      constexpr uint32_t idNN = ptx::idesc_bf16(128, 128, true, true);
-      bool ok = true;
-      for (int k = 0; k < nch && ok; ++k) {
-        const int s = k & 1;
-        const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile, z = sb + OFF_Z + (uint32_t)s * kTile;
-        if (!only) {
-          // the state's copy, and the last X S read
-          if (!wait_warp(BAR_X, (uint32_t)k) || !wait_warp(BAR_S, (uint32_t)k) || (k && !wait_warp(BAR_OREAD, (uint32_t)k + 1u))) break;
-          ptx::tc_fence_after();
+    const bool lead = ptx::elect_one();
+    constexpr uint32_t idKN = ptx::idesc_bf16(128, 128, false, true);
+    bool ok = true;
+    for (int k = 0; k < nch && ok; ++k) {
+      const int s = k & 1;
+      ok = wait_warp(BAR_Z + s, (uint32_t)(k >> 1)) && wait_warp(BAR_SREAD, (uint32_t)k);
 #pragma unroll 1
-          for (int kk = 0; kk < 8; ++kk)
-            ptx::umma_bf16_if(lead, tm + TM_XS, kmaj(sb + OFF_X) + k_step(kk), kmaj(sb + OFF_S) + k_step(kk), idKK, kk > 0);
-          ptx::umma_commit_if(lead, bar(BAR_XS));
-          ptx::umma_commit_if(lead, bar(BAR_XFREE));
-        }
-        if (!wait_warp(BAR_Z + s, (uint32_t)(k >> 1))) break;
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const int n = 4 * k + i, slot = n % SLOTS, b = BACK ? i : 3 - i;
-          ok = wait_warp(BAR_FULL + slot, (uint32_t)(n / SLOTS));
-          if (!ok) break;
-          ptx::tc_fence_after();
-          const uint64_t zd = mnmaj(z + (uint32_t)b * (kSlice * 128)), yd = mnmaj(y + (uint32_t)b * (kSlice * 128));
-          const uint64_t wd = mnmaj(sb + OFF_W + (uint32_t)(slot * (NT - 1)) * kSliceTile, kSliceBlock);
-#pragma unroll
-          for (int part = 0; part < NT; ++part)
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-              ptx::umma_bf16_if(lead, tm + TM_U, zd + kk * kMnStep,
-                             (part == 0 ? yd : wd + (uint64_t)(part - 1) * (kSliceTile >> 4)) + kk * kMnStep, idNN,
-                             (i > 0) | (part + kk > 0));
-          ptx::umma_commit_if(lead, bar(BAR_EMPTY + slot));
-        }
+      for (int i = 0; i < SLICES && ok; ++i) {
+        const int n = SLICES * k + i, slot = n & 1, t0 = (BACK ? i : SLICES - 1 - i) * SLICE;
+        ok = wait_warp(BAR_FULL + slot, (uint32_t)(n >> 1));
         if (!ok) break;
-        ptx::umma_commit_if(lead, bar(BAR_U));
-        if (only) ptx::umma_commit_if(lead, bar(BAR_FREE + s));
+        ptx::tc_fence_after();
+        const uint64_t zd = mnmaj(sb + OFF_Z + (uint32_t)s * kTile + (uint32_t)t0 * 128u);
+#pragma unroll
+        for (int part = 0; part < NT; ++part)
+#pragma unroll
+          for (int kk = 0; kk < SLICE / 16; ++kk)
+            ptx::umma_bf16_ts_if(lead, tm + TM_S, tm + TM_W + (uint32_t)(slot * 64 + part * (SLICE / 2) + kk * 8),
+                                 zd + kk * kMnStep, idKN, 1u);
+        ptx::umma_commit_if(lead, bar(BAR_EMPTY + slot));
       }
-      ptx::umma_commit_if(lead, bar(BAR_DRAIN));  // all products, before the tensor memory is freed
-      drain_bar(bar(BAR_DRAIN), 0u, P.wait_ns);
+      if (!ok) break;
+      ptx::umma_commit_if(lead, bar(BAR_U));
+      ptx::umma_commit_if(lead, bar(BAR_FREE + s));
     }
+    ptx::umma_commit_if(lead, bar(BAR_DRAIN));  // all products, before the tensor memory is freed
+    drain_bar(bar(BAR_DRAIN), 0u, P.wait_ns);
   } else if (warp == 3) {
     // ---------------------------------------------------------------- the rows' products
     if (!only) {
@@ -277,31 +293,38 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
       constexpr uint32_t idKN = ptx::idesc_bf16(128, 128, false, true);
       for (int k = 0; k < nch; ++k) {
         const int s = k & 1;
-        const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile, z = sb + OFF_Z + (uint32_t)s * kTile;
+        const uint64_t x = kmaj(sb + OFF_X), y = kmaj(sb + OFF_Y + (uint32_t)s * kTile);
+        const uint64_t z = mnmaj(sb + OFF_Z + (uint32_t)s * kTile), st = mnmaj(sb + OFF_S);
         if (!wait_warp(BAR_X, (uint32_t)k) || !wait_warp(BAR_Y + s, (uint32_t)(k >> 1))) break;
         if (rows_of(k) < C && !wait_warp(BAR_CLEAN, 0u)) break;
         ptx::tc_fence_after();
-#pragma unroll 1
-        for (int kk = 0; kk < 8; ++kk)
-          ptx::umma_bf16_if(lead, tm + TM_G, kmaj(sb + OFF_X) + k_step(kk), kmaj(y) + k_step(kk), idKK, kk > 0);
-        ptx::umma_commit_if(lead, bar(BAR_G + s));
-        ptx::umma_commit_if(lead, bar(BAR_XFREE));
-        if (!wait_warp(BAR_Z + s, (uint32_t)(k >> 1)) || !wait_warp(BAR_P, (uint32_t)k)) break;
-        if (k && !wait_warp(BAR_OREAD, (uint32_t)k + 1u)) break;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) ptx::umma_bf16_if(lead, tm + TM_G, x + k_step(kk), y + k_step(kk), idKK, kk > 0);
+        ptx::umma_commit_if(lead, bar(BAR_G));
+        if (!wait_warp(BAR_S, (uint32_t)k) || (k && !wait_warp(BAR_OREAD, (uint32_t)k + 1u))) break;
         ptx::tc_fence_after();
-#pragma unroll 1
+#pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          ptx::umma_bf16_ts_if(lead, tm + TM_PZ, tm + TM_G + kk * 8, mnmaj(z) + kk * kMnStep, idKN, kk > 0);
+          ptx::umma_bf16_if(lead, tm + TM_OUT, x + k_step(kk), st + kk * kMnStep, idKN, kk > 0);
+        ptx::umma_commit_if(lead, bar(BAR_XS));
+        if (!wait_warp(BAR_Z + s, (uint32_t)(k >> 1)) || !wait_warp(BAR_P, (uint32_t)k)) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          ptx::umma_bf16_ts_if(lead, tm + TM_OUT, tm + TM_P + kk * 8, z + kk * kMnStep, idKN, 1u);
         ptx::umma_commit_if(lead, bar(BAR_PZ));
+        ptx::umma_commit_if(lead, bar(BAR_FREE + s));
       }
       ptx::umma_commit_if(lead, bar(BAR_DRAIN + 1));
       drain_bar(bar(BAR_DRAIN + 1), 0u, P.wait_ns);
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------------- decays and stores
-    // Lane l sums tokens 4 l .. 4 l + 3 in fp64 (a chunk may hold resets beside weak decays); 8
-    // lanes are a block of 32 tokens.  Forward, `edge` of token i is the log2 decay from its
-    // block's start to it, itself included; backward, from it to the block's end, itself not.
+    // Lane l sums tokens 4 l .. 4 l + 3; 8 lanes are a block of 32 tokens.  The sums are whole numbers
+    // of 2^-32 in log2 (a chunk may hold resets beside weak decays, which fp32 sums would blur; in
+    // fp64 this warp took 5000 cycles a chunk, more than anything else).  Forward, `edge` of token i
+    // is the decay from its block's start to it, itself included; backward, from it to the block's
+    // end, itself not.
     const float fixed = r.per_head ? static_cast<const float *>(r.log_a)[h] : 0.f;
     const __nv_bfloat16 *la = static_cast<const __nv_bfloat16 *>(r.log_a);
     auto load = [&](int k, float (&a)[4]) {
@@ -312,373 +335,479 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         a[j] = i >= rows ? 0.f : r.per_head ? fixed : __bfloat162float(la[(size_t)(pc.t0 + c0 + i) * H + h]);
       }
     };
-    // chunk k's out tile; the stage is free once it has been read
+    // chunk k's out tile
     auto store = [&](int k) {
-      if (only) return wait_warp(BAR_FREE + (k & 1), (uint32_t)(k >> 1));
-      if (!wait_warp(BAR_STAGED + (k & 1), (uint32_t)(k >> 1))) return false;
+      if (only) return true;
+      if (!wait_warp(BAR_STAGED, (uint32_t)k)) return false;
       if (lane == 0) {
         if (!r.out_f32 && rows_of(k) == C) {
-          const uint32_t src = sb + OFF_Y + (uint32_t)(k & 1) * kTile;
           const int t0 = pc.t0 + chunk_no(k) * C;
-          for (int b = 0; b < 2; ++b) ptx::tma_store_3d(&P.tm_o, src + b * kBlock, b * 64, h, t0);
+          for (int b = 0; b < 2; ++b) ptx::tma_store_3d(&P.tm_o, sb + OFF_O + b * kBlock, b * 64, h, t0);
           ptx::bulk_commit_group();
           ptx::bulk_wait_group_read0();
         }
-        ptx::mbar_arrive(bar(BAR_FREE + (k & 1)));
+        ptx::mbar_arrive(bar(BAR_OFREE));
       }
       return true;
     };
-    double logs = 0.0;
+    using fix = long long;
+    auto value = [](fix x) { return __ll2float_rn(x) * 0x1p-32f; };
+    fix logs = 0;
     float a[4];
     if (nch > 0) load(0, a);
     bool ok = true;
-    // the last two rounds only store
-    for (int k = 0; k < (only ? nch : nch + 2) && ok; ++k) {
-      if (k >= nch) {
-        if (k >= 2) ok = store(k - 2);
-        continue;
+    fix rho = 0;  // the accumulator holds 2^rho times the state
+    for (int k = 0; k <= nch && ok; ++k) {
+      const uint32_t stage = dec + DEC_W + (uint32_t)(k & 1) * DEC_STAGE;
+      if (k == nch) {
+        if (k >= 2) ok = wait_warp(BAR_WFREE + (k & 1), (uint32_t)(k >> 1) + 1u);
+        if (!ok) break;
+        if (lane == 0) {
+          sts_f32(stage + DEC_G, ptx::ex2(value(-rho)));
+          ptx::mbar_arrive(bar(BAR_DEC + (k & 1)));
+        }
+        break;
       }
-      double own[4];  // inclusive sums inside the lane
+      fix own[4];  // inclusive sums inside the lane
 #pragma unroll
-      for (int j = 0; j < 4; ++j) own[j] = (double)fmaxf(a[j], kMinLog) + (j ? own[j - 1] : 0.0);
+      for (int j = 0; j < 4; ++j)
+        own[j] = __float2ll_rn(fmaxf(a[j], kMinLog) * kLog2 * 0x1p32f) + (j ? own[j - 1] : 0);
       if (k + 1 < nch) load(k + 1, a);
-      double incl = own[3];
+      fix incl = own[3];
 #pragma unroll
       for (int d = 1; d < 8; d <<= 1) {
-        const double up = __shfl_up_sync(0xffffffffu, incl, d, 8);
+        const fix up = __shfl_up_sync(0xffffffffu, incl, d, 8);
         if ((lane & 7) >= d) incl += up;
       }
-      const double total = __shfl_sync(0xffffffffu, incl, 7, 8), before = incl - own[3];
-      float hi[4], beta[4];
-      uint32_t lo[4];
+      const fix total = __shfl_sync(0xffffffffu, incl, 7, 8), before = incl - own[3];
+      fix far = 0, all = 0;  // from the edge of the lane's block to the chunk's far end; the chunk's
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const fix t = __shfl_sync(0xffffffffu, total, 8 * b);
+        all += t;
+        if (BACK ? b < (lane >> 3) : b > (lane >> 3)) far += t;
+      }
+      logs += all;
+      const bool mild = all >= -kMild, keep = rho - all <= kMild;
+      const float behind = ptx::ex2(value(-rho)), back = keep ? 1.f : ptx::ex2(value(all - rho));
+      rho = keep ? rho - all : 0;
+      float one[4], two[4];
+      uint32_t w[2][3];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const double in = before + own[j];
-        const double edge = (BACK ? total - in : in) * (double)kLog2, rest = (BACK ? in : total - in) * (double)kLog2;
-        hi[j] = (float)edge;
-        lo[j] = bf16_bits((float)(edge - (double)hi[j]));
-        beta[j] = ptx::ex2((float)rest);
+        const fix in = before + own[j], rest = BACK ? in : total - in;
+        const float first = value(mild ? all - rest - far : BACK ? total - in : in);
+        one[j] = mild ? ptx::ex2(first) : first;
+        two[j] = ptx::ex2(mild ? -first : value(rest));
+        float left = ptx::ex2(value(rest + far + rho));
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+          const uint32_t b = bf16_bits(left);
+          left -= bf16_value((uint16_t)b);
+          w[j >> 1][n] = j & 1 ? w[j >> 1][n] | b << 16 : b;
+        }
       }
-      if (k >= 2) ok = store(k - 2);
+      if (k >= 2) ok = wait_warp(BAR_WFREE + (k & 1), (uint32_t)(k >> 1) + 1u);
       if (!ok) break;
-      const uint32_t at = dec(k & 1);
-      sts_v4(at + DEC_HI + 16 * lane, make_uint4(__float_as_uint(hi[0]), __float_as_uint(hi[1]), __float_as_uint(hi[2]),
-                                                 __float_as_uint(hi[3])));
-      sts_v2(at + DEC_LO + 8 * lane, make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16));
-      sts_v4(at + DEC_BETA + 16 * lane, make_uint4(__float_as_uint(beta[0]), __float_as_uint(beta[1]),
-                                                   __float_as_uint(beta[2]), __float_as_uint(beta[3])));
-      if ((lane & 7) == 0) sts_f32(at + DEC_TOT + (lane >> 3) * 4, (float)(total * (double)kLog2));
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int n = 0; n < 3; ++n) sts_u32(stage + 24 * lane + 12 * q + 4 * n, w[q][n]);
+      if (lane == 0) sts_v2(stage + DEC_G, make_uint2(__float_as_uint(behind), __float_as_uint(back)));
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(BAR_DEC + (k & 1)));
-      if (only) {
-        logs += __shfl_sync(0xffffffffu, total, 0) + __shfl_sync(0xffffffffu, total, 8) +
-                __shfl_sync(0xffffffffu, total, 16) + __shfl_sync(0xffffffffu, total, 24);
-      }
-    }
-    if (only && lane == 0) r.piece_log[unit] = logs;
-    if (!only && lane == 0) ptx::bulk_wait_group0();
-  } else if (warp < 8) {
-    // ---------------------------------------------------------------- P and out: a token row a thread
-    if (!only) {
-      const int wq = warp & 3, row = wq * 32 + lane;
-      const uint32_t lanes = tm + ((uint32_t)(wq * 32) << 16);
-      for (int k = 0; k < nch; ++k) {
-        const int s = k & 1;
-        const uint32_t at = dec(s);
-        const bool in = row < rows_of(k);
-        const size_t tok = (size_t)pc.t0 + (size_t)chunk_no(k) * C + row;
-        const __nv_bfloat16 *m = nullptr;
-        if (r.m && in) {
-          m = static_cast<const __nv_bfloat16 *>(r.m) + (tok * r.Hm + h / (H / r.Hm)) * D;
-          prefetch_l2(m);
-          prefetch_l2(m + 64);
-        }
-        if (!wait_warp(BAR_DEC + s, (uint32_t)(k >> 1))) break;
-        const float edge = lds_f32(at + DEC_HI + row * 4), edge_lo = bf16_value(lds_u16(at + DEC_LO + row * 2));
-        float near = edge;  // log2 f_i: to the chunk's near end
-        for (int b = BACK ? wq + 1 : 0; b < (BACK ? 4 : wq); ++b) near += lds_f32(at + DEC_TOT + b * 4);
-        const float f = ptx::ex2(near);
-        if (!wait_warp(BAR_G + s, (uint32_t)(k >> 1))) break;
-        ptx::tc_fence_after();
-#pragma unroll 1
-        for (int cb = 0; cb < 4; ++cb) {
-          uint32_t out[16];
-          if (BACK ? cb < wq : cb > wq) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) out[j] = 0u;
-          } else {
-            uint32_t g[32];
-            ptx::tmem_ld32(lanes + TM_G + cb * 32, g);
-            if (cb == wq) {
-              // both tokens in one block: the decay between them, pair by pair
-              const float2 minus = make_float2(-1.f, -1.f), e2 = make_float2(edge, edge);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int j4 = 0; j4 < 8; ++j4) {
-                const float4 e = lds_f4(at + DEC_HI + cb * 128 + j4 * 16);
-                const uint2 l = lds_v2(at + DEC_LO + cb * 64 + j4 * 8);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const int j = j4 * 4 + 2 * i;
-                  const uint32_t lw = i ? l.y : l.x;
-                  const float2 eh = i ? make_float2(e.z, e.w) : make_float2(e.x, e.y);
-                  const float2 d = fma2(eh, minus, e2);
-                  const float2 w = make_float2(ptx::ex2(d.x + (edge_lo - __uint_as_float(lw << 16))),
-                                               ptx::ex2(d.y + (edge_lo - __uint_as_float(lw & 0xffff0000u))));
-                  const float2 v = mul2(w, pair(g[j], g[j + 1]));
-                  out[2 * j4 + i] = pack_bf16x2((BACK ? j >= lane : j <= lane) ? v.x : 0.f,
-                                                (BACK ? j + 1 >= lane : j + 1 <= lane) ? v.y : 0.f);
-                }
-              }
-            } else {
-              // through the edges of the two blocks: a row factor times a column factor, both <= 1
-              float between = edge;
-              for (int b = BACK ? wq + 1 : cb + 1; b < (BACK ? cb : wq); ++b) between += lds_f32(at + DEC_TOT + b * 4);
-              const float alpha = ptx::ex2(between);
-              const float2 a2 = make_float2(alpha, alpha);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int j4 = 0; j4 < 8; ++j4) {
-                const float4 be = lds_f4(at + DEC_BETA + cb * 128 + j4 * 16);
-                const float2 v = mul2(mul2(a2, make_float2(be.x, be.y)), pair(g[4 * j4], g[4 * j4 + 1]));
-                const float2 u = mul2(mul2(a2, make_float2(be.z, be.w)), pair(g[4 * j4 + 2], g[4 * j4 + 3]));
-                out[2 * j4] = pack_bf16x2(v.x, v.y);
-                out[2 * j4 + 1] = pack_bf16x2(u.x, u.y);
-              }
-            }
-          }
-          // columns 16 cb .. are G columns of block cb / 2, read already
-          ptx::tmem_st16(lanes + TM_G + cb * 16, out);
-        }
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
+      if (!only) {
+        if (k) ok = wait_warp(BAR_ROWFREE, (uint32_t)k + 1u);
+        if (!ok) break;
+        sts_v4(dec + DEC_EDGE + 16 * lane, make_uint4(__float_as_uint(one[0]), __float_as_uint(one[1]),
+                                                      __float_as_uint(one[2]), __float_as_uint(one[3])));
+        sts_v4(dec + DEC_BETA + 16 * lane, make_uint4(__float_as_uint(two[0]), __float_as_uint(two[1]),
+                                                      __float_as_uint(two[2]), __float_as_uint(two[3])));
+        if ((lane & 7) == 0) sts_f32(dec + DEC_TOT + (lane >> 3) * 4, mild ? 1.f : value(total));
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(BAR_P));
-        const float2 f2 = make_float2(f, f);
-        float2 dot = make_float2(0.f, 0.f);
-        const bool whole = rows_of(k) == C && !r.out_f32;
-        const uint32_t dst = sb + OFF_Y + (uint32_t)s * kTile;
-        if (!wait_warp(BAR_XS, (uint32_t)k) || !wait_warp(BAR_PZ, (uint32_t)k) || !wait_warp(BAR_U, (uint32_t)k)) break;
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_ROWDEC));
+      }
+      if (k) ok = store(k - 1);
+    }
+    if (ok && nch > 0) store(nch - 1);
+    if (only && lane == 0) r.piece_log[unit] = (double)logs * (0x1p-32 / (double)kLog2);
+    if (!only && lane == 0) ptx::bulk_wait_group0();
+  } else if (warp < 12) {
+    // ---------------------------------------------------------------- P and out: half a token row a thread
+    const int wq = warp & 3, row = wq * 32 + lane, half = (warp - kRows0) >> 2;
+    const uint32_t lanes = tm + ((uint32_t)(wq * 32) << 16);
+    for (int k = 0; k < (only ? 0 : nch); ++k) {
+      const uint32_t at = dec;
+      const bool in = row < rows_of(k);
+      const size_t tok = (size_t)pc.t0 + (size_t)chunk_no(k) * C + row;
+      const __nv_bfloat16 *m = nullptr;
+      if (r.m && in) {
+        m = static_cast<const __nv_bfloat16 *>(r.m) + (tok * r.Hm + h / (H / r.Hm)) * D + half * 64;
+        prefetch_l2(m);
+      }
+      if (!wait_warp(BAR_ROWDEC, (uint32_t)k)) break;
+      const float edge = lds_f32(at + DEC_EDGE + row * 4);
+      const bool mild = lds_f32(at + DEC_TOT) > 0.f;
+      float f = edge;
+      if (!mild) {
+        for (int b = BACK ? wq + 1 : 0; b < (BACK ? 4 : wq); ++b) f += lds_f32(at + DEC_TOT + b * 4);
+        f = ptx::ex2(f);
+      }
+      float2 f2 = make_float2(f, f);
+      if (!wait_warp(BAR_G, (uint32_t)k)) break;
+      ptx::tc_fence_after();
+      // two of the four blocks of 32 columns each; P's 16 columns of a block lie where this warp has
+      // read G already: blocks 1 and 0 write G columns 48.. and 32.., blocks 2 and 3 write 64.. and 80..
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const int cb = half ? 2 + i : 1 - i;
+        uint32_t out[16];
+        if (BACK ? cb < wq : cb > wq) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) out[j] = 0u;
+        } else {
+          uint32_t g[32];
+          ptx::tmem_ld32(lanes + TM_G + cb * 32, g);
+          if (mild) {
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int j4 = 0; j4 < 8; ++j4) {
+              const float4 be = lds_f4(at + DEC_BETA + cb * 128 + j4 * 16);
+              const float2 v = mul2(make_float2(be.x, be.y), pair(g[4 * j4], g[4 * j4 + 1]));
+              const float2 u = mul2(make_float2(be.z, be.w), pair(g[4 * j4 + 2], g[4 * j4 + 3]));
+              out[2 * j4] = pack_bf16x2(v.x, v.y);
+              out[2 * j4 + 1] = pack_bf16x2(u.x, u.y);
+            }
+            if (cb == wq)
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                out[j] &= ((BACK ? 2 * j >= lane : 2 * j <= lane) ? 0xffffu : 0u) |
+                          ((BACK ? 2 * j + 1 >= lane : 2 * j + 1 <= lane) ? 0xffff0000u : 0u);
+          } else if (cb == wq) {
+            // both tokens in one block: the decay between them, pair by pair
+            const float2 minus = make_float2(-1.f, -1.f), e2 = make_float2(edge, edge);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int j4 = 0; j4 < 8; ++j4) {
+              const float4 e = lds_f4(at + DEC_EDGE + cb * 128 + j4 * 16);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const int j = j4 * 4 + 2 * q;
+                const float2 d = fma2(q ? make_float2(e.z, e.w) : make_float2(e.x, e.y), minus, e2);
+                const float2 v = mul2(make_float2(ptx::ex2(d.x), ptx::ex2(d.y)), pair(g[j], g[j + 1]));
+                out[2 * j4 + q] = pack_bf16x2((BACK ? j >= lane : j <= lane) ? v.x : 0.f,
+                                              (BACK ? j + 1 >= lane : j + 1 <= lane) ? v.y : 0.f);
+              }
+            }
+          } else {
+            // through the edges of the two blocks: a row factor times a column factor, both <= 1
+            float between = edge;
+            for (int b = BACK ? wq + 1 : cb + 1; b < (BACK ? cb : wq); ++b) between += lds_f32(at + DEC_TOT + b * 4);
+            const float alpha = ptx::ex2(between);
+            const float2 a2 = make_float2(alpha, alpha);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int j4 = 0; j4 < 8; ++j4) {
+              const float4 be = lds_f4(at + DEC_BETA + cb * 128 + j4 * 16);
+              const float2 v = mul2(mul2(a2, make_float2(be.x, be.y)), pair(g[4 * j4], g[4 * j4 + 1]));
+              const float2 u = mul2(mul2(a2, make_float2(be.z, be.w)), pair(g[4 * j4 + 2], g[4 * j4 + 3]));
+              out[2 * j4] = pack_bf16x2(v.x, v.y);
+              out[2 * j4 + 1] = pack_bf16x2(u.x, u.y);
+            }
+          }
+        }
+        ptx::tmem_st16(lanes + TM_P + cb * 16, out);
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(BAR_ROWFREE));
+      if (!mild) {
+        if (!wait_warp(BAR_XS, (uint32_t)k)) break;
         ptx::tc_fence_after();
 #pragma unroll 1
-        for (int cb = 0; cb < 8; ++cb) {
-          uint4 mw[2];
-          if (m)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) mw[j] = *reinterpret_cast<const uint4 *>(m + cb * 16 + 8 * j);
-          uint32_t u[16], v[16];
-          ptx::tmem_ld16(lanes + TM_PZ + cb * 16, u);
-          ptx::tmem_ld16(lanes + TM_XS + cb * 16, v);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[16];
+          ptx::tmem_ld16(lanes + TM_OUT + half * 64 + c * 16, v);
           ptx::tmem_wait_ld();
-          if (cb == 7) {  // the accumulators are in registers
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(BAR_OREAD));
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(f * __uint_as_float(v[j]));
+          ptx::tmem_st16(lanes + TM_OUT + half * 64 + c * 16, v);
+        }
+        f2 = make_float2(1.f, 1.f);
+      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(BAR_P));
+
+      float2 dot = make_float2(0.f, 0.f);
+      const bool whole = rows_of(k) == C && !r.out_f32;
+      if (!wait_warp(BAR_PZ, (uint32_t)k) || (k && !wait_warp(BAR_OFREE, (uint32_t)k + 1u))) break;
+      ptx::tc_fence_after();
+      const uint32_t dst = sb + OFF_O + (uint32_t)half * kBlock;
+      const size_t at_out = (tok * H + h) * D + half * 64;
+#pragma unroll 1
+      for (int cb = 0; cb < 4; ++cb) {
+        uint4 mw[2];
+        if (m)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) mw[j] = *reinterpret_cast<const uint4 *>(m + cb * 16 + 8 * j);
+        __syncwarp();
+        uint32_t u[16];
+        ptx::tmem_ld16(lanes + TM_OUT + half * 64 + cb * 16, u);
+        ptx::tmem_wait_ld();
+        float2 o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = mul2(f2, pair(u[2 * j], u[2 * j + 1]));
+        if (m)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t w[4] = {mw[j].x, mw[j].y, mw[j].z, mw[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dot = fma2(pair(w[i] << 16, w[i] & 0xffff0000u), o[4 * j + i], dot);
           }
-          float2 o[8];
+        if (r.out_f32) {
+          if (in) {
+            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(r.out) + at_out + cb * 16);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = fma2(f2, pair(v[2 * j], v[2 * j + 1]), pair(u[2 * j], u[2 * j + 1]));
-          if (m)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t w[4] = {mw[j].x, mw[j].y, mw[j].z, mw[j].w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) dot = fma2(pair(w[i] << 16, w[i] & 0xffff0000u), o[4 * j + i], dot);
-            }
+            for (int j = 0; j < 4; ++j) p[j] = make_float4(o[2 * j].x, o[2 * j].y, o[2 * j + 1].x, o[2 * j + 1].y);
+          }
+        } else {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint4 w = make_uint4(pack_bf16x2(o[4 * j].x, o[4 * j].y), pack_bf16x2(o[4 * j + 1].x, o[4 * j + 1].y),
-                                       pack_bf16x2(o[4 * j + 2].x, o[4 * j + 2].y),
-                                       pack_bf16x2(o[4 * j + 3].x, o[4 * j + 3].y));
-            const size_t at_out = (tok * H + h) * D + cb * 16 + 8 * j;
-            if (whole) {
-              sts_v4(dst + (uint32_t)(cb >> 2) * kBlock + swz(row, (uint32_t)((cb & 3) * 2 + j)), w);
-            } else if (in && r.out_f32) {
-              float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(r.out) + at_out);
-              p[0] = make_float4(o[4 * j].x, o[4 * j].y, o[4 * j + 1].x, o[4 * j + 1].y);
-              p[1] = make_float4(o[4 * j + 2].x, o[4 * j + 2].y, o[4 * j + 3].x, o[4 * j + 3].y);
-            } else if (in) {
-              *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(r.out) + at_out) = w;
-            }
+                                       pack_bf16x2(o[4 * j + 2].x, o[4 * j + 2].y), pack_bf16x2(o[4 * j + 3].x, o[4 * j + 3].y));
+            if (whole) sts_v4(dst + swz(row, (uint32_t)(2 * cb + j)), w);
+            else if (in) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(r.out) + at_out + cb * 16 + 8 * j) = w;
           }
-          __syncwarp();
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(BAR_STAGED + s));
-        if (m) r.dots[tok * H + h] = dot.x + dot.y;
-      }
-    }
-  } else {
-    // ---------------------------------------------------------------- state: warp -> 32 z rows x 64 y columns
-    const int wq = warp & 3, half = (warp - 8) >> 2, zrow = wq * 32 + lane;
-    const int stid = tid - 256;
-    const uint32_t lanes = tm + ((uint32_t)(wq * 32) << 16) + TM_U + half * 64;
-    float S[64];
-    {
-      const float *start = nullptr;
-      bool st = false;
-      if (!only) {
-        if (r.piece_state && pc.count > 1) {
-          start = r.piece_state + (size_t)unit * D * D;
-        } else if (r.start) {
-          start = r.start + ((size_t)pc.n * H + h) * D * D;
-          st = r.start_t;
         }
       }
-      if (!start) {
-#pragma unroll
-        for (int j = 0; j < 64; ++j) S[j] = 0.f;
-      } else if (!st) {
-#pragma unroll
-        for (int j = 0; j < 64; ++j) S[j] = start[(half * 64 + j) * D + zrow];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float4 v = *reinterpret_cast<const float4 *>(start + zrow * D + half * 64 + 4 * j);
-          S[4 * j] = v.x; S[4 * j + 1] = v.y; S[4 * j + 2] = v.z; S[4 * j + 3] = v.w;
-        }
-      }
-    }
-    auto write_state = [&]() {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sts_v4(sb + OFF_S + half * kBlock + swz(zrow, (uint32_t)j), pack8(S + 8 * j, 1.f));
+      ptx::tc_fence_before();
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(BAR_S));
+      if (lane == 0) {
+        ptx::mbar_arrive(bar(BAR_OREAD));
+        ptx::mbar_arrive(bar(BAR_STAGED));
+      }
+      if (m) r.dots[((size_t)half * r.cut.t_total + tok) * H + h] = dot.x + dot.y;
+    }
+  } else if (warp < kWeigh0) {
+    // ---------------------------------------------------------------- state: warp -> 32 y rows x 64 z columns
+    const int wq = warp & 3, half = (warp - kState0) >> 2, yrow = wq * 32 + lane, stid = tid - 32 * kState0;
+    const uint32_t quad = tm + ((uint32_t)(wq * 32) << 16);
+    // 32 columns of a state in memory: [dy][dz], or [dz][dy] with `flip`
+    auto load_state = [&](const float *p, bool flip, int z0, uint32_t (&v)[32]) {
+      if (!flip) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 w = *reinterpret_cast<const uint4 *>(p + yrow * D + z0 + 4 * j);
+          v[4 * j] = w.x; v[4 * j + 1] = w.y; v[4 * j + 2] = w.z; v[4 * j + 3] = w.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(p[(z0 + j) * D + yrow]);
+      }
     };
-    // marks of this thread's part of the state at the end of group `g` of chunks
+    auto store_state = [&](float *p, bool flip, int z0, const uint32_t (&v)[32]) {
+      if (!flip) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4 *>(p + yrow * D + z0 + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) p[(z0 + j) * D + yrow] = __uint_as_float(v[j]);
+      }
+    };
+    const float *start = nullptr;
+    float *dst = nullptr;
+    bool flip_start = false, flip_dst = false;
+    if (only) {
+      dst = r.piece_state + (size_t)unit * D * D;
+    } else {
+      if (r.piece_state && pc.count > 1) {
+        start = r.piece_state + (size_t)unit * D * D;
+      } else if (r.start) {
+        start = r.start + ((size_t)pc.n * H + h) * D * D;
+        flip_start = r.start_t;
+      }
+      if (r.fin && pc.s == (BACK ? 0 : pc.count - 1)) {
+        dst = r.fin + ((size_t)pc.n * H + h) * D * D;
+        flip_dst = r.fin_t;
+      }
+    }
+#pragma unroll 1
+    for (int c = 2 * half; c < 2 * half + 2; ++c) {
+      uint32_t v[32];
+      if (start) {
+        load_state(start, flip_start, c * 32, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0u;
+      }
+      __syncwarp();
+      ptx::tmem_st32(quad + TM_S + c * 32, v);
+    }
+    ptx::tmem_wait_st();
+    // marks of this thread's part of the state behind group `g` of chunks
     auto mark_unit = [&](int g) { return (size_t)mark_slot(unit / H, pc.t0 + g * kGroup * C) * H + h; };
     auto ends_group = [&](int no) { return (no + 1) % kGroup == 0 || no == nch - 1; };
-    if (!only && nch > 0) write_state();
+    for (int k = 0; k <= nch; ++k) {
+      const int s = k & 1;
+      const uint32_t par = (uint32_t)(k >> 1);
+      const bool last = k == nch;
+      // the state before the k-th chunk walked: its copy for X S, and scaled back where due
+      if (!wait_warp(BAR_DEC + s, par)) break;
+      const uint32_t gs = dec + DEC_W + (uint32_t)s * DEC_STAGE + DEC_G;
+      const float behind = lds_f32(gs), back = last ? 1.f : lds_f32(gs + 4);
+      const float2 behind2 = make_float2(behind, behind);
+      __syncwarp();
+      if (lane == 0 && !last) ptx::mbar_arrive(bar(BAR_WFREE + s));
+      if (k && !wait_warp(BAR_U, (uint32_t)k + 1u)) break;
+      if (k && !only && !last && !wait_warp(BAR_XS, (uint32_t)k + 1u)) break;  // the last copy has been read
+      ptx::tc_fence_after();
+      const float *mark_in = nullptr;
+      float *mark_out = nullptr;
+      size_t mu = 0;
+      if (r.marks && !only) {
+        const int no = chunk_no(k);  // forward: the group in front of chunk k is done; backward: k's begins
+        if (BACK && !last && ends_group(no)) {
+          mu = mark_unit(no / kGroup);
+          mark_in = r.marks + mu * (D * D) + 4 * yrow;
+        }
+        if (!BACK && k && ends_group(k - 1)) mark_out = r.marks + mark_unit((k - 1) / kGroup) * (D * D) + 4 * yrow;
+        if (BACK && !last && no % kGroup == 1 && no > kGroup) {  // the next group's mark, two chunks ahead
+          const char *next = reinterpret_cast<const char *>(r.marks + mark_unit(no / kGroup - 1) * (D * D)) + stid * 128;
+          prefetch_l2(next);
+          prefetch_l2(next + 32768);
+        }
+      }
+      float dot = 0.f;
+#pragma unroll 1
+      for (int c = 2 * half; c < 2 * half + 2; ++c) {
+        uint32_t v[32];
+        ptx::tmem_ld32(quad + TM_S + c * 32, v);
+        ptx::tmem_wait_ld();
+        if (back != 1.f) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(back * __uint_as_float(v[8 * i + j]));
+            ptx::tmem_st8(quad + TM_S + c * 32 + 8 * i, u);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float2 w = mul2(behind2, pair(v[2 * j], v[2 * j + 1]));
+          v[2 * j] = __float_as_uint(w.x);
+          v[2 * j + 1] = __float_as_uint(w.y);
+        }
+        if (mark_in) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 w = *reinterpret_cast<const float4 *>(mark_in + (c * 8 + j) * 512);
+            dot = fmaf(w.x, __uint_as_float(v[4 * j]), fmaf(w.y, __uint_as_float(v[4 * j + 1]),
+                  fmaf(w.z, __uint_as_float(v[4 * j + 2]), fmaf(w.w, __uint_as_float(v[4 * j + 3]), dot))));
+          }
+        }
+        if (mark_out) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4 *>(mark_out + (c * 8 + j) * 512) =
+                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+        if (last) {
+          if (dst) store_state(dst, flip_dst, c * 32, v);
+          continue;
+        }
+        if (!only)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            sts_v4(sb + OFF_S + (uint32_t)(c >> 1) * kBlock + swz(yrow, (uint32_t)((c & 1) * 4 + j)),
+                   pack8(reinterpret_cast<const float *>(v) + 8 * j, 1.f));
+      }
+      if (!last) {
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        if (!only) ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(BAR_SREAD));
+          if (!only) ptx::mbar_arrive(bar(BAR_S));
+        }
+      }
+      if (mark_in) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+        if (lane == 0) r.mark_dots[mu * kMarkDots + (warp - kState0)] = dot;
+      }
+      if (last) break;
+    }
+  } else {
+    // ---------------------------------------------------------------- w o Y: warp -> 32 y columns, half the tokens
+    const int wq = warp & 3, half = (warp - kWeigh0) >> 2, id = tid - 32 * kWeigh0;
+    const uint32_t quad = tm + ((uint32_t)(wq * 32) << 16);
+    // this lane's row of the four matrices (8 columns x 8 tokens) of 16 columns and 16 tokens
+    const int row = ((lane >> 4) << 3) | (lane & 7);
+    const uint32_t chunk = (uint32_t)(wq & 1) * 4u + (uint32_t)(lane >> 3 & 1);
+    const uint32_t mine = (uint32_t)(wq >> 1) * kBlock;
     bool ok = true;
     for (int k = 0; k < nch && ok; ++k) {
       const int s = k & 1, rows = rows_of(k);
-      if (BACK && r.mark_dots && !only) {
-        const int no = chunk_no(k);
-        if (ends_group(no)) {
-          const size_t mu = mark_unit(no / kGroup);
-          const float4 *mark = reinterpret_cast<const float4 *>(r.marks + mu * (D * D)) + stid;
-          float dot = 0.f;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float4 v = mark[j * 256];
-            dot = fmaf(v.x, S[4 * j], fmaf(v.y, S[4 * j + 1], fmaf(v.z, S[4 * j + 2], fmaf(v.w, S[4 * j + 3], dot))));
-          }
-#pragma unroll
-          for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-          if (lane == 0) r.mark_dots[mu * 8 + (warp - 8)] = dot;
-        }
-        if (no % kGroup == 1 && no > kGroup) {  // the next group's mark, two chunks ahead
-          const char *next = reinterpret_cast<const char *>(r.marks + mark_unit(no / kGroup - 1) * (D * D)) + stid * 256;
-          prefetch_l2(next);
-          prefetch_l2(next + 128);
-        }
-      }
-      const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile, par = (uint32_t)(k >> 1);
-      ok = wait_warp(BAR_DEC + s, par) && wait_warp(BAR_Y + s, par) && (rows == C || wait_warp(BAR_Z + s, par));
-      if (ok && rows < C) {
+      const uint32_t par = (uint32_t)(k >> 1), y = sb + OFF_Y + (uint32_t)s * kTile;
+      if (!wait_warp(BAR_DEC + s, par) || !wait_warp(BAR_Y + s, par)) break;
+      if (rows < C) {
         // rows behind the sequence meet zero weights, which a NaN would outlive
-        for (int t = stid >> 4; t < C; t += 16)
+        if (!wait_warp(BAR_Z + s, par)) break;
+        for (int t = id >> 4; t < C; t += 16)
           if (t >= rows) {
-            const uint32_t to = y + (uint32_t)(stid >> 3 & 1) * kBlock + swz(t, (uint32_t)(stid & 7));
+            const uint32_t to = y + (uint32_t)(id >> 3 & 1) * kBlock + swz(t, (uint32_t)(id & 7));
             sts_v4(to, make_uint4(0u, 0u, 0u, 0u));
             sts_v4(to + (OFF_Z - OFF_Y), make_uint4(0u, 0u, 0u, 0u));
           }
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(BAR_CLEAN));
+        if (!wait_warp(BAR_CLEAN, 0u)) break;  // other warps' rows are read too
       }
-      if (ok && !only) ok = wait_warp(BAR_G + s, (uint32_t)(k >> 1));  // Y may be overwritten
-      if (!ok) break;
-      const float4 tot = lds_f4(dec(s) + DEC_TOT);
-      const float g = ptx::ex2((tot.x + tot.y) + (tot.z + tot.w));
-      float far = 0.f;  // from the edge of the tokens' block to the chunk's far end
+      // slices in the order of the walk; two tokens to a word, transposed into tensor memory
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int b = BACK ? i : 3 - i, n = 4 * k + i, slot = n % SLOTS;
-        const float wb = ptx::ex2(far);
-        far += lds_f32(dec(s) + DEC_TOT + b * 4);
-        const int t = stid >> 4;  // rows t and t + 16 of the slice
-        const uint32_t c = (uint32_t)(stid & 15), in_row = swz(t, c & 7u);
-        const uint32_t to = y + (c >> 3) * kBlock + (uint32_t)b * (kSlice * 128) + in_row;
-        const uint32_t ring = sb + OFF_W + (uint32_t)slot * (NT - 1) * kSliceTile + (c >> 3) * kSliceBlock + in_row;
-        const uint4 yv[2] = {lds_v4(to), lds_v4(to + 2048)};
-        const uint32_t be = dec(s) + DEC_BETA + (b * kSlice + t) * 4;
-        const float w[2] = {wb * lds_f32(be), wb * lds_f32(be + 64)};
-        if (n >= SLOTS) ok = wait_warp(BAR_EMPTY + slot, (uint32_t)(n / SLOTS) + 1u);
+      for (int i = 0; i < SLICES && ok; ++i) {
+        const int n = SLICES * k + i, slot = n & 1, t0 = (BACK ? i : SLICES - 1 - i) * SLICE + half * (SLICE / 2);
+        if (n >= 2) ok = wait_warp(BAR_EMPTY + slot, (uint32_t)(n >> 1) + 1u);
         if (!ok) break;
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int t = 0; t < SLICE / 2; t += 16) {
+          // weights of the pairs of tokens that this lane's columns of the matrices are
+          const uint32_t ws = dec + DEC_W + (uint32_t)s * DEC_STAGE + (uint32_t)((t0 + t) / 2 + (lane & 3)) * 12u;
+          __nv_bfloat162 w[2][3];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t yw[4] = {yv[q].x, yv[q].y, yv[q].z, yv[q].w};
-          const float2 w2 = make_float2(w[q], w[q]), minus = make_float2(-1.f, -1.f);
-          uint32_t part[3][4];
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // the first terms are cut, the last rounded: 8 bits each, the signs all the same
-            float2 v = mul2(pair(yw[j] << 16, yw[j] & 0xffff0000u), w2);
+            for (int j = 0; j < (NT == 2 ? 2 : 3); ++j) w[q][j] = bf2(__float_as_uint(lds_f32(ws + 48 * q + 4 * j)));
+          const uint32_t to = quad + TM_W + (uint32_t)(slot * 64 + half * (SLICE / 4) + t / 2);
 #pragma unroll
-            for (int p = 0; p < NT; ++p) {
-              part[p][j] = p + 1 < NT ? pack_cut(v) : pack_bf16x2(v.x, v.y);
-              if (p + 1 < NT) v = fma2(cut2(v), minus, v);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t yw[4], terms[NT][4];
+            ptx::ldmatrix4_trans(y + mine + (uint32_t)(t0 + t) * 128u + swz(row, chunk + 2u * c), yw);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              uint32_t got[NT];
+              weigh<NT>(bf2(yw[p]), w[p >> 1][0], w[p >> 1][1], w[p >> 1][2], got);
+#pragma unroll
+              for (int m = 0; m < NT; ++m) terms[m][p] = got[m];
             }
-          }
-          sts_v4(to + q * 2048, make_uint4(part[0][0], part[0][1], part[0][2], part[0][3]));
 #pragma unroll
-          for (int p = 1; p < NT; ++p)
-            sts_v4(ring + (p - 1) * kSliceTile + q * 2048, make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]));
+            for (int m = 0; m < NT; ++m)
+              ptx::tmem_st_16x8(to + ((uint32_t)(16 * c) << 16) + (uint32_t)m * (SLICE / 2), terms[m]);
+          }
         }
-        ptx::fence_proxy_async_smem();
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(BAR_FULL + slot));
       }
-      if (!ok) break;
-      ok = wait_warp(BAR_U, (uint32_t)k);
-      if (!ok) break;
-      ptx::tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t u[32];
-        ptx::tmem_ld32(lanes + c * 32, u);
-        ptx::tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float *p = S + c * 32 + 2 * j;
-          const float2 v = fma2(make_float2(g, g), make_float2(p[0], p[1]), pair(u[2 * j], u[2 * j + 1]));
-          p[0] = v.x;
-          p[1] = v.y;
-        }
-      }
-      ptx::tc_fence_before();
-      if (!only && k + 1 < nch) {
-        ok = wait_warp(BAR_XS, (uint32_t)k);  // the last copy has been read
-        if (!ok) break;
-        write_state();
-      }
-      if (!BACK && r.marks && !only && ends_group(k)) {
-        float4 *mark = reinterpret_cast<float4 *>(r.marks + mark_unit(k / kGroup) * (D * D)) + stid;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) mark[j * 256] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
-      }
-    }
-    float *dst = nullptr;
-    bool dt = false;
-    if (only) {
-      dst = r.piece_state + (size_t)unit * D * D;
-    } else if (r.fin && pc.s == (BACK ? 0 : pc.count - 1)) {
-      dst = r.fin + ((size_t)pc.n * H + h) * D * D;
-      dt = r.fin_t;
-    }
-    if (dst && ok) {
-      if (!dt) {
-#pragma unroll
-        for (int j = 0; j < 64; ++j) dst[(half * 64 + j) * D + zrow] = S[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          *reinterpret_cast<float4 *>(dst + zrow * D + half * 64 + 4 * j) =
-              make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
-      }
+      if (lane == 0) ptx::mbar_arrive(bar(BAR_WFREE + s));
     }
   }
   __syncwarp();
@@ -707,7 +836,8 @@ __global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *d
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
       const size_t at = (t0 + first + j) * H + h;
-      v[j] = first + j < cnt ? dots_q[at] - dots_k[at] : 0.f;
+      const size_t too = at + (size_t)c.t_total * H;  // the other half of the columns
+      v[j] = first + j < cnt ? (dots_q[at] + dots_q[too]) - (dots_k[at] + dots_k[too]) : 0.f;
     }
 #pragma unroll
     for (int j = kEach - 2; j >= 0; --j) v[j] += v[j + 1];
@@ -718,10 +848,10 @@ __global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *d
       const float down = __shfl_down_sync(0xffffffffu, incl, d);
       if (lane + d < 32) incl += down;
     }
-    const float *end = mark_dots + ((size_t)mark_slot(unit / H, (int)t0) * H + h) * 8;
+    const float *end = mark_dots + ((size_t)mark_slot(unit / H, (int)t0) * H + h) * kMarkDots;
     float behind = incl - own;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) behind += end[w];
+    for (int w = 0; w < kMarkDots; ++w) behind += end[w];
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
       if (first + j < cnt) dlog[(t0 + first + j) * H + h] = __float2bfloat16_rn(v[j] + behind);
@@ -757,8 +887,8 @@ cudaError_t launch_run_tc(const Run &r, int terms, int32_t *status, cudaStream_t
     P.dbg_skip = 1;
     P.wait_ns = hook_ns;
   }
-  if (r.back) return terms == 3 ? launch_t<true, 3>(P, s) : launch_t<true, 2>(P, s);
-  return terms == 3 ? launch_t<false, 3>(P, s) : launch_t<false, 2>(P, s);
+  if (r.back) return terms == 4 ? launch_t<true, 4>(P, s) : launch_t<true, 2>(P, s);
+  return terms == 4 ? launch_t<false, 4>(P, s) : launch_t<false, 2>(P, s);
 }
 
 cudaError_t launch_dlog_tc(const float *dots_q, const float *dots_k, const float *mark_dots, const Cut &c, void *dlog,
