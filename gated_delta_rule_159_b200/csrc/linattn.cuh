@@ -117,7 +117,8 @@ struct Run {
   double *piece_log;     // [n_pieces * H]
   int state_only;        // write piece_state and piece_log, no out
   // For the gradient of log_a: partial dots of every out row with the row of m (Hm heads, dz
-  // columns) over the columns of one slice (the tensor-core runs have two), [slices][T, H]; NULL: none.
+  // columns) over the columns of one slice, [slices][T, H] (the tensor-core runs: two halves, [2][H, T]);
+  // NULL: none.
   const void *m;
   int Hm;
   float *dots;

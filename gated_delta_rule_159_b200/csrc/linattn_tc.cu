@@ -541,16 +541,16 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
 
       float2 dot = make_float2(0.f, 0.f);
       const bool whole = rows_of(k) == C && !r.out_f32;
+      uint4 mw[2];  // 16 values of m's row, asked for one step ahead
+      if (m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mw[j] = *reinterpret_cast<const uint4 *>(m + 8 * j);
       if (!wait_warp(BAR_PZ, (uint32_t)k) || (k && !wait_warp(BAR_OFREE, (uint32_t)k + 1u))) break;
       ptx::tc_fence_after();
       const uint32_t dst = sb + OFF_O + (uint32_t)half * kBlock;
       const size_t at_out = (tok * H + h) * D + half * 64;
 #pragma unroll 1
       for (int cb = 0; cb < 4; ++cb) {
-        uint4 mw[2];
-        if (m)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) mw[j] = *reinterpret_cast<const uint4 *>(m + cb * 16 + 8 * j);
         __syncwarp();
         uint32_t u[16];
         ptx::tmem_ld16(lanes + TM_OUT + half * 64 + cb * 16, u);
@@ -562,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint32_t w[4] = {mw[j].x, mw[j].y, mw[j].z, mw[j].w};
+            if (cb < 3) mw[j] = *reinterpret_cast<const uint4 *>(m + (cb + 1) * 16 + 8 * j);
 #pragma unroll
             for (int i = 0; i < 4; ++i) dot = fma2(pair(w[i] << 16, w[i] & 0xffff0000u), o[4 * j + i], dot);
           }
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         ptx::mbar_arrive(bar(BAR_OREAD));
         ptx::mbar_arrive(bar(BAR_STAGED));
       }
-      if (m) r.dots[((size_t)half * r.cut.t_total + tok) * H + h] = dot.x + dot.y;
+      if (m) r.dots[(size_t)(half * H + h) * r.cut.t_total + tok] = dot.x + dot.y;
     }
   } else if (warp < kWeigh0) {
     // ---------------------------------------------------------------- state: warp -> 32 y rows x 64 z columns
@@ -821,40 +822,38 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
 
 // dlog_a_t = sum_{t <= i in the group} (q_i . dq_i - k_i . dk_i) + <S, dLoss/dS> behind the group.  The dots carry
 // bf16 products whose errors would add up along a sequence; the marks' product starts each group afresh.
-// A warp per group of kGroup chunks, 16 tokens a lane.
+// A warp per group of kGroup chunks.
 constexpr int kDlogWarps = 4;
 __global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *dots_q, const float *dots_k,
                                                                   const float *mark_dots, Cut c, __nv_bfloat16 *dlog) {
-  constexpr int kTokens = kGroup * C, kEach = kTokens / 32;
+  constexpr int kTokens = kGroup * C;
   const int H = c.H, unit = blockIdx.x, h = unit % H, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Piece pc;
   if (!find_piece(c, unit / H, &pc)) return;
+  const size_t half = (size_t)H * c.t_total;  // the dots of the other half of the columns
   for (int g = blockIdx.y * kDlogWarps + warp; g * kTokens < pc.len; g += gridDim.y * kDlogWarps) {
-    const size_t t0 = (size_t)pc.t0 + (size_t)g * kTokens;
-    const int cnt = min(kTokens, pc.len - g * kTokens), first = lane * kEach;
-    float v[kEach];
+    const size_t t0 = (size_t)pc.t0 + (size_t)g * kTokens, at = (size_t)h * c.t_total + t0;
+    const int cnt = min(kTokens, pc.len - g * kTokens);
+    float v[kTokens / 32];
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const size_t at = (t0 + first + j) * H + h;
-      const size_t too = at + (size_t)c.t_total * H;  // the other half of the columns
-      v[j] = first + j < cnt ? (dots_q[at] + dots_q[too]) - (dots_k[at] + dots_k[too]) : 0.f;
-    }
-#pragma unroll
-    for (int j = kEach - 2; j >= 0; --j) v[j] += v[j + 1];
-    const float own = v[0];
-    float incl = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const float down = __shfl_down_sync(0xffffffffu, incl, d);
-      if (lane + d < 32) incl += down;
+    for (int j = 0; j < kTokens / 32; ++j) {
+      const size_t i = at + 32 * j + lane;
+      v[j] = 32 * j + lane < cnt ? (dots_q[i] + dots_q[half + i]) - (dots_k[i] + dots_k[half + i]) : 0.f;
     }
     const float *end = mark_dots + ((size_t)mark_slot(unit / H, (int)t0) * H + h) * kMarkDots;
-    float behind = incl - own;
+    float behind = 0.f;
 #pragma unroll
     for (int w = 0; w < kMarkDots; ++w) behind += end[w];
 #pragma unroll
-    for (int j = 0; j < kEach; ++j)
-      if (first + j < cnt) dlog[(t0 + first + j) * H + h] = __float2bfloat16_rn(v[j] + behind);
+    for (int j = kTokens / 32 - 1; j >= 0; --j) {
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const float down = __shfl_down_sync(0xffffffffu, v[j], d);
+        if (lane + d < 32) v[j] += down;
+      }
+      if (32 * j + lane < cnt) dlog[(t0 + 32 * j + lane) * H + h] = __float2bfloat16_rn(v[j] + behind);
+      behind += __shfl_sync(0xffffffffu, v[j], 0);
+    }
   }
 }
 
