@@ -18,12 +18,12 @@
 // Memory is what bounds it: 4 tiles of 32 KB a chunk, 128 KB against 2.9 us of 6.6 TB/s / 148 SMs;
 // the products take 5 x 512 (NT = 2) or 7 x 512 tensor cycles.  What costs time is the chains of
 // short steps on the CUDA cores, so they run side by side, each a group of warps of its own: warp 0
-// loads; warp 1 issues the state's products, warp 3 the rows' (G, X S, P Z); warp 2 sums the decays
-// and stores; warps 4-11 own half a token row a thread (P, out); warps 12-19 copy the state to bf16
-// for X S (and scale it); warps 20-27 weight Y, transposed into tensor memory: with w o Y in shared
-// memory (every term written, and read with Z) that memory's 128 bytes a cycle were short.  X has
-// one tile, Y and Z two stages.  The loops stay rolled: unrolled, the roles together ran out of
-// the instruction cache.
+// loads; warp 1 issues the state's products, warp 3 the rows' (G, X S, P Z); warp 2 sums the decays;
+// warps 4-11 write P, half a token row a thread, and warps 12-19 out; warps 20-27 copy the state to
+// bf16 for X S (and scale it) and weight Y, transposed into tensor memory: with w o Y in shared memory
+// (every term written, and read with Z) that memory's 128 bytes a cycle were short, and they still
+// are what the CUDA cores wait for while products run.  X has one tile, Y and Z two stages.  The
+// loops stay rolled: unrolled, the roles together ran out of the instruction cache.
 #include <cstring>
 
 #include "linattn.cuh"
@@ -37,7 +37,7 @@ using namespace gdn2::tc;
 
 constexpr int D = 128;
 constexpr int C = kChunk;
-constexpr int kRows0 = 4, kState0 = 12, kWeigh0 = 20;  // first warps of the groups of 8
+constexpr int kRows0 = 4, kOut0 = 12, kState0 = 20;  // first warps of the groups of 8
 constexpr int kThreads = 32 * 28;
 constexpr uint32_t kTile = C * D * 2;       // 32 KB, two column blocks of 64
 constexpr uint32_t kBlock = kTile / 2;
@@ -67,11 +67,9 @@ enum {
   BAR_X,            // X loaded
   BAR_XS,           // X S done, X and the state's copy free
   BAR_G,            // X Y^T done
-  BAR_P,            // P written (and X S scaled)
+  BAR_P,            // P written, and X S scaled where it has to be
   BAR_PZ,           // P Z done
   BAR_OREAD,        // out read
-  BAR_STAGED,       // out tile staged
-  BAR_OFREE,        // and stored
   BAR_S,            // the state's copy written
   BAR_SREAD,        // the state read (and scaled)
   BAR_U,            // update done
@@ -207,9 +205,9 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
   if (tid == 0) {
     *abort_flag = 0;
     for (int b = 0; b < N_BARS; ++b) {
-      const bool group = b == BAR_P || b == BAR_OREAD || b == BAR_STAGED || b == BAR_ROWFREE || b == BAR_S ||
-                         b == BAR_SREAD || b == BAR_CLEAN || b == BAR_FULL || b == BAR_FULL + 1;
-      const bool two = b == BAR_WFREE || b == BAR_WFREE + 1;                      // groups
+      const bool group = b == BAR_OREAD || b == BAR_WFREE || b == BAR_WFREE + 1 || b == BAR_S || b == BAR_SREAD ||
+                         b == BAR_CLEAN || b == BAR_FULL || b == BAR_FULL + 1;
+      const bool two = b == BAR_P || b == BAR_ROWFREE;                           // groups
       const bool both = (b == BAR_FREE || b == BAR_FREE + 1) && !only;           // issuers
       ptx::mbar_init(bar(b), group ? 8 : two ? 16 : both ? 2 : 1);
     }
@@ -319,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
       drain_bar(bar(BAR_DRAIN + 1), 0u, P.wait_ns);
     }
   } else if (warp == 2) {
-    // ---------------------------------------------------------------- decays and stores
+    // ---------------------------------------------------------------- decays
     // Lane l sums tokens 4 l .. 4 l + 3; 8 lanes are a block of 32 tokens.  The sums are whole numbers
     // of 2^-32 in log2 (a chunk may hold resets beside weak decays, which fp32 sums would blur; in
     // fp64 this warp took 5000 cycles a chunk, more than anything else).  Forward, `edge` of token i
@@ -334,21 +332,6 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         const int i = 4 * lane + j;
         a[j] = i >= rows ? 0.f : r.per_head ? fixed : __bfloat162float(la[(size_t)(pc.t0 + c0 + i) * H + h]);
       }
-    };
-    // chunk k's out tile
-    auto store = [&](int k) {
-      if (only) return true;
-      if (!wait_warp(BAR_STAGED, (uint32_t)k)) return false;
-      if (lane == 0) {
-        if (!r.out_f32 && rows_of(k) == C) {
-          const int t0 = pc.t0 + chunk_no(k) * C;
-          for (int b = 0; b < 2; ++b) ptx::tma_store_3d(&P.tm_o, sb + OFF_O + b * kBlock, b * 64, h, t0);
-          ptx::bulk_commit_group();
-          ptx::bulk_wait_group_read0();
-        }
-        ptx::mbar_arrive(bar(BAR_OFREE));
-      }
-      return true;
     };
     using fix = long long;
     auto value = [](fix x) { return __ll2float_rn(x) * 0x1p-32f; };
@@ -427,33 +410,17 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(BAR_ROWDEC));
       }
-      if (k) ok = store(k - 1);
     }
-    if (ok && nch > 0) store(nch - 1);
     if (only && lane == 0) r.piece_log[unit] = (double)logs * (0x1p-32 / (double)kLog2);
-    if (!only && lane == 0) ptx::bulk_wait_group0();
-  } else if (warp < 12) {
-    // ---------------------------------------------------------------- P and out: half a token row a thread
+  } else if (warp < kOut0) {
+    // ---------------------------------------------------------------- P: half a token row a thread
     const int wq = warp & 3, row = wq * 32 + lane, half = (warp - kRows0) >> 2;
     const uint32_t lanes = tm + ((uint32_t)(wq * 32) << 16);
     for (int k = 0; k < (only ? 0 : nch); ++k) {
       const uint32_t at = dec;
-      const bool in = row < rows_of(k);
-      const size_t tok = (size_t)pc.t0 + (size_t)chunk_no(k) * C + row;
-      const __nv_bfloat16 *m = nullptr;
-      if (r.m && in) {
-        m = static_cast<const __nv_bfloat16 *>(r.m) + (tok * r.Hm + h / (H / r.Hm)) * D + half * 64;
-        prefetch_l2(m);
-      }
       if (!wait_warp(BAR_ROWDEC, (uint32_t)k)) break;
       const float edge = lds_f32(at + DEC_EDGE + row * 4);
       const bool mild = lds_f32(at + DEC_TOT) > 0.f;
-      float f = edge;
-      if (!mild) {
-        for (int b = BACK ? wq + 1 : 0; b < (BACK ? 4 : wq); ++b) f += lds_f32(at + DEC_TOT + b * 4);
-        f = ptx::ex2(f);
-      }
-      float2 f2 = make_float2(f, f);
       if (!wait_warp(BAR_G, (uint32_t)k)) break;
       ptx::tc_fence_after();
       // two of the four blocks of 32 columns each; P's 16 columns of a block lie where this warp has
@@ -518,6 +485,35 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         }
         ptx::tmem_st16(lanes + TM_P + cb * 16, out);
       }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(bar(BAR_ROWFREE));
+        ptx::mbar_arrive(bar(BAR_P));
+      }
+    }
+  } else if (warp < kState0) {
+    // ---------------------------------------------------------------- out: half a token row a thread
+    const int wq = warp & 3, row = wq * 32 + lane, half = (warp - kOut0) >> 2;
+    const uint32_t lanes = tm + ((uint32_t)(wq * 32) << 16) + TM_OUT + half * 64;
+    const uint32_t tile = sb + OFF_O + (uint32_t)half * kBlock;
+    for (int k = 0; k < (only ? 0 : nch); ++k) {
+      const bool in = row < rows_of(k);
+      const size_t tok = (size_t)pc.t0 + (size_t)chunk_no(k) * C + row;
+      const __nv_bfloat16 *m = nullptr;
+      if (r.m && in) {
+        m = static_cast<const __nv_bfloat16 *>(r.m) + (tok * r.Hm + h / (H / r.Hm)) * D + half * 64;
+        prefetch_l2(m);
+      }
+      if (!wait_warp(BAR_ROWDEC, (uint32_t)k)) break;
+      float f = lds_f32(dec + DEC_EDGE + row * 4);
+      const bool mild = lds_f32(dec + DEC_TOT) > 0.f;
+      if (!mild) {
+        for (int b = BACK ? wq + 1 : 0; b < (BACK ? 4 : wq); ++b) f += lds_f32(dec + DEC_TOT + b * 4);
+        f = ptx::ex2(f);
+      }
+      float2 f2 = make_float2(f, f);
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(BAR_ROWFREE));
       if (!mild) {
@@ -526,34 +522,35 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t v[16];
-          ptx::tmem_ld16(lanes + TM_OUT + half * 64 + c * 16, v);
+          ptx::tmem_ld16(lanes + c * 16, v);
           ptx::tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(f * __uint_as_float(v[j]));
-          ptx::tmem_st16(lanes + TM_OUT + half * 64 + c * 16, v);
+          ptx::tmem_st16(lanes + c * 16, v);
         }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
         f2 = make_float2(1.f, 1.f);
       }
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(BAR_P));
-
+      if (lane == 0) {
+        ptx::mbar_arrive(bar(BAR_P));
+        ptx::bulk_wait_group_read0();  // this warp's rows of the tile
+      }
       float2 dot = make_float2(0.f, 0.f);
-      const bool whole = rows_of(k) == C && !r.out_f32;
+      const bool whole = wq * 32 + 32 <= rows_of(k) && !r.out_f32;
       uint4 mw[2];  // 16 values of m's row, asked for one step ahead
       if (m)
 #pragma unroll
         for (int j = 0; j < 2; ++j) mw[j] = *reinterpret_cast<const uint4 *>(m + 8 * j);
-      if (!wait_warp(BAR_PZ, (uint32_t)k) || (k && !wait_warp(BAR_OFREE, (uint32_t)k + 1u))) break;
+      if (!wait_warp(BAR_PZ, (uint32_t)k)) break;
       ptx::tc_fence_after();
-      const uint32_t dst = sb + OFF_O + (uint32_t)half * kBlock;
       const size_t at_out = (tok * H + h) * D + half * 64;
 #pragma unroll 1
       for (int cb = 0; cb < 4; ++cb) {
         __syncwarp();
         uint32_t u[16];
-        ptx::tmem_ld16(lanes + TM_OUT + half * 64 + cb * 16, u);
+        ptx::tmem_ld16(lanes + cb * 16, u);
         ptx::tmem_wait_ld();
         float2 o[8];
 #pragma unroll
@@ -577,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
           for (int j = 0; j < 2; ++j) {
             const uint4 w = make_uint4(pack_bf16x2(o[4 * j].x, o[4 * j].y), pack_bf16x2(o[4 * j + 1].x, o[4 * j + 1].y),
                                        pack_bf16x2(o[4 * j + 2].x, o[4 * j + 2].y), pack_bf16x2(o[4 * j + 3].x, o[4 * j + 3].y));
-            if (whole) sts_v4(dst + swz(row, (uint32_t)(2 * cb + j)), w);
+            if (whole) sts_v4(tile + swz(row, (uint32_t)(2 * cb + j)), w);
             else if (in) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(r.out) + at_out + cb * 16 + 8 * j) = w;
           }
         }
@@ -587,195 +584,55 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) {
         ptx::mbar_arrive(bar(BAR_OREAD));
-        ptx::mbar_arrive(bar(BAR_STAGED));
+        if (whole) {
+          ptx::tma_store_3d(&P.tm_o, tile + (uint32_t)wq * 4096u, half * 64, h, pc.t0 + chunk_no(k) * C + wq * 32);
+          ptx::bulk_commit_group();
+        }
       }
       if (m) r.dots[(size_t)(half * H + h) * r.cut.t_total + tok] = dot.x + dot.y;
     }
-  } else if (warp < kWeigh0) {
-    // ---------------------------------------------------------------- state: warp -> 32 y rows x 64 z columns
+    if (lane == 0) ptx::bulk_wait_group0();
+  } else {
+    // ---------------------------------------------------------------- state (warp: 32 y rows x 64 z columns) and w o Y
+    // (warp: 32 y columns, half the tokens of a slice)
     const int wq = warp & 3, half = (warp - kState0) >> 2, yrow = wq * 32 + lane, stid = tid - 32 * kState0;
     const uint32_t quad = tm + ((uint32_t)(wq * 32) << 16);
-    // 32 columns of a state in memory: [dy][dz], or [dz][dy] with `flip`
-    auto load_state = [&](const float *p, bool flip, int z0, uint32_t (&v)[32]) {
+    // 16 columns of a state in memory: [dy][dz], or [dz][dy] with `flip`
+    auto load_state = [&](const float *p, bool flip, int z0, uint32_t (&v)[16]) {
       if (!flip) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const uint4 w = *reinterpret_cast<const uint4 *>(p + yrow * D + z0 + 4 * j);
           v[4 * j] = w.x; v[4 * j + 1] = w.y; v[4 * j + 2] = w.z; v[4 * j + 3] = w.w;
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(p[(z0 + j) * D + yrow]);
+        for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(p[(z0 + j) * D + yrow]);
       }
     };
-    auto store_state = [&](float *p, bool flip, int z0, const uint32_t (&v)[32]) {
+    auto store_state = [&](float *p, bool flip, int z0, const uint32_t (&v)[16]) {
       if (!flip) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 4; ++j)
           *reinterpret_cast<uint4 *>(p + yrow * D + z0 + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) p[(z0 + j) * D + yrow] = __uint_as_float(v[j]);
+        for (int j = 0; j < 16; ++j) p[(z0 + j) * D + yrow] = __uint_as_float(v[j]);
       }
     };
-    const float *start = nullptr;
-    float *dst = nullptr;
-    bool flip_start = false, flip_dst = false;
-    if (only) {
-      dst = r.piece_state + (size_t)unit * D * D;
-    } else {
-      if (r.piece_state && pc.count > 1) {
-        start = r.piece_state + (size_t)unit * D * D;
-      } else if (r.start) {
-        start = r.start + ((size_t)pc.n * H + h) * D * D;
-        flip_start = r.start_t;
-      }
-      if (r.fin && pc.s == (BACK ? 0 : pc.count - 1)) {
-        dst = r.fin + ((size_t)pc.n * H + h) * D * D;
-        flip_dst = r.fin_t;
-      }
-    }
-#pragma unroll 1
-    for (int c = 2 * half; c < 2 * half + 2; ++c) {
-      uint32_t v[32];
-      if (start) {
-        load_state(start, flip_start, c * 32, v);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0u;
-      }
-      __syncwarp();
-      ptx::tmem_st32(quad + TM_S + c * 32, v);
-    }
-    ptx::tmem_wait_st();
-    // marks of this thread's part of the state behind group `g` of chunks
-    auto mark_unit = [&](int g) { return (size_t)mark_slot(unit / H, pc.t0 + g * kGroup * C) * H + h; };
-    auto ends_group = [&](int no) { return (no + 1) % kGroup == 0 || no == nch - 1; };
-    for (int k = 0; k <= nch; ++k) {
-      const int s = k & 1;
-      const uint32_t par = (uint32_t)(k >> 1);
-      const bool last = k == nch;
-      // the state before the k-th chunk walked: its copy for X S, and scaled back where due
-      if (!wait_warp(BAR_DEC + s, par)) break;
-      const uint32_t gs = dec + DEC_W + (uint32_t)s * DEC_STAGE + DEC_G;
-      const float behind = lds_f32(gs), back = last ? 1.f : lds_f32(gs + 4);
-      const float2 behind2 = make_float2(behind, behind);
-      __syncwarp();
-      if (lane == 0 && !last) ptx::mbar_arrive(bar(BAR_WFREE + s));
-      if (k && !wait_warp(BAR_U, (uint32_t)k + 1u)) break;
-      if (k && !only && !last && !wait_warp(BAR_XS, (uint32_t)k + 1u)) break;  // the last copy has been read
-      ptx::tc_fence_after();
-      const float *mark_in = nullptr;
-      float *mark_out = nullptr;
-      size_t mu = 0;
-      if (r.marks && !only) {
-        const int no = chunk_no(k);  // forward: the group in front of chunk k is done; backward: k's begins
-        if (BACK && !last && ends_group(no)) {
-          mu = mark_unit(no / kGroup);
-          mark_in = r.marks + mu * (D * D) + 4 * yrow;
-        }
-        if (!BACK && k && ends_group(k - 1)) mark_out = r.marks + mark_unit((k - 1) / kGroup) * (D * D) + 4 * yrow;
-        if (BACK && !last && no % kGroup == 1 && no > kGroup) {  // the next group's mark, two chunks ahead
-          const char *next = reinterpret_cast<const char *>(r.marks + mark_unit(no / kGroup - 1) * (D * D)) + stid * 128;
-          prefetch_l2(next);
-          prefetch_l2(next + 32768);
-        }
-      }
-      float dot = 0.f;
-#pragma unroll 1
-      for (int c = 2 * half; c < 2 * half + 2; ++c) {
-        uint32_t v[32];
-        ptx::tmem_ld32(quad + TM_S + c * 32, v);
-        ptx::tmem_wait_ld();
-        if (back != 1.f) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t u[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(back * __uint_as_float(v[8 * i + j]));
-            ptx::tmem_st8(quad + TM_S + c * 32 + 8 * i, u);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 w = mul2(behind2, pair(v[2 * j], v[2 * j + 1]));
-          v[2 * j] = __float_as_uint(w.x);
-          v[2 * j + 1] = __float_as_uint(w.y);
-        }
-        if (mark_in) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 w = *reinterpret_cast<const float4 *>(mark_in + (c * 8 + j) * 512);
-            dot = fmaf(w.x, __uint_as_float(v[4 * j]), fmaf(w.y, __uint_as_float(v[4 * j + 1]),
-                  fmaf(w.z, __uint_as_float(v[4 * j + 2]), fmaf(w.w, __uint_as_float(v[4 * j + 3]), dot))));
-          }
-        }
-        if (mark_out) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4 *>(mark_out + (c * 8 + j) * 512) =
-                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        }
-        if (last) {
-          if (dst) store_state(dst, flip_dst, c * 32, v);
-          continue;
-        }
-        if (!only)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            sts_v4(sb + OFF_S + (uint32_t)(c >> 1) * kBlock + swz(yrow, (uint32_t)((c & 1) * 4 + j)),
-                   pack8(reinterpret_cast<const float *>(v) + 8 * j, 1.f));
-      }
-      if (!last) {
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        if (!only) ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(bar(BAR_SREAD));
-          if (!only) ptx::mbar_arrive(bar(BAR_S));
-        }
-      }
-      if (mark_in) {
-#pragma unroll
-        for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-        if (lane == 0) r.mark_dots[mu * kMarkDots + (warp - kState0)] = dot;
-      }
-      if (last) break;
-    }
-  } else {
-    // ---------------------------------------------------------------- w o Y: warp -> 32 y columns, half the tokens
-    const int wq = warp & 3, half = (warp - kWeigh0) >> 2, id = tid - 32 * kWeigh0;
-    const uint32_t quad = tm + ((uint32_t)(wq * 32) << 16);
     // this lane's row of the four matrices (8 columns x 8 tokens) of 16 columns and 16 tokens
     const int row = ((lane >> 4) << 3) | (lane & 7);
     const uint32_t chunk = (uint32_t)(wq & 1) * 4u + (uint32_t)(lane >> 3 & 1);
     const uint32_t mine = (uint32_t)(wq >> 1) * kBlock;
-    bool ok = true;
-    for (int k = 0; k < nch && ok; ++k) {
-      const int s = k & 1, rows = rows_of(k);
-      const uint32_t par = (uint32_t)(k >> 1), y = sb + OFF_Y + (uint32_t)s * kTile;
-      if (!wait_warp(BAR_DEC + s, par) || !wait_warp(BAR_Y + s, par)) break;
-      if (rows < C) {
-        // rows behind the sequence meet zero weights, which a NaN would outlive
-        if (!wait_warp(BAR_Z + s, par)) break;
-        for (int t = id >> 4; t < C; t += 16)
-          if (t >= rows) {
-            const uint32_t to = y + (uint32_t)(id >> 3 & 1) * kBlock + swz(t, (uint32_t)(id & 7));
-            sts_v4(to, make_uint4(0u, 0u, 0u, 0u));
-            sts_v4(to + (OFF_Z - OFF_Y), make_uint4(0u, 0u, 0u, 0u));
-          }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(BAR_CLEAN));
-        if (!wait_warp(BAR_CLEAN, 0u)) break;  // other warps' rows are read too
-      }
-      // slices in the order of the walk; two tokens to a word, transposed into tensor memory
+    // slices first .. last - 1 (in the order of the walk) of chunk k's w o Y, two tokens to a word,
+    // transposed into tensor memory
+    auto weigh_slices = [&](int k, int first, int last) {
+      const int s = k & 1;
+      const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile;
 #pragma unroll 1
-      for (int i = 0; i < SLICES && ok; ++i) {
+      for (int i = first; i < last; ++i) {
         const int n = SLICES * k + i, slot = n & 1, t0 = (BACK ? i : SLICES - 1 - i) * SLICE + half * (SLICE / 2);
-        if (n >= 2) ok = wait_warp(BAR_EMPTY + slot, (uint32_t)(n >> 1) + 1u);
-        if (!ok) break;
+        if (n >= 2 && !wait_warp(BAR_EMPTY + slot, (uint32_t)(n >> 1) + 1u)) return false;
         ptx::tc_fence_after();
 #pragma unroll 1
         for (int t = 0; t < SLICE / 2; t += 16) {
@@ -808,6 +665,148 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(BAR_FULL + slot));
       }
+      return true;
+    };
+    const float *start = nullptr;
+    float *dst = nullptr;
+    bool flip_start = false, flip_dst = false;
+    if (only) {
+      dst = r.piece_state + (size_t)unit * D * D;
+    } else {
+      if (r.piece_state && pc.count > 1) {
+        start = r.piece_state + (size_t)unit * D * D;
+      } else if (r.start) {
+        start = r.start + ((size_t)pc.n * H + h) * D * D;
+        flip_start = r.start_t;
+      }
+      if (r.fin && pc.s == (BACK ? 0 : pc.count - 1)) {
+        dst = r.fin + ((size_t)pc.n * H + h) * D * D;
+        flip_dst = r.fin_t;
+      }
+    }
+#pragma unroll 1
+    for (int c = 4 * half; c < 4 * half + 4; ++c) {
+      uint32_t v[16];
+      if (start) {
+        load_state(start, flip_start, c * 16, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = 0u;
+      }
+      __syncwarp();
+      ptx::tmem_st16(quad + TM_S + c * 16, v);
+    }
+    ptx::tmem_wait_st();
+    // marks of this thread's part of the state behind group `g` of chunks
+    auto mark_unit = [&](int g) { return (size_t)mark_slot(unit / H, pc.t0 + g * kGroup * C) * H + h; };
+    auto ends_group = [&](int no) { return (no + 1) % kGroup == 0 || no == nch - 1; };
+    for (int k = 0; k <= nch; ++k) {
+      const int s = k & 1;
+      const uint32_t par = (uint32_t)(k >> 1);
+      const bool last = k == nch;
+      // the state before the k-th chunk walked: its copy for X S, and scaled back where due
+      // the first slice, while the last update still runs
+      if (!last) {
+        const int rows = rows_of(k);
+        const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile;
+        if (!wait_warp(BAR_DEC + s, par) || !wait_warp(BAR_Y + s, par)) break;
+        if (rows < C) {
+          // rows behind the sequence meet zero weights, which a NaN would outlive
+          if (!wait_warp(BAR_Z + s, par)) break;
+          for (int t = stid >> 4; t < C; t += 16)
+            if (t >= rows) {
+              const uint32_t to = y + (uint32_t)(stid >> 3 & 1) * kBlock + swz(t, (uint32_t)(stid & 7));
+              sts_v4(to, make_uint4(0u, 0u, 0u, 0u));
+              sts_v4(to + (OFF_Z - OFF_Y), make_uint4(0u, 0u, 0u, 0u));
+            }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(BAR_CLEAN));
+          if (!wait_warp(BAR_CLEAN, 0u)) break;  // other warps' rows are read too
+        }
+        if (!weigh_slices(k, 0, 1)) break;
+      } else if (!wait_warp(BAR_DEC + s, par)) {
+        break;
+      }
+      const uint32_t gs = dec + DEC_W + (uint32_t)s * DEC_STAGE + DEC_G;
+      const float behind = lds_f32(gs), back = last ? 1.f : lds_f32(gs + 4);
+      const float2 behind2 = make_float2(behind, behind);
+      if (k && !wait_warp(BAR_U, (uint32_t)k + 1u)) break;
+      ptx::tc_fence_after();
+      const float *mark_in = nullptr;
+      float *mark_out = nullptr;
+      size_t mu = 0;
+      if (r.marks && !only) {
+        const int no = chunk_no(k);  // forward: the group in front of chunk k is done; backward: k's begins
+        if (BACK && !last && ends_group(no)) {
+          mu = mark_unit(no / kGroup);
+          mark_in = r.marks + mu * (D * D) + 4 * yrow;
+        }
+        if (!BACK && k && ends_group(k - 1)) mark_out = r.marks + mark_unit((k - 1) / kGroup) * (D * D) + 4 * yrow;
+        if (BACK && !last && no % kGroup == 1 && no > kGroup) {  // the next group's mark, two chunks ahead
+          const char *next = reinterpret_cast<const char *>(r.marks + mark_unit(no / kGroup - 1) * (D * D)) + stid * 128;
+          prefetch_l2(next);
+          prefetch_l2(next + 32768);
+        }
+      }
+      float dot = 0.f;
+      uint32_t copy[32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 4 * half + i;  // 16 columns each
+        uint32_t v[16];
+        ptx::tmem_ld16(quad + TM_S + c * 16, v);
+        ptx::tmem_wait_ld();
+        if (back != 1.f) {
+          uint32_t u[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(back * __uint_as_float(v[j]));
+          ptx::tmem_st16(quad + TM_S + c * 16, u);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 w = mul2(behind2, pair(v[2 * j], v[2 * j + 1]));
+          v[2 * j] = __float_as_uint(w.x);
+          v[2 * j + 1] = __float_as_uint(w.y);
+          copy[8 * i + j] = pack_bf16x2(w.x, w.y);
+        }
+        if (mark_in) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 w = *reinterpret_cast<const float4 *>(mark_in + (c * 4 + j) * 512);
+            dot = fmaf(w.x, __uint_as_float(v[4 * j]), fmaf(w.y, __uint_as_float(v[4 * j + 1]),
+                  fmaf(w.z, __uint_as_float(v[4 * j + 2]), fmaf(w.w, __uint_as_float(v[4 * j + 3]), dot))));
+          }
+        }
+        if (mark_out) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(mark_out + (c * 4 + j) * 512) =
+                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+        if (last && dst) store_state(dst, flip_dst, c * 16, v);
+      }
+      if (last) break;
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(BAR_SREAD));
+      if (!only) {
+        if (k && !wait_warp(BAR_XS, (uint32_t)k + 1u)) break;  // the last copy has been read
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          sts_v4(sb + OFF_S + half * kBlock + swz(yrow, (uint32_t)j),
+                 make_uint4(copy[4 * j], copy[4 * j + 1], copy[4 * j + 2], copy[4 * j + 3]));
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_S));
+      }
+      if (mark_in) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+        if (lane == 0) r.mark_dots[mu * kMarkDots + (warp - kState0)] = dot;
+      }
+      if (!weigh_slices(k, 1, SLICES)) break;
       if (lane == 0) ptx::mbar_arrive(bar(BAR_WFREE + s));
     }
   }
@@ -878,7 +877,7 @@ cudaError_t launch_run_tc(const Run &r, int terms, int32_t *status, cudaStream_t
   if (T > 0) {
     bool ok = make_row_tile_map(&P.tm_y, r.y, T, r.Hy, C) && make_row_tile_map(&P.tm_z, r.z, T, r.Hz, C);
     if (ok && !r.state_only) ok = make_row_tile_map(&P.tm_x, r.x, T, r.Hx, C);
-    if (ok && !r.state_only && !r.out_f32) ok = make_row_tile_map(&P.tm_o, r.out, T, r.cut.H, C);
+    if (ok && !r.state_only && !r.out_f32) ok = make_row_tile_map(&P.tm_o, r.out, T, r.cut.H, 32);
     if (!ok) return cudaErrorInvalidValue;
   }
   uint64_t hook_ns = 0;
