@@ -29,6 +29,15 @@ __device__ __forceinline__ int code_of(float x, float inv, uint32_t byte) {
   const int lim = byte >= 249u ? 63 : 127;
   return max(-lim, min(lim, __float2int_rn(x * inv)));
 }
+// Four codes.  x / 2^e is exact and at most 127, so adding 1.5 * 2^23 leaves it, rounded half to even,
+// in the low bits: one operation where a conversion and two clamps took the save past its memory time.
+__device__ __forceinline__ uint32_t codes4(const float *f, float inv) {
+  constexpr float kShift = 12582912.f;
+  uint32_t t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = __float_as_uint(fmaf(f[i], inv, kShift));
+  return __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+}
 // 2^e; 255 gives +inf, and 0 * inf = NaN is what such a block restores to.
 __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
@@ -56,34 +65,54 @@ __device__ __forceinline__ void load8<float>(const float *p, float (&f)[8]) {
 
 // cols % 8 == 0: a thread holds 8 values (one 16-byte load in bf16) and 4 lanes a block.  The unit
 // of work is a (row, block) pair of 4 lanes, so a row's last block may have fewer than 4 live lanes.
-template <typename T>
+// FLAT: cols % 32 == 0, so the rows need not be told apart and the 64-bit divisions, which took
+// longer than the memory, fall away.
+// Streaming bounds it: a thread takes kUnits units a thread block's span apart and asks for all of
+// them before it uses the first, 16 KB (bf16) a thread block in flight.
+constexpr int kUnits = 4;
+template <typename T, bool FLAT>
 __global__ void __launch_bounds__(kThreads) save8_kernel(const T *__restrict__ x, int8_t *__restrict__ codes,
                                                          uint8_t *__restrict__ scales, int64_t rows, int cols,
                                                          int blocks) {
   const int64_t total = rows * blocks;
-  const int64_t at = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 2;
+  const int64_t first = (int64_t)blockIdx.x * (kThreads / 4 * kUnits) + (threadIdx.x >> 2);
   const int sub = threadIdx.x & 3;
-  if (at - (threadIdx.x >> 2 & 7) >= total) return;  // the whole warp is past the end
-  const int64_t row = at / blocks;
-  const int col = (int)(at - row * blocks) * 32 + sub * 8;
-  const bool live = at < total && col < cols;
-  float f[8];
-  uint32_t top = 0;
-  if (live) {
-    load8<T>(x + row * cols + col, f);
+  float f[kUnits][8];
+  int64_t from[kUnits];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, abs_bits(f[i]));
+  for (int u = 0; u < kUnits; ++u) {
+    const int64_t at = first + u * (kThreads / 4);
+    if constexpr (FLAT) {
+      from[u] = at < total ? at * 32 + sub * 8 : -1;
+    } else {
+      const int64_t row = at / blocks;
+      const int col = (int)(at - row * blocks) * 32 + sub * 8;
+      from[u] = at < total && col < cols ? row * cols + col : -1;
+    }
+    if (from[u] >= 0) load8<T>(x + from[u], f[u]);
   }
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  if (!live) return;
-  const uint32_t byte = scale_byte(top);
-  const float inv = inverse_scale(byte);
-  uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i >> 2] |= ((uint32_t)code_of(f[i], inv, byte) & 255u) << (8 * (i & 3));
-  *reinterpret_cast<uint2 *>(codes + row * cols + col) = make_uint2(w[0], w[1]);
-  if (sub == 0) scales[at] = (uint8_t)byte;
+  for (int u = 0; u < kUnits; ++u) {
+    uint32_t top = 0;
+    if (from[u] >= 0)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, abs_bits(f[u][i]));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if (from[u] < 0) continue;
+    const uint32_t byte = scale_byte(top);
+    const float inv = inverse_scale(byte);
+    uint32_t w[2] = {codes4(f[u], inv), codes4(f[u] + 4, inv)};
+    if (byte >= 249u) {  // near the end of fp32's range, or an infinity or a NaN
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if ((i & 3) == 0) w[i >> 2] = 0;
+        w[i >> 2] |= ((uint32_t)code_of(f[u][i], inv, byte) & 255u) << (8 * (i & 3));
+      }
+    }
+    *reinterpret_cast<uint2 *>(codes + from[u]) = make_uint2(w[0], w[1]);
+    if (sub == 0) scales[first + u * (kThreads / 4)] = (uint8_t)byte;
+  }
 }
 
 // Any cols: a warp per block, a lane per value.
@@ -103,29 +132,44 @@ __global__ void __launch_bounds__(kThreads) save1_kernel(const T *__restrict__ x
   if (lane == 0) scales[at] = (uint8_t)byte;
 }
 
-// cols % 8 == 0: a thread restores 8 values.
-template <typename T>
+// cols % 8 == 0: a thread restores kUnits times 8 values, all asked for before the first is used.
+template <typename T, bool FLAT>
 __global__ void __launch_bounds__(kThreads) restore8_kernel(const int8_t *__restrict__ codes,
                                                             const uint8_t *__restrict__ scales, T *__restrict__ x,
                                                             int64_t rows, int cols, int blocks) {
   const int per_row = cols >> 3;
-  const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (at >= rows * per_row) return;
-  const int64_t row = at / per_row;
-  const int c8 = (int)(at - row * per_row);
-  const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(codes + at * 8));
-  const float s = scale_value(scales[row * blocks + (c8 >> 2)]);
-  float f[8];
+  const int64_t total = rows * per_row, first = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+  uint2 code[kUnits];
+  uint32_t byte[kUnits];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = (float)(int8_t)((i < 4 ? u.x : u.y) >> (8 * (i & 3))) * s;
-  if constexpr (sizeof(T) == 2) {
-    const uint4 o = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                               pack_bf16x2(f[6], f[7]));
-    *reinterpret_cast<uint4 *>(x + at * 8) = o;
-  } else {
-    float4 *o = reinterpret_cast<float4 *>(x + at * 8);
-    o[0] = make_float4(f[0], f[1], f[2], f[3]);
-    o[1] = make_float4(f[4], f[5], f[6], f[7]);
+  for (int u = 0; u < kUnits; ++u) {
+    const int64_t at = first + u * kThreads;
+    if (at >= total) break;
+    code[u] = __ldcs(reinterpret_cast<const uint2 *>(codes + at * 8));
+    if constexpr (FLAT) {
+      byte[u] = scales[at >> 2];
+    } else {
+      const int64_t row = at / per_row;
+      byte[u] = scales[row * blocks + ((int)(at - row * per_row) >> 2)];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const int64_t at = first + u * kThreads;
+    if (at >= total) break;
+    const float s = scale_value(byte[u]);
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (float)(int8_t)((i < 4 ? code[u].x : code[u].y) >> (8 * (i & 3))) * s;
+    if constexpr (sizeof(T) == 2) {
+      const uint4 o = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                 pack_bf16x2(f[6], f[7]));
+      *reinterpret_cast<uint4 *>(x + at * 8) = o;
+    } else {
+      float4 *o = reinterpret_cast<float4 *>(x + at * 8);
+      o[0] = make_float4(f[0], f[1], f[2], f[3]);
+      o[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
   }
 }
 
@@ -144,9 +188,11 @@ template <typename T>
 cudaError_t save_t(const T *x, int8_t *codes, uint8_t *scales, int64_t rows, int cols, cudaStream_t s) {
   const int blocks = (cols + 31) / 32;
   const int64_t units = rows * blocks;
-  if (cols % 8 == 0)
-    save8_kernel<T><<<(unsigned)((units * 4 + kThreads - 1) / kThreads), kThreads, 0, s>>>(x, codes, scales, rows, cols,
-                                                                                            blocks);
+  const unsigned grid = (unsigned)((units * 4 + kThreads * kUnits - 1) / (kThreads * kUnits));
+  if (cols % 32 == 0)
+    save8_kernel<T, true><<<grid, kThreads, 0, s>>>(x, codes, scales, rows, cols, blocks);
+  else if (cols % 8 == 0)
+    save8_kernel<T, false><<<grid, kThreads, 0, s>>>(x, codes, scales, rows, cols, blocks);
   else
     save1_kernel<T><<<(unsigned)((units * 32 + kThreads - 1) / kThreads), kThreads, 0, s>>>(x, codes, scales, rows,
                                                                                              cols, blocks);
@@ -157,9 +203,12 @@ template <typename T>
 cudaError_t restore_t(const int8_t *codes, const uint8_t *scales, T *x, int64_t rows, int cols, cudaStream_t s) {
   const int blocks = (cols + 31) / 32;
   const int64_t n = cols % 8 == 0 ? rows * cols / 8 : rows * cols;
-  const unsigned grid = (unsigned)((n + kThreads - 1) / kThreads);
-  if (cols % 8 == 0)
-    restore8_kernel<T><<<grid, kThreads, 0, s>>>(codes, scales, x, rows, cols, blocks);
+  const int64_t each = cols % 8 == 0 ? kThreads * kUnits : kThreads;
+  const unsigned grid = (unsigned)((n + each - 1) / each);
+  if (cols % 32 == 0)
+    restore8_kernel<T, true><<<grid, kThreads, 0, s>>>(codes, scales, x, rows, cols, blocks);
+  else if (cols % 8 == 0)
+    restore8_kernel<T, false><<<grid, kThreads, 0, s>>>(codes, scales, x, rows, cols, blocks);
   else
     restore1_kernel<T><<<grid, kThreads, 0, s>>>(codes, scales, x, rows, cols, blocks);
   return cudaGetLastError();

@@ -1,6 +1,8 @@
 // linattn.cu -- linear attention with a decay per head on the CUDA cores: the run for fp32 inputs
 // and for head sizes the tensor-core run does not take, the single-token step, and the helpers
 // both runs share (the cut plan, the join of the pieces, the gradient of log_a, head sums).
+#include <type_traits>
+
 #include "linattn.cuh"
 
 namespace gdn2 {
@@ -68,7 +70,9 @@ __global__ void __launch_bounds__(256) join_kernel(Run r) {
       const int s = r.back ? count - 1 - (i0 + j) : i0 + j;
       if (i0 + j < count - 1) {
         got[j] = r.piece_state[(unit0 + (int64_t)s * H) * size + e];
-        g[j] = (float)exp(r.piece_log[unit0 + (int64_t)s * H]);
+        const double l = r.piece_log[unit0 + (int64_t)s * H];
+        const float hi = (float)l;
+        g[j] = expf(hi) * (1.f + (float)(l - (double)hi));
       }
     }
 #pragma unroll
@@ -319,17 +323,32 @@ __global__ void __launch_bounds__(kScan) dlog_kernel(const float *dq, int nq, co
 }
 
 // ---------------------------------------------------------------- heads that share q and k
-template <typename T>
+// A thread sums VEC columns: 16-byte loads of the parts, which are most of what it moves.
+template <typename T, int VEC>
 __global__ void __launch_bounds__(256) group_sum_kernel(const float *part, T *out, int64_t total, int share, int d,
                                                         const int32_t *cu, int n_seqs, int Hg) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // over [T, Hg, d]
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;  // over [T, Hg, d]
   if (i >= total) return;
   const int64_t row = i / d, t = row / Hg;
   if (cu && (t < cu[0] || t >= cu[n_seqs])) return;  // outside every sequence: left as it was
   const float *p = part + row * share * d + (i - row * d);
-  float v = 0.f;
-  for (int s = 0; s < share; ++s) v += p[(int64_t)s * d];
-  out[i] = from_f32<T>(v);
+  float v[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) v[j] = 0.f;
+  for (int s = 0; s < share; ++s) {
+    if constexpr (VEC == 4) {
+      const float4 f = __ldcs(reinterpret_cast<const float4 *>(p + (int64_t)s * d));
+      v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+    } else {
+      v[0] += p[(int64_t)s * d];
+    }
+  }
+  if constexpr (VEC == 4 && sizeof(T) == 2)
+    *reinterpret_cast<uint2 *>(out + i) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  else if constexpr (VEC == 4)
+    *reinterpret_cast<float4 *>(out + i) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    out[i] = from_f32<T>(v[0]);
 }
 
 // ---------------------------------------------------------------- single-token step
@@ -454,15 +473,17 @@ cudaError_t launch_dlog_simt(const float *dots_q, int nq, const float *dots_k, i
 
 cudaError_t launch_group_sum(const float *part, void *out, const Cut &c, int Hg, int d, int dtype, cudaStream_t s) {
   const int64_t total = (int64_t)c.t_total * Hg * d;
-  const int H = c.H;
+  const int share = c.H / Hg;
   if (total == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)((total + 255) / 256);
-  if (dtype == GDN2_BF16)
-    group_sum_kernel<<<grid, 256, 0, s>>>(part, static_cast<__nv_bfloat16 *>(out), total, H / Hg, d, c.cu,
-                                            c.n_seqs, Hg);
-  else
-    group_sum_kernel<<<grid, 256, 0, s>>>(part, static_cast<float *>(out), total, H / Hg, d, c.cu,
-                                            c.n_seqs, Hg);
+  const int vec = d % 4 == 0 ? 4 : 1;
+  const unsigned grid = (unsigned)((total + 256 * vec - 1) / (256 * vec));
+  auto go = [&](auto *o) {
+    using T = std::remove_pointer_t<decltype(o)>;
+    if (vec == 4) group_sum_kernel<T, 4><<<grid, 256, 0, s>>>(part, o, total, share, d, c.cu, c.n_seqs, Hg);
+    else group_sum_kernel<T, 1><<<grid, 256, 0, s>>>(part, o, total, share, d, c.cu, c.n_seqs, Hg);
+  };
+  if (dtype == GDN2_BF16) go(static_cast<__nv_bfloat16 *>(out));
+  else go(static_cast<float *>(out));
   return cudaGetLastError();
 }
 

@@ -24,6 +24,7 @@
 // (every term written, and read with Z) that memory's 128 bytes a cycle were short, and they still
 // are what the CUDA cores wait for while products run.  X has one tile, Y and Z two stages.  The
 // loops stay rolled: unrolled, the roles together ran out of the instruction cache.
+#include <atomic>
 #include <cstring>
 
 #include "linattn.cuh"
@@ -859,8 +860,15 @@ __global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *d
 template <bool BACK, int NT>
 cudaError_t launch_t(const TcRun &P, cudaStream_t s) {
   auto kern = run_tc_kernel<BACK, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  static std::atomic<uint64_t> ready{0};  // a bit for each device that has been told
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   kern<<<(unsigned)((int64_t)P.r.cut.n_pieces * P.r.cut.H), kThreads, kSmemBytes, s>>>(P);
   return cudaGetLastError();
 }

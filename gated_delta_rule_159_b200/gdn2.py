@@ -159,11 +159,12 @@ def _ptr(t: Optional[torch.Tensor]):
         raise ValueError("gdn2 tensors must live on a CUDA device")
     if not t.is_contiguous():
         raise ValueError("gdn2 tensors must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device) -> int:
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _check(rc: int):
