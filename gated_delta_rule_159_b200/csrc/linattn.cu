@@ -85,55 +85,66 @@ __global__ void __launch_bounds__(256) join_kernel(Run r) {
   }
 }
 
-// ---------------------------------------------------------------- the run, token by token in fp32
-// The columns of the state do not mix: a warp owns 16 of them and all dy rows, 8 lanes x R rows
-// by 4 lanes x 4 columns, in registers.  Per token a lane updates R x 4 elements and multiplies
-// them by x; four shuffles sum each column over its 8 lanes.  4 dy dz FMA-class operations a token
-// on the CUDA cores bound it (and the chain of tokens, where there are few units).
-constexpr int TB = 32;     // tokens staged at a time
-constexpr int WARPS = 2;   // warps of a block
-constexpr int COLS = 16 * WARPS;
+// ---------------------------------------------------------------- the run in fp32
+// Tiles of 32 tokens: G = X Y^T, P = G o D, out = P Z + f o (X S), S <- g S + (w o Y)^T Z, all in fp32 on
+// the CUDA cores.  A block takes a (piece, head) and 64 of the state's columns, which do not mix.
+// Per tile and token a block does 64 (2 dy + 64) + 32 dy multiply-adds; shared memory, read by 16
+// bytes, and they bound it about alike (token by token, a chain of shuffles and dependent sums
+// for each, it took 54 us for 32 tokens).  The decays are summed in whole numbers of 2^-32: a tile may
+// hold resets beside weak decays, and differences of their sums have to stay exact.
+constexpr int TB = 32;
+constexpr int COLS = 64;
+constexpr int kRunThreads = 256;
 
-// A fixed decay's rounding is the same at every token, and a state that keeps n tokens would be off
-// by n of them: the product with the state takes the decay in two parts.
-__device__ __forceinline__ float2 split_exp(float la) {
-  const double a = exp((double)la);
-  const float hi = (float)a;
-  return make_float2(hi, (float)(a - (double)hi));
+struct RunSmem {
+  int ys;  // floats a row of X and Y (4 banks further on each row)
+  int off_y, off_z, off_s, off_m, total;
+  __host__ __device__ RunSmem(int dy, bool dots) {
+    const int dyp = (dy + 7) / 8 * 8;
+    ys = dyp + 4;
+    off_y = TB * ys;
+    off_z = off_y + TB * ys;
+    off_s = off_z + TB * COLS;
+    off_m = off_s + dyp * COLS;
+    total = off_m + (dots ? TB * COLS : 0);
+  }
+};
+
+__device__ __forceinline__ float4 ld4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float part4(const float4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ void fma4(float (&acc)[4], float a, const float4 &b) {
+  acc[0] = fmaf(a, b.x, acc[0]);
+  acc[1] = fmaf(a, b.y, acc[1]);
+  acc[2] = fmaf(a, b.z, acc[2]);
+  acc[3] = fmaf(a, b.w, acc[3]);
 }
 
-template <int R>
-__device__ __forceinline__ int row_of(int rg, int r) {
-  constexpr int V = R < 4 ? R : 4;
-  return (r / V) * (8 * V) + rg * V + r % V;
-}
-
-template <typename T, int R>
-__global__ void __launch_bounds__(32 * WARPS) run_kernel(Run p) {
-  constexpr int DP = 8 * R;
-  constexpr int V = R < 4 ? R : 4;
-  __shared__ __align__(16) float xs[TB][DP];
-  __shared__ __align__(16) float ys[TB][DP];
-  __shared__ __align__(16) float zs[TB][COLS];
-  __shared__ float ms[TB][COLS];
-  __shared__ float2 decay[TB];  // e^{log_a} as a sum of two floats
-  __shared__ float raw[TB];
-  __shared__ float part[TB][WARPS];
-  const int H = p.cut.H, unit = blockIdx.x, h = unit % H;
+// ROWS rows of out a thread: 1 where the slice has at most 32 columns, else 2.
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(kRunThreads) run_kernel(Run p) {
+  extern __shared__ __align__(16) float sm[];
+  __shared__ __align__(16) float ps[TB][TB + 4];
+  __shared__ float dot[TB][COLS / 4 + 1];
+  __shared__ long long cum[TB];  // sums of log_a from the tile's first token, inclusive
+  __shared__ float fs[TB], ws[TB];
+  const int H = p.cut.H, unit = blockIdx.x, h = unit % H, tid = threadIdx.x;
   Piece pc;
   if (!find_piece(p.cut, unit / H, &pc)) return;
   if (p.state_only && (pc.count < 2 || pc.s == (p.back ? 0 : pc.count - 1))) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rg = lane & 7, cg = lane >> 3;
-  const int col0 = blockIdx.y * COLS, wcol = warp * 16 + cg * 4;
+  const RunSmem L(p.dy, p.m != nullptr);
+  float *xs = sm, *yv = sm + L.off_y, *zs = sm + L.off_z, *ss = sm + L.off_s, *ms = sm + L.off_m;
+  const int dyp = L.ys - 4, col0 = blockIdx.y * COLS, width = min(COLS, p.dz - col0), groups = (width + 3) / 4;
   const T *x = static_cast<const T *>(p.x), *y = static_cast<const T *>(p.y), *z = static_cast<const T *>(p.z);
   const T *m = static_cast<const T *>(p.m);
   const int hx = h / (H / p.Hx), hy = h / (H / p.Hy), hz = h / (H / p.Hz), hm = p.m ? h / (H / p.Hm) : 0;
 
-  float S[R][4];
+  // this thread's part of the state: 8 rows by 4 columns
+  const int cg = tid % groups, yg = tid / groups;
+  const bool owner = yg * 8 < p.dy;
+  float S[8][4];
+  const size_t state = (size_t)p.dy * p.dz;
   const float *start = nullptr;
   bool st = false;
-  const size_t state = (size_t)p.dy * p.dz;
   if (!p.state_only) {
     if (p.piece_state && pc.count > 1) {
       start = p.piece_state + (size_t)unit * state;
@@ -143,135 +154,200 @@ __global__ void __launch_bounds__(32 * WARPS) run_kernel(Run p) {
     }
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int r = 0; r < 8; ++r)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int row = row_of<R>(rg, r), col = col0 + wcol + c;
-      S[r][c] = start && row < p.dy && col < p.dz ? start[st ? (size_t)col * p.dy + row : (size_t)row * p.dz + col]
-                                                  : 0.f;
+      const int row = yg * 8 + r, col = col0 + cg * 4 + c;
+      S[r][c] = start && row < p.dy && col < p.dz ? start[st ? (size_t)col * p.dy + row : (size_t)row * p.dz + col] : 0.f;
     }
 
   const float fixed = p.per_head ? static_cast<const float *>(p.log_a)[h] : 0.f;
-  double logs = 0.0;
+  long long logs = 0;
   const int tiles = (pc.len + TB - 1) / TB;
-  float2 carry = make_float2(1.f, 0.f);  // backward: the decay of the token after this one, applied before its update
   for (int it = 0; it < tiles; ++it) {
-    const int tile = p.back ? tiles - 1 - it : it;
-    const int t0 = tile * TB, cnt = min(TB, pc.len - t0);
+    const int t0 = (p.back ? tiles - 1 - it : it) * TB, cnt = min(TB, pc.len - t0);
+    const size_t tok0 = (size_t)(pc.t0 + t0);
     __syncthreads();
-    for (int i = tid; i < cnt * DP; i += 32 * WARPS) {
-      const int t = i / DP, c = i % DP;
-      const bool in = c < p.dy;
-      const size_t tok = (size_t)(pc.t0 + t0 + t);
-      if (!p.state_only) xs[t][c] = in ? to_f32<T>(x[(tok * p.Hx + hx) * p.dy + c]) : 0.f;
-      ys[t][c] = in ? to_f32<T>(y[(tok * p.Hy + hy) * p.dy + c]) : 0.f;
-    }
-    for (int i = tid; i < cnt * COLS; i += 32 * WARPS) {
-      const int t = i / COLS, c = i % COLS;
-      const bool in = col0 + c < p.dz;
-      const size_t tok = (size_t)(pc.t0 + t0 + t);
-      zs[t][c] = in ? to_f32<T>(z[(tok * p.Hz + hz) * p.dz + col0 + c]) : 0.f;
-      if (m) ms[t][c] = in ? to_f32<T>(m[(tok * p.Hm + hm) * p.dz + col0 + c]) : 0.f;
-    }
-    for (int t = tid; t < cnt; t += 32 * WARPS) {
-      const float la = p.per_head ? fixed
-                                  : to_f32<T>(static_cast<const T *>(p.log_a)[(size_t)(pc.t0 + t0 + t) * H + h]);
-      raw[t] = fmaxf(la, kMinLog);
-      decay[t] = split_exp(raw[t]);
-    }
-    __syncthreads();
-    if (p.state_only && blockIdx.y == 0 && tid == 0)
-      for (int t = 0; t < cnt; ++t) logs += (double)raw[t];
-    for (int i = 0; i < cnt; ++i) {
-      const int t = p.back ? cnt - 1 - i : i;
-      const float2 mine = decay[t];
-      const float2 a = p.back ? carry : mine;
-      carry = mine;
-      const float4 z4 = *reinterpret_cast<const float4 *>(&zs[t][wcol]);
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    {  // 8 threads a token, every eighth column each: all of a round's loads before the first store
+      const int t = tid >> 3, l = tid & 7;
+      const bool in = t < cnt;
+      const T *px = p.state_only ? nullptr : x + ((tok0 + t) * p.Hx + hx) * p.dy;
+      const T *py = y + ((tok0 + t) * p.Hy + hy) * p.dy, *pz = z + ((tok0 + t) * p.Hz + hz) * p.dz + col0;
+      const T *pm = m ? m + ((tok0 + t) * p.Hm + hm) * p.dz + col0 : nullptr;
+      for (int c0 = l; c0 < dyp || c0 < COLS; c0 += 64) {
+        float vx[8], vy[8], vz[8], vm[8];
 #pragma unroll
-      for (int rv = 0; rv < R / V; ++rv) {
-        float yv[V], xv[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          yv[j] = ys[t][rv * 8 * V + rg * V + j];
-          xv[j] = p.state_only ? 0.f : xs[t][rv * 8 * V + rg * V + j];
+        for (int j = 0; j < 8; ++j) {
+          const int c = c0 + 8 * j;
+          vx[j] = in && px && c < p.dy ? to_f32<T>(px[c]) : 0.f;
+          vy[j] = in && c < p.dy ? to_f32<T>(py[c]) : 0.f;
+          vz[j] = in && c < width ? to_f32<T>(pz[c]) : 0.f;
+          vm[j] = in && pm && c < width ? to_f32<T>(pm[c]) : 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          float(&s)[4] = S[rv * V + j];
-          s[0] = fmaf(a.x, s[0], fmaf(a.y, s[0], yv[j] * z4.x));
-          s[1] = fmaf(a.x, s[1], fmaf(a.y, s[1], yv[j] * z4.y));
-          s[2] = fmaf(a.x, s[2], fmaf(a.y, s[2], yv[j] * z4.z));
-          s[3] = fmaf(a.x, s[3], fmaf(a.y, s[3], yv[j] * z4.w));
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[c] = fmaf(xv[j], s[c], acc[c]);
+        for (int j = 0; j < 8; ++j) {
+          const int c = c0 + 8 * j;
+          if (c < dyp) {
+            xs[t * L.ys + c] = vx[j];
+            yv[t * L.ys + c] = vy[j];
+          }
+          if (c < COLS) {
+            zs[t * COLS + c] = vz[j];
+            if (m) ms[t * COLS + c] = vm[j];
+          }
         }
       }
-      if (p.state_only) continue;
-      // sum over the 8 row lanes: each step halves the columns a lane keeps, the last joins halves
-      const bool b0 = rg & 1, b1 = rg & 2;
-      float k0 = b0 ? acc[2] : acc[0], k1 = b0 ? acc[3] : acc[1];
-      k0 += __shfl_xor_sync(0xffffffffu, b0 ? acc[0] : acc[2], 1);
-      k1 += __shfl_xor_sync(0xffffffffu, b0 ? acc[1] : acc[3], 1);
-      float o = b1 ? k1 : k0;
-      o += __shfl_xor_sync(0xffffffffu, b1 ? k0 : k1, 2);
-      o += __shfl_xor_sync(0xffffffffu, o, 4);
-      const int c = wcol + (b0 ? 2 : 0) + (b1 ? 1 : 0), col = col0 + c;
-      if (rg < 4 && col < p.dz) {
-        const size_t at = ((size_t)(pc.t0 + t0 + t) * H + h) * p.dz + col;
-        if (p.out_f32) static_cast<float *>(p.out)[at] = o;
-        else static_cast<T *>(p.out)[at] = from_f32<T>(o);
+    }
+    if (owner && !p.state_only)
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        *reinterpret_cast<float4 *>(ss + (yg * 8 + r) * COLS + cg * 4) = make_float4(S[r][0], S[r][1], S[r][2], S[r][3]);
+    if (tid < TB) {
+      float la = 0.f;
+      if (tid < cnt) la = p.per_head ? fixed : to_f32<T>(static_cast<const T *>(p.log_a)[(tok0 + tid) * H + h]);
+      long long sum = __float2ll_rn(fmaxf(la, kMinLog) * 0x1p32f);
+#pragma unroll
+      for (int d = 1; d < TB; d <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, sum, d);
+        if (tid >= d) sum += up;
+      }
+      const long long all = __shfl_sync(0xffffffffu, sum, TB - 1);
+      cum[tid] = sum;
+      const float here = expf(__ll2float_rn(sum) * 0x1p-32f), rest = expf(__ll2float_rn(all - sum) * 0x1p-32f);
+      fs[tid] = p.back ? rest : here;
+      ws[tid] = p.back ? here : rest;
+      logs += all;
+    }
+    __syncthreads();
+    const float g = expf(__ll2float_rn(cum[TB - 1]) * 0x1p-32f);
+
+    if (!p.state_only) {
+      {  // P: row i, columns j = c + 8 q
+        const int i = tid >> 3, c = tid & 7;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int k = 0; k < dyp; k += 4) {
+          const float4 a = ld4(xs + i * L.ys + k);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 b = ld4(yv + (c + 8 * q) * L.ys + k);
+            acc[q] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, acc[q]))));
+          }
+        }
+        const long long mine = cum[i];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int j = c + 8 * q;
+          const bool in = (p.back ? j >= i : j <= i) && j < cnt;
+          const long long d = p.back ? cum[j] - mine : mine - cum[j];
+          ps[i][j] = in ? acc[q] * expf(__ll2float_rn(d) * 0x1p-32f) : 0.f;
+        }
+      }
+      __syncthreads();
+      const int rg = tid / groups;  // rows rg * ROWS ..
+      if (rg * ROWS < TB) {
+        float acc[ROWS][4];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
+#pragma unroll 2
+        for (int k = 0; k < dyp; k += 4) {
+          float4 a[ROWS];
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) a[r] = ld4(xs + (rg * ROWS + r) * L.ys + k);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 b = ld4(ss + (k + q) * COLS + cg * 4);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) fma4(acc[r], part4(a[r], q), b);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          const float f = fs[rg * ROWS + r];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[r][c] *= f;
+        }
+#pragma unroll 2
+        for (int k = 0; k < TB; k += 4) {
+          float4 a[ROWS];
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) a[r] = ld4(&ps[rg * ROWS + r][k]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 b = ld4(zs + (k + q) * COLS + cg * 4);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) fma4(acc[r], part4(a[r], q), b);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          const int t = rg * ROWS + r;
+          if (m) {
+            const float4 b = ld4(ms + t * COLS + cg * 4);
+            dot[t][cg] = fmaf(acc[r][0], b.x, fmaf(acc[r][1], b.y, fmaf(acc[r][2], b.z, acc[r][3] * b.w)));
+          }
+          if (t >= cnt) continue;
+          const size_t at = ((tok0 + t) * H + h) * p.dz + col0 + cg * 4;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (cg * 4 + c < width) {
+              if (p.out_f32) static_cast<float *>(p.out)[at + c] = acc[r][c];
+              else static_cast<T *>(p.out)[at + c] = from_f32<T>(acc[r][c]);
+            }
+        }
       }
       if (m) {
-        float d = rg < 4 ? o * ms[t][c] : 0.f;
-#pragma unroll
-        for (int b = 16; b; b >>= 1) d += __shfl_xor_sync(0xffffffffu, d, b);
-        if (lane == 0) part[t][warp] = d;
+        __syncthreads();
+        if (tid < cnt) {
+          float d = 0.f;
+          for (int c = 0; c < groups; ++c) d += dot[tid][c];
+          p.dots[((size_t)blockIdx.y * p.cut.t_total + tok0 + tid) * H + h] = d;
+        }
       }
     }
-    if (m && !p.state_only) {
-      __syncthreads();
-      for (int t = tid; t < cnt; t += 32 * WARPS) {
-        float d = 0.f;
-        for (int w = 0; w < WARPS; ++w) d += part[t][w];
-        p.dots[((size_t)blockIdx.y * p.cut.t_total + (pc.t0 + t0 + t)) * H + h] = d;
+    if (owner) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) S[r][c] *= g;
+#pragma unroll 4
+      for (int t = 0; t < TB; ++t) {  // zeros behind the sequence
+        const float w = ws[t];
+        const float4 a = ld4(yv + t * L.ys + yg * 8), b = ld4(yv + t * L.ys + yg * 8 + 4), v = ld4(zs + t * COLS + cg * 4);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) fma4(S[r], w * part4(r < 4 ? a : b, r & 3), v);
       }
     }
   }
-  if (p.back)
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) S[r][c] = fmaf(carry.x, S[r][c], carry.y * S[r][c]);
 
   float *dst = nullptr;
   bool dt = false;
   if (p.state_only) {
     dst = p.piece_state + (size_t)unit * state;
-    if (blockIdx.y == 0 && tid == 0) p.piece_log[unit] = logs;
+    if (blockIdx.y == 0 && tid == 0) p.piece_log[unit] = (double)logs * 0x1p-32;
   } else if (p.fin && pc.s == (p.back ? 0 : pc.count - 1)) {
     dst = p.fin + ((size_t)pc.n * H + h) * state;
     dt = p.fin_t;
   }
-  if (!dst) return;
+  if (!dst || !owner) return;
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int r = 0; r < 8; ++r)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int row = row_of<R>(rg, r), col = col0 + wcol + c;
+      const int row = yg * 8 + r, col = col0 + cg * 4 + c;
       if (row < p.dy && col < p.dz) dst[dt ? (size_t)col * p.dy + row : (size_t)row * p.dz + col] = S[r][c];
     }
 }
 
-template <typename T>
+template <typename T, int ROWS>
 cudaError_t launch_run_t(const Run &r, cudaStream_t s) {
+  const int bytes = RunSmem(r.dy, r.m != nullptr).total * (int)sizeof(float);
+  const cudaError_t e = cudaFuncSetAttribute(run_kernel<T, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((int64_t)r.cut.n_pieces * r.cut.H), (unsigned)simt_slices(r.dz));
-  const int R = (r.dy + 7) / 8;
-  if (R <= 2) run_kernel<T, 2><<<grid, 32 * WARPS, 0, s>>>(r);
-  else if (R <= 4) run_kernel<T, 4><<<grid, 32 * WARPS, 0, s>>>(r);
-  else if (R <= 8) run_kernel<T, 8><<<grid, 32 * WARPS, 0, s>>>(r);
-  else run_kernel<T, 16><<<grid, 32 * WARPS, 0, s>>>(r);
+  run_kernel<T, ROWS><<<grid, kRunThreads, bytes, s>>>(r);
   return cudaGetLastError();
 }
 
@@ -352,6 +428,26 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const float *part, T *ou
 }
 
 // ---------------------------------------------------------------- single-token step
+// e^la as the sum of two floats: a fixed decay's rounding is the same at every token, and a state that
+// keeps n of them would be off by n.  la = n ln 2 + r (Cody and Waite's two-part ln 2), then the
+// Taylor series of e^r, its terms from r^2 / 2 on in one float (below 2^-4, so 2^-28 off).
+__device__ __forceinline__ float2 split_exp(float la) {
+  if (la <= kMinLog) return make_float2(0.f, 0.f);
+  const float n = rintf(la * 1.44269504f);
+  const float big = fmaf(n, -0.693359375f, la);         // exact
+  const float r = fmaf(n, 2.12194440e-4f, big), r_lo = fmaf(n, 2.12194440e-4f, big - r);
+  float e = 1.f / 40320.f;
+  e = fmaf(e, r, 1.f / 5040.f);
+  e = fmaf(e, r, 1.f / 720.f);
+  e = fmaf(e, r, 1.f / 120.f);
+  e = fmaf(e, r, 1.f / 24.f);
+  e = fmaf(e, r, 1.f / 6.f);
+  e = fmaf(e, r, 0.5f);
+  const float rest = fmaf(e * r, r, r_lo);
+  const float a = 1.f + r, b = r - (a - 1.f);            // 1 + r
+  const float hi = a + (rest + b), lo = (rest + b) - (hi - a);
+  return make_float2(ldexpf(hi, (int)n), ldexpf(lo, (int)n));
+}
 // The state is read once and written once: 8 bytes an element against 4 operations, so HBM bounds
 // it.  A block per (row, head); a thread owns VEC columns and every nrg-th row, and requests eight
 // rows before it uses the first, so a block keeps 32 KB and more in flight.
@@ -458,7 +554,8 @@ cudaError_t launch_join(const Run &r, cudaStream_t s) {
 int simt_slices(int dz) { return (dz + COLS - 1) / COLS; }
 
 cudaError_t launch_run_simt(const Run &r, cudaStream_t s) {
-  return r.dtype == GDN2_BF16 ? launch_run_t<__nv_bfloat16>(r, s) : launch_run_t<float>(r, s);
+  if (r.dz <= 32) return r.dtype == GDN2_BF16 ? launch_run_t<__nv_bfloat16, 1>(r, s) : launch_run_t<float, 1>(r, s);
+  return r.dtype == GDN2_BF16 ? launch_run_t<__nv_bfloat16, 2>(r, s) : launch_run_t<float, 2>(r, s);
 }
 
 cudaError_t launch_dlog_simt(const float *dots_q, int nq, const float *dots_k, int nk, const float *S_T,

@@ -63,7 +63,7 @@ bool tensor_core(const gdn2_linattn_dims *d) { return d->d_k == 128 && d->d_v ==
 // Where the (sequence, head) units alone leave SMs idle, long sequences are cut into pieces that
 // run side by side (each piece's end state first, the join, then the outputs): half as much again
 // of the work, spread over all SMs.  The target is the balanced share of tokens per worker; the
-// tensor-core run has one worker per SM, the fp32 run (a slice of 32 state columns each) four.
+// tensor-core run has one worker per SM, the fp32 run (a slice of 64 state columns each) two.
 Cut make_cut(const gdn2_linattn_dims *d, const int32_t *cu, bool packed) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
@@ -73,9 +73,9 @@ Cut make_cut(const gdn2_linattn_dims *d, const int32_t *cu, bool packed) {
   const int64_t T = tokens_of(d, packed);
   const bool tc = tensor_core(d);
   const int slices = tc ? 1 : gdn2::lin::simt_slices(d->d_k < d->d_v ? d->d_k : d->d_v);
-  const int64_t workers = tc ? sms : 4 * (int64_t)sms;
+  const int64_t workers = tc ? sms : 2 * (int64_t)sms;
   int64_t target = (T * d->n_heads * slices + workers - 1) / workers;
-  const int64_t least = tc ? 512 : 256;
+  const int64_t least = tc ? 512 : 128;
   if (target < least) target = least;
   Cut c;
   memset(&c, 0, sizeof(c));
