@@ -10,13 +10,14 @@ namespace lin {
 namespace {
 
 // ---------------------------------------------------------------- plan and join
-// Exclusive running count of pieces over the sequences (one block).
-__global__ void __launch_bounds__(1024) plan_kernel(Cut c, int32_t *seg_off) {
+// Exclusive running count of pieces over the sequences (one block) into seg_off, and the pieces'
+// numbers from the longest down into order; either may be NULL.
+__global__ void __launch_bounds__(1024) plan_kernel(Cut c, int32_t *seg_off, int32_t *order) {
   __shared__ int warp_sum[32];
   __shared__ int base;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) base = 0;
-  for (int n0 = 0; n0 < c.n_seqs; n0 += 1024) {
+  for (int n0 = 0; seg_off && n0 < c.n_seqs; n0 += 1024) {
     const int n = n0 + threadIdx.x;
     int v = 0;
     if (n < c.n_seqs) {
@@ -43,6 +44,30 @@ __global__ void __launch_bounds__(1024) plan_kernel(Cut c, int32_t *seg_off) {
     }
     __syncthreads();
   }
+  if (!order) return;
+  __syncthreads();
+  // keys: chunks, then the lower number first; 0 is no piece.  A bitonic sort, largest first.
+  __shared__ uint32_t key[kMaxSorted];
+  c.seg_off = seg_off;
+  const int i = threadIdx.x;
+  Piece p;
+  key[i] = i < c.n_pieces && find_piece(c, i, &p)
+               ? (uint32_t)min(p.len / kChunk + 1, (1 << 21) - 1) << 10 | (uint32_t)(kMaxSorted - 1 - i)
+               : 0u;
+  for (int size = 2; size <= kMaxSorted; size *= 2)
+    for (int step = size / 2; step; step /= 2) {
+      __syncthreads();
+      const int j = i ^ step;
+      if (j > i) {
+        const uint32_t a = key[i], b = key[j];
+        if ((a < b) == ((i & size) == 0)) {
+          key[i] = b;
+          key[j] = a;
+        }
+      }
+    }
+  __syncthreads();
+  if (i < c.n_pieces) order[i] = key[i] ? kMaxSorted - 1 - (int)(key[i] & (kMaxSorted - 1)) : -1;
 }
 
 // piece_state[s] holds the end state of piece s from zero; in its place comes the state piece s
@@ -127,9 +152,10 @@ __global__ void __launch_bounds__(kRunThreads) run_kernel(Run p) {
   __shared__ float dot[TB][COLS / 4 + 1];
   __shared__ long long cum[TB];  // sums of log_a from the tile's first token, inclusive
   __shared__ float fs[TB], ws[TB];
-  const int H = p.cut.H, unit = blockIdx.x, h = unit % H, tid = threadIdx.x;
+  const int H = p.cut.H, tid = threadIdx.x;
   Piece pc;
-  if (!find_piece(p.cut, unit / H, &pc)) return;
+  if (!find_unit(p.cut, blockIdx.x, &pc)) return;
+  const int unit = pc.unit, h = unit % H;
   if (p.state_only && (pc.count < 2 || pc.s == (p.back ? 0 : pc.count - 1))) return;
   const RunSmem L(p.dy, p.m != nullptr);
   float *xs = sm, *yv = sm + L.off_y, *zs = sm + L.off_z, *ss = sm + L.off_s, *ms = sm + L.off_m;
@@ -540,8 +566,8 @@ cudaError_t launch_step_t(const StepProblem &p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_plan(const Cut &c, int32_t *seg_off, cudaStream_t s) {
-  plan_kernel<<<1, 1024, 0, s>>>(c, seg_off);
+cudaError_t launch_plan(const Cut &c, int32_t *seg_off, int32_t *order, cudaStream_t s) {
+  plan_kernel<<<1, 1024, 0, s>>>(c, seg_off, order);
   return cudaGetLastError();
 }
 

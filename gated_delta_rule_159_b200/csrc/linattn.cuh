@@ -16,11 +16,15 @@ struct Cut {
   const int32_t *cu;       // device [n_seqs + 1] token offsets, or NULL: n_seqs x seq_len tokens
   const int32_t *seg_off;  // device [n_seqs + 1]: first piece of every sequence (packed batches with
                            // cuts), or NULL: every sequence has `per_seq` pieces
+  const int32_t *order;    // device [n_pieces]: the pieces from the longest down (-1 behind the last), or
+                           // NULL: as they come.  Blocks start in that order, so that no long piece is left
+                           // for the end of a ragged batch.
   int n_seqs, seq_len, H;
   int per_seq;             // pieces per sequence without seg_off
   int n_pieces;            // pieces in all (an upper bound with seg_off)
   int target;
   int t_total;
+  int sorted;              // the call asks for an order
 };
 
 // Length of the pieces of a sequence of `len` tokens, and their number.
@@ -39,7 +43,9 @@ struct Piece {
   int n, s, count;  // sequence, index of the piece in it, pieces of the sequence
   int t0, len;      // first token, tokens
   int first_piece;  // global index of the sequence's piece 0
+  int unit;         // global index of the piece, times H, plus the head
 };
+constexpr int kMaxSorted = 1024;  // pieces that one block sorts
 
 // Bounds of sequence n; offsets outside [0, t_total] or out of order are cut back to it.
 __device__ __forceinline__ void seq_bounds(const Cut &c, int n, int *t0, int *len) {
@@ -89,6 +95,13 @@ constexpr int kMarkDots = 8;  // partial products a mark, one of each state warp
 __host__ __device__ inline int mark_slot(int g, int t) { return g + t / (kGroup * kChunk); }
 inline size_t mark_slots(const Cut &c) { return (size_t)c.n_pieces + (size_t)(c.t_total / (kGroup * kChunk)) + 1; }
 
+// The piece of the block's unit (a position in the order, and a head).
+__device__ __forceinline__ bool find_unit(const Cut &c, int block, Piece *p) {
+  const int pos = block / c.H, g = c.order ? c.order[pos] : pos;
+  p->unit = g * c.H + block % c.H;
+  return g >= 0 && find_piece(c, g, p);
+}
+
 // log_a below this is a reset: e^-104 is 0 in fp32, and sums over a chunk stay finite and fine enough
 // (32 resets come to 4800 in log2, a float's step there is 2^-11).
 constexpr float kMinLog = -104.f;
@@ -130,7 +143,7 @@ struct Run {
   int dtype;
 };
 
-cudaError_t launch_plan(const Cut &c, int32_t *seg_off, cudaStream_t stream);
+cudaError_t launch_plan(const Cut &c, int32_t *seg_off, int32_t *order, cudaStream_t stream);
 cudaError_t launch_join(const Run &r, cudaStream_t stream);
 int simt_slices(int dz);
 cudaError_t launch_run_simt(const Run &r, cudaStream_t stream);

@@ -94,19 +94,21 @@ Cut make_cut(const gdn2_linattn_dims *d, const int32_t *cu, bool packed) {
     c.per_seq = gdn2::lin::piece_count(d->seq_len, c.target);
     c.n_pieces = d->n_seqs * c.per_seq;
   }
+  c.sorted = packed && c.n_pieces > 1 && c.n_pieces <= gdn2::lin::kMaxSorted && (int64_t)c.n_pieces * c.H * slices > workers;
   return c;
 }
 bool has_cuts(const Cut &c) { return c.n_pieces > c.n_seqs; }
 
-// The cut's part of a workspace: piece offsets, log sums and states.
+// The cut's part of a workspace: piece offsets and order, log sums and states.
 struct CutLayout {
-  size_t off_seg, off_log, off_state, end;
+  size_t off_seg, off_order, off_log, off_state, end;
 };
 CutLayout cut_layout(const Cut &c, size_t at, size_t state) {
   CutLayout L;
   const size_t units = has_cuts(c) ? (size_t)c.n_pieces * c.H : 0;
   L.off_seg = at;
-  L.off_log = L.off_seg + (units ? up256(((size_t)c.n_seqs + 1) * sizeof(int32_t)) : 0);
+  L.off_order = L.off_seg + (units ? up256(((size_t)c.n_seqs + 1) * sizeof(int32_t)) : 0);
+  L.off_log = L.off_order + (c.sorted ? up256((size_t)c.n_pieces * sizeof(int32_t)) : 0);
   L.off_state = L.off_log + up256(units * sizeof(double));
   L.end = L.off_state + up256(units * state * sizeof(float));
   return L;
@@ -158,10 +160,12 @@ cudaError_t full_run(Run r, int terms, int32_t *status, bool tc, cudaStream_t s)
 cudaError_t prepare(Cut &c, char *ws, const CutLayout &L, cudaStream_t s) {
   cudaError_t e = cudaMemsetAsync(ws, 0, kHeader, s);
   if (e != cudaSuccess) return e;
-  if (c.cu && has_cuts(c)) {
-    int32_t *off = reinterpret_cast<int32_t *>(ws + L.off_seg);
-    e = gdn2::lin::launch_plan(c, off, s);
+  if (c.cu && (has_cuts(c) || c.sorted)) {
+    int32_t *off = has_cuts(c) ? reinterpret_cast<int32_t *>(ws + L.off_seg) : nullptr;
+    int32_t *order = c.sorted ? reinterpret_cast<int32_t *>(ws + L.off_order) : nullptr;
+    e = gdn2::lin::launch_plan(c, off, order, s);
     c.seg_off = off;
+    c.order = order;
   }
   return e;
 }

@@ -178,9 +178,10 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
   const Run &r = P.r;
   const uint32_t sb = ptx::smem_u32(smem);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int H = r.cut.H, unit = blockIdx.x, h = unit % H;
+  const int H = r.cut.H;
   Piece pc;
-  if (!find_piece(r.cut, unit / H, &pc)) return;
+  if (!find_unit(r.cut, blockIdx.x, &pc)) return;
+  const int unit = pc.unit, h = unit % H;
   const bool only = r.state_only != 0;
   if (only && (pc.count < 2 || pc.s == (BACK ? 0 : pc.count - 1))) return;
   if (sb & 1023u) {  // the swizzled tiles need it; dynamic shared memory starts on it
