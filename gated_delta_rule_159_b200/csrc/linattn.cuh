@@ -88,9 +88,11 @@ __device__ __forceinline__ bool find_piece(const Cut &c, int g, Piece *p) {
 }
 
 // Groups of chunks that dlog_a of the tensor-core runs is summed over, numbered from each piece's
-// start.  Slot of the group that starts at token t of piece g: pieces are in token order, so no two
-// share one.
-constexpr int kGroup = 4;
+// start.  A group ends with an exact product of the two states, in between bf16 products add up: over
+// 4096 tokens dlog_a is off by 0.40% with groups of 4 chunks, 0.32% with 2 and 0.27% with 1 (0.17% is its
+// own rounding), and the gradients of 8 x 4096 take 553, 553 and 613 us.  Slot of the group that starts at
+// token t of piece g: pieces are in token order, so no two share one.
+constexpr int kGroup = 2;
 constexpr int kMarkDots = 8;  // partial products a mark, one of each state warp
 __host__ __device__ inline int mark_slot(int g, int t) { return g + t / (kGroup * kChunk); }
 inline size_t mark_slots(const Cut &c) { return (size_t)c.n_pieces + (size_t)(c.t_total / (kGroup * kChunk)) + 1; }
