@@ -842,7 +842,8 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
 // A warp per group of kGroup chunks.
 constexpr int kDlogWarps = 4;
 __global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *dots_q, const float *dots_k,
-                                                                  const float *mark_dots, Cut c, __nv_bfloat16 *dlog) {
+                                                                  const float *mark_dots, Cut c, int no_start,
+                                                                  __nv_bfloat16 *dlog) {
   constexpr int kTokens = kGroup * C;
   const int H = c.H, unit = blockIdx.x, h = unit % H, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Piece pc;
@@ -868,7 +869,9 @@ __global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *d
         const float down = __shfl_down_sync(0xffffffffu, v[j], d);
         if (lane + d < 32) v[j] += down;
       }
-      if (32 * j + lane < cnt) dlog[(t0 + 32 * j + lane) * H + h] = __float2bfloat16_rn(v[j] + behind);
+      // the first token decays nothing where no state comes in
+      const bool none = no_start && pc.s == 0 && g == 0 && 32 * j + lane == 0;
+      if (32 * j + lane < cnt) dlog[(t0 + 32 * j + lane) * H + h] = __float2bfloat16_rn(none ? 0.f : v[j] + behind);
       behind += __shfl_sync(0xffffffffu, v[j], 0);
     }
   }
@@ -914,12 +917,12 @@ cudaError_t launch_run_tc(const Run &r, int terms, int32_t *status, cudaStream_t
   return terms == 4 ? launch_t<false, 4>(P, s) : launch_t<false, 2>(P, s);
 }
 
-cudaError_t launch_dlog_tc(const float *dots_q, const float *dots_k, const float *mark_dots, const Cut &c, void *dlog,
-                           cudaStream_t s) {
+cudaError_t launch_dlog_tc(const float *dots_q, const float *dots_k, const float *mark_dots, const Cut &c, bool no_start,
+                           void *dlog, cudaStream_t s) {
   if (c.t_total == 0) return cudaSuccess;
   const int64_t groups = (int64_t)c.t_total / (kGroup * C * kDlogWarps) + 1;  // of the longest piece, at most
   const dim3 grid((unsigned)((int64_t)c.n_pieces * c.H), (unsigned)(groups < 16 ? groups : 16));
-  dlog_tc_kernel<<<grid, 32 * kDlogWarps, 0, s>>>(dots_q, dots_k, mark_dots, c, static_cast<__nv_bfloat16 *>(dlog));
+  dlog_tc_kernel<<<grid, 32 * kDlogWarps, 0, s>>>(dots_q, dots_k, mark_dots, c, no_start, static_cast<__nv_bfloat16 *>(dlog));
   return cudaGetLastError();
 }
 

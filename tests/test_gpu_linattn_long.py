@@ -143,3 +143,12 @@ def test_a_training_step_from_checkpoints(g):
         # their root mean square: 1.1% a saved factor, of which every gradient has two at most: 1.6%.
         off = (got[x].double() - plain[x].double()).norm() / plain[x].double().norm()
         assert off < 2 * 0.016, (x, float(off))
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 24)])
+def test_the_first_token_decays_nothing_without_a_state(g, dtype, d):
+    p, cu = ref.problem((1, 200, 1, 0, 2), 2, 1, d, d, dtype, "token", False, seed=39)
+    dS_T = torch.randn(5, 2, d, d, device="cuda")
+    got = g.linattn_bwd(p["q"], p["k"], p["v"], p["log_a"], p["dO"], None, dS_T, p["cu"])
+    first = [c for c, e in zip(cu, cu[1:]) if e > c]
+    assert (got["dlog_a"][first] == 0).all() and (got["dlog_a"][cu[1] + 1:cu[2]] != 0).any()
