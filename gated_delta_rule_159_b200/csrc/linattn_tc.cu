@@ -70,7 +70,8 @@ enum {
   BAR_WFREE = 8,    // + stage: and used
   BAR_FULL = 10,    // + slot: a slice of w o Y written
   BAR_EMPTY = 12,   // + slot: its products done
-  BAR_ROWDEC = 14,  // the rows' decays there
+  BAR_U = 14,       // + parity: update done
+  BAR_ROWDEC = 16,  // the rows' decays there
   BAR_ROWFREE,      // and used
   BAR_X,            // X loaded
   BAR_XS,           // X S done, X and the state's copy free
@@ -80,7 +81,6 @@ enum {
   BAR_OREAD,        // out read
   BAR_S,            // the state's copy written
   BAR_SREAD,        // the state read (and scaled)
-  BAR_U,            // update done
   BAR_CLEAN,        // Y's and Z's rows behind the sequence cleared
   BAR_DRAIN,        // + 0, 1
   N_BARS = BAR_DRAIN + 2
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
         ptx::umma_commit_if(lead, bar(BAR_EMPTY + slot));
       }
       if (!ok) break;
-      ptx::umma_commit_if(lead, bar(BAR_U));
+      ptx::umma_commit_if(lead, bar(BAR_U + s));
       ptx::umma_commit_if(lead, bar(BAR_FREE + s));
     }
     ptx::umma_commit_if(lead, bar(BAR_DRAIN));  // all products, before the tensor memory is freed
@@ -718,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
     // marks of this thread's part of the state behind group `g` of chunks
     auto mark_unit = [&](int g) { return (size_t)mark_slot(unit / H, pc.t0 + g * kGroup * C) * H + h; };
     auto ends_group = [&](int no) { return (no + 1) % kGroup == 0 || no == nch - 1; };
+    int seen = 0;  // updates waited for
     for (int k = 0; k <= nch; ++k) {
       const int s = k & 1;
       const uint32_t par = (uint32_t)(k >> 1);
@@ -749,80 +750,93 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
       const uint32_t gs = dec + DEC_W + (uint32_t)s * DEC_STAGE + DEC_G;
       const float behind = lds_f32(gs), back = last ? 1.f : lds_f32(gs + 4);
       const float2 behind2 = make_float2(behind, behind);
-      if (k && !wait_warp(BAR_U, (uint32_t)k + 1u)) break;
-      ptx::tc_fence_after();
-      const float *mark_in = nullptr;
-      float *mark_out = nullptr;
-      size_t mu = 0;
-      if (r.marks && !only) {
-        const int no = chunk_no(k);  // forward: the group in front of chunk k is done; backward: k's begins
-        if (BACK && !last && ends_group(no)) {
-          mu = mark_unit(no / kGroup);
-          mark_in = r.marks + mu * (D * D) + 4 * yrow;
-        }
-        if (!BACK && k && ends_group(k - 1)) mark_out = r.marks + mark_unit((k - 1) / kGroup) * (D * D) + 4 * yrow;
-        if (BACK && !last && no % kGroup == 1 && no > kGroup) {  // the next group's mark, two chunks ahead
-          const char *next = reinterpret_cast<const char *>(r.marks + mark_unit(no / kGroup - 1) * (D * D)) + stid * 128;
-          prefetch_l2(next);
-          prefetch_l2(next + 32768);
-        }
+      // with neither a copy to write nor anything to scale, the state is not read: the next update
+      // follows at once.  One update stays unseen at most, so that no phase is missed.
+      const bool pass = only && !last && back == 1.f;
+      const int need = pass ? k - 1 : k;  // updates that have to be done
+      bool ok = true;
+      while (ok && seen < need) {
+        ok = wait_warp(BAR_U + (seen & 1), (uint32_t)(seen >> 1));
+        ++seen;
       }
-      float dot = 0.f;
-      uint32_t copy[32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = 4 * half + i;  // 16 columns each
-        uint32_t v[16];
-        ptx::tmem_ld16(quad + TM_S + c * 16, v);
-        ptx::tmem_wait_ld();
-        if (back != 1.f) {
-          uint32_t u[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(back * __uint_as_float(v[j]));
-          ptx::tmem_st16(quad + TM_S + c * 16, u);
+      if (!ok) break;
+      if (pass) {
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_SREAD));
+      } else {
+        ptx::tc_fence_after();
+        const float *mark_in = nullptr;
+        float *mark_out = nullptr;
+        size_t mu = 0;
+        if (r.marks && !only) {
+          const int no = chunk_no(k);  // forward: the group in front of chunk k is done; backward: k's begins
+          if (BACK && !last && ends_group(no)) {
+            mu = mark_unit(no / kGroup);
+            mark_in = r.marks + mu * (D * D) + 4 * yrow;
+          }
+          if (!BACK && k && ends_group(k - 1)) mark_out = r.marks + mark_unit((k - 1) / kGroup) * (D * D) + 4 * yrow;
+          if (BACK && !last && no % kGroup == 1 && no > kGroup) {  // the next group's mark, two chunks ahead
+            const char *next = reinterpret_cast<const char *>(r.marks + mark_unit(no / kGroup - 1) * (D * D)) + stid * 128;
+            prefetch_l2(next);
+            prefetch_l2(next + 32768);
+          }
         }
+        float dot = 0.f;
+        uint32_t copy[32];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 w = mul2(behind2, pair(v[2 * j], v[2 * j + 1]));
-          v[2 * j] = __float_as_uint(w.x);
-          v[2 * j + 1] = __float_as_uint(w.y);
-          copy[8 * i + j] = pack_bf16x2(w.x, w.y);
+        for (int i = 0; i < 4; ++i) {
+          const int c = 4 * half + i;  // 16 columns each
+          uint32_t v[16];
+          ptx::tmem_ld16(quad + TM_S + c * 16, v);
+          ptx::tmem_wait_ld();
+          if (back != 1.f) {
+            uint32_t u[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(back * __uint_as_float(v[j]));
+            ptx::tmem_st16(quad + TM_S + c * 16, u);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 w = mul2(behind2, pair(v[2 * j], v[2 * j + 1]));
+            v[2 * j] = __float_as_uint(w.x);
+            v[2 * j + 1] = __float_as_uint(w.y);
+            copy[8 * i + j] = pack_bf16x2(w.x, w.y);
+          }
+          if (mark_in) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 w = *reinterpret_cast<const float4 *>(mark_in + (c * 4 + j) * 512);
+              dot = fmaf(w.x, __uint_as_float(v[4 * j]), fmaf(w.y, __uint_as_float(v[4 * j + 1]),
+                    fmaf(w.z, __uint_as_float(v[4 * j + 2]), fmaf(w.w, __uint_as_float(v[4 * j + 3]), dot))));
+            }
+          }
+          if (mark_out) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4 *>(mark_out + (c * 4 + j) * 512) =
+                  make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          }
+          if (last && dst) store_state(dst, flip_dst, c * 16, v);
+        }
+        if (last) break;
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_SREAD));
+        if (!only) {
+          if (k && !wait_warp(BAR_XS, (uint32_t)k + 1u)) break;  // the last copy has been read
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            sts_v4(sb + OFF_S + half * kBlock + swz(yrow, (uint32_t)j),
+                   make_uint4(copy[4 * j], copy[4 * j + 1], copy[4 * j + 2], copy[4 * j + 3]));
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(BAR_S));
         }
         if (mark_in) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 w = *reinterpret_cast<const float4 *>(mark_in + (c * 4 + j) * 512);
-            dot = fmaf(w.x, __uint_as_float(v[4 * j]), fmaf(w.y, __uint_as_float(v[4 * j + 1]),
-                  fmaf(w.z, __uint_as_float(v[4 * j + 2]), fmaf(w.w, __uint_as_float(v[4 * j + 3]), dot))));
-          }
+          for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+          if (lane == 0) r.mark_dots[mu * kMarkDots + (warp - kState0)] = dot;
         }
-        if (mark_out) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4 *>(mark_out + (c * 4 + j) * 512) =
-                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        }
-        if (last && dst) store_state(dst, flip_dst, c * 16, v);
-      }
-      if (last) break;
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(BAR_SREAD));
-      if (!only) {
-        if (k && !wait_warp(BAR_XS, (uint32_t)k + 1u)) break;  // the last copy has been read
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          sts_v4(sb + OFF_S + half * kBlock + swz(yrow, (uint32_t)j),
-                 make_uint4(copy[4 * j], copy[4 * j + 1], copy[4 * j + 2], copy[4 * j + 3]));
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(BAR_S));
-      }
-      if (mark_in) {
-#pragma unroll
-        for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-        if (lane == 0) r.mark_dots[mu * kMarkDots + (warp - kState0)] = dot;
       }
       if (!weigh_slices(k, 1, SLICES)) break;
       if (lane == 0) ptx::mbar_arrive(bar(BAR_WFREE + s));
