@@ -48,7 +48,7 @@ LINATTN_HEAD_DECAY = 1
 DEBUG_CHUNK = 1
 DEBUG_DECODE = 2
 DEBUG_BWD = 3
-DEBUG_LINATTN = 4
+DEBUG_LINATTN = 5
 
 
 class Dims(ctypes.Structure):

@@ -457,8 +457,9 @@ int gdn2_chunk_fwd_noalloc_status(gdn2_stream_t stream);
  *   seq_len     as in gdn2_dims.
  *   flags       GDN2_LINATTN_HEAD_DECAY: log_a is fp32 [H], one fixed decay per head; else log_a is
  *               [T_tot, H] of dtype_in.
- * log_a <= 0 (not checked); -infinity (a reset) is allowed, a NaN counts as one, and log_a below -104 counts as -104 in the prompt and
- * gradient calls (a factor of 0 in fp32).  Conventions otherwise as above.  Supported: d_k and d_v
+ * log_a <= 0 (not checked); -infinity (a reset) is allowed; in the prompt and gradient calls log_a below
+ * -104 counts as -104 (a factor of 0 in fp32), and so does a NaN.  Conventions otherwise as above.
+ * Supported: d_k and d_v
  * up to 128, bf16 or fp32.  d_k = d_v = 128 in bf16 runs on the tensor cores: bf16 products and fp32
  * sums; the state is fp32 throughout, and S_T and dS0 are off by a few 1e-7 for decays of up to some
  * hundred tokens, by about 2e-6 at some thousand.  Everything else runs in fp32.
@@ -588,7 +589,7 @@ enum gdn2_debug_site {
   GDN2_DEBUG_CHUNK = 1,
   GDN2_DEBUG_DECODE = 2,
   GDN2_DEBUG_BWD = 3,
-  GDN2_DEBUG_LINATTN = 4
+  GDN2_DEBUG_LINATTN = 5
 };
 int gdn2_debug_timeout_once(int32_t site, uint64_t wait_ns);
 
