@@ -74,7 +74,11 @@ __global__ void __launch_bounds__(1024) plan_kernel(Cut c, int32_t *seg_off, int
 // starts from: start_{s+1} = e^{sum log_a of s} start_s + end_s (from the last piece down in a
 // backward run).  Elementwise in the state, serial over the pieces; the loads of the next piece
 // do not depend on the sum, so four are kept in flight.
-__global__ void __launch_bounds__(256) join_kernel(Run r) {
+struct Runs {
+  Run run[kMaxRuns];
+};
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Runs P) {
+  const Run &r = P.run[blockIdx.z];
   const int size = r.dy * r.dz, H = r.cut.H;
   const int n = blockIdx.x / H, h = blockIdx.x % H;
   const int first = r.cut.seg_off ? r.cut.seg_off[n] : n * r.cut.per_seq;
@@ -146,7 +150,8 @@ __device__ __forceinline__ void fma4(float (&acc)[4], float a, const float4 &b) 
 
 // ROWS rows of out a thread: 1 where the slice has at most 32 columns, else 2.
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(kRunThreads) run_kernel(Run p) {
+__global__ void __launch_bounds__(kRunThreads) run_kernel(const __grid_constant__ Runs P) {
+  const Run &p = P.run[blockIdx.z];
   extern __shared__ __align__(16) float sm[];
   __shared__ __align__(16) float ps[TB][TB + 4];
   __shared__ float dot[TB][COLS / 4 + 1];
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kRunThreads) run_kernel(Run p) {
   __shared__ float fs[TB], ws[TB];
   const int H = p.cut.H, tid = threadIdx.x;
   Piece pc;
-  if (!find_unit(p.cut, blockIdx.x, &pc)) return;
+  if (blockIdx.y * COLS >= p.dz || !find_unit(p.cut, blockIdx.x, &pc)) return;
   const int unit = pc.unit, h = unit % H;
   if (p.state_only && (pc.count < 2 || pc.s == (p.back ? 0 : pc.count - 1))) return;
   const RunSmem L(p.dy, p.m != nullptr);
@@ -368,12 +373,18 @@ __global__ void __launch_bounds__(kRunThreads) run_kernel(Run p) {
 }
 
 template <typename T, int ROWS>
-cudaError_t launch_run_t(const Run &r, cudaStream_t s) {
-  const int bytes = RunSmem(r.dy, r.m != nullptr).total * (int)sizeof(float);
+cudaError_t launch_run_t(const Run *r, int n, int widest, cudaStream_t s) {
+  Runs P;
+  int bytes = 0;
+  for (int i = 0; i < n; ++i) {
+    P.run[i] = r[i];
+    const int mine = RunSmem(r[i].dy, r[i].m != nullptr).total * (int)sizeof(float);
+    if (mine > bytes) bytes = mine;
+  }
   const cudaError_t e = cudaFuncSetAttribute(run_kernel<T, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((int64_t)r.cut.n_pieces * r.cut.H), (unsigned)simt_slices(r.dz));
-  run_kernel<T, ROWS><<<grid, kRunThreads, bytes, s>>>(r);
+  const dim3 grid((unsigned)((int64_t)r->cut.n_pieces * r->cut.H), (unsigned)simt_slices(widest), (unsigned)n);
+  run_kernel<T, ROWS><<<grid, kRunThreads, bytes, s>>>(P);
   return cudaGetLastError();
 }
 
@@ -573,17 +584,24 @@ cudaError_t launch_plan(const Cut &c, int32_t *seg_off, int32_t *order, cudaStre
   return cudaGetLastError();
 }
 
-cudaError_t launch_join(const Run &r, cudaStream_t s) {
-  const dim3 grid((unsigned)(r.cut.n_seqs * r.cut.H), (unsigned)((r.dy * r.dz + 255) / 256));
-  join_kernel<<<grid, 256, 0, s>>>(r);
+cudaError_t launch_join(const Run *r, int n, cudaStream_t s) {
+  Runs P;
+  for (int i = 0; i < n; ++i) P.run[i] = r[i];
+  const dim3 grid((unsigned)(r->cut.n_seqs * r->cut.H), (unsigned)((r->dy * r->dz + 255) / 256), (unsigned)n);
+  join_kernel<<<grid, 256, 0, s>>>(P);
   return cudaGetLastError();
 }
 
 int simt_slices(int dz) { return (dz + COLS - 1) / COLS; }
 
-cudaError_t launch_run_simt(const Run &r, cudaStream_t s) {
-  if (r.dz <= 32) return r.dtype == GDN2_BF16 ? launch_run_t<__nv_bfloat16, 1>(r, s) : launch_run_t<float, 1>(r, s);
-  return r.dtype == GDN2_BF16 ? launch_run_t<__nv_bfloat16, 2>(r, s) : launch_run_t<float, 2>(r, s);
+cudaError_t launch_run_simt(const Run *r, int n, cudaStream_t s) {
+  int widest = 0;
+  for (int i = 0; i < n; ++i)
+    if (r[i].dz > widest) widest = r[i].dz;
+  const bool bf16 = r->dtype == GDN2_BF16;
+  if (widest <= 32)
+    return bf16 ? launch_run_t<__nv_bfloat16, 1>(r, n, widest, s) : launch_run_t<float, 1>(r, n, widest, s);
+  return bf16 ? launch_run_t<__nv_bfloat16, 2>(r, n, widest, s) : launch_run_t<float, 2>(r, n, widest, s);
 }
 
 cudaError_t launch_dlog_simt(const float *dots_q, int nq, const float *dots_k, int nk, const float *S_T,

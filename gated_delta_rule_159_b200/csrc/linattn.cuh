@@ -138,20 +138,27 @@ struct Run {
   int Hm;
   float *dots;
   // Tensor-core runs: marks of the state behind every group of kGroup chunks, [slots][H][dy * dz]
-  // in the state warps' own order; the forward form writes them, the backward form multiplies its
-  // state at the same place with them into mark_dots [slots][H][kMarkDots].  NULL: none.
+  // in the state warps' own order; the forward form writes them, and so does the backward form with
+  // mark_dots NULL; else it multiplies its state at the same place with them into mark_dots
+  // [slots][H][kMarkDots].  NULL: none.
   float *marks, *mark_dots;
   Cut cut;
   int dtype;
 };
 
 cudaError_t launch_plan(const Cut &c, int32_t *seg_off, int32_t *order, cudaStream_t stream);
-cudaError_t launch_join(const Run &r, cudaStream_t stream);
+// n runs over the same cut: the forward, or the three of the gradients in one launch.
+constexpr int kMaxRuns = 3;
+cudaError_t launch_join(const Run *r, int n, cudaStream_t stream);
 int simt_slices(int dz);
-cudaError_t launch_run_simt(const Run &r, cudaStream_t stream);
+cudaError_t launch_run_simt(const Run *r, int n, cudaStream_t stream);
 // The run on the tensor cores (linattn_tc.cu): bf16, dy = dz = 128.  `terms`: bf16 values that
 // stand for a weighted row of y in the state's update, 4 (26 bits) or 2 (17).
 cudaError_t launch_run_tc(const Run &r, int terms, int32_t *status, cudaStream_t stream);
+// The gradients' three runs in one launch, four terms each.
+cudaError_t launch_grads_tc(const Run *r, int32_t *status, cudaStream_t stream);
+// mark_dots of the marks that the dq and the dk run wrote in one launch.
+cudaError_t launch_marks(const float *a, const float *b, float *mark_dots, const Cut &c, cudaStream_t stream);
 // dlog_a of the fp32 runs: dots_q (of dq with q), dots_k (of dk with k), and <S_T, dS_T> (S_T
 // may be NULL with dS_T).
 cudaError_t launch_dlog_simt(const float *dots_q, int nq, const float *dots_k, int nk, const float *S_T,

@@ -60,21 +60,27 @@ int check_sizes(const gdn2_linattn_dims *d, bool packed) {
 
 bool tensor_core(const gdn2_linattn_dims *d) { return d->d_k == 128 && d->d_v == 128 && d->dtype_in == GDN2_BF16; }
 
-// Where the (sequence, head) units alone leave SMs idle, long sequences are cut into pieces that
-// run side by side (each piece's end state first, the join, then the outputs): half as much again
-// of the work, spread over all SMs.  The target is the balanced share of tokens per worker; the
-// tensor-core run has one worker per SM, the fp32 run (a slice of 64 state columns each) two.
-Cut make_cut(const gdn2_linattn_dims *d, const int32_t *cu, bool packed) {
+int sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
     cudaGetLastError();
     sms = 148;
   }
+  return sms;
+}
+
+// Where the (sequence, head) units alone leave SMs idle, long sequences are cut into pieces that
+// run side by side (each piece's end state first, the join, then the outputs): half as much again
+// of the work, spread over all SMs.  The target is the balanced share of tokens per worker; the
+// tensor-core run has one worker per SM, the fp32 run (a slice of 64 state columns each) two.
+// `runs` of them share the launch.
+Cut make_cut(const gdn2_linattn_dims *d, const int32_t *cu, bool packed, int runs = 1) {
+  const int sms = sm_count();
   const int64_t T = tokens_of(d, packed);
   const bool tc = tensor_core(d);
   const int slices = tc ? 1 : gdn2::lin::simt_slices(d->d_k < d->d_v ? d->d_k : d->d_v);
   const int64_t workers = tc ? sms : 2 * (int64_t)sms;
-  int64_t target = (T * d->n_heads * slices + workers - 1) / workers;
+  int64_t target = (T * d->n_heads * slices * runs + workers - 1) / workers;
   const int64_t least = tc ? 512 : 128;
   if (target < least) target = least;
   Cut c;
@@ -94,7 +100,7 @@ Cut make_cut(const gdn2_linattn_dims *d, const int32_t *cu, bool packed) {
     c.per_seq = gdn2::lin::piece_count(d->seq_len, c.target);
     c.n_pieces = d->n_seqs * c.per_seq;
   }
-  c.sorted = packed && c.n_pieces > 1 && c.n_pieces <= gdn2::lin::kMaxSorted && (int64_t)c.n_pieces * c.H * slices > workers;
+  c.sorted = packed && c.n_pieces > 1 && c.n_pieces <= gdn2::lin::kMaxSorted && (int64_t)c.n_pieces * c.H * slices * runs > workers;
   return c;
 }
 bool has_cuts(const Cut &c) { return c.n_pieces > c.n_seqs; }
@@ -103,14 +109,14 @@ bool has_cuts(const Cut &c) { return c.n_pieces > c.n_seqs; }
 struct CutLayout {
   size_t off_seg, off_order, off_log, off_state, end;
 };
-CutLayout cut_layout(const Cut &c, size_t at, size_t state) {
+CutLayout cut_layout(const Cut &c, size_t at, size_t state, size_t runs = 1) {
   CutLayout L;
   const size_t units = has_cuts(c) ? (size_t)c.n_pieces * c.H : 0;
   L.off_seg = at;
   L.off_order = L.off_seg + (units ? up256(((size_t)c.n_seqs + 1) * sizeof(int32_t)) : 0);
   L.off_log = L.off_order + (c.sorted ? up256((size_t)c.n_pieces * sizeof(int32_t)) : 0);
-  L.off_state = L.off_log + up256(units * sizeof(double));
-  L.end = L.off_state + up256(units * state * sizeof(float));
+  L.off_state = L.off_log + up256(runs * units * sizeof(double));
+  L.end = L.off_state + up256(runs * units * state * sizeof(float));
   return L;
 }
 
@@ -137,22 +143,28 @@ int check_log_a(const gdn2_linattn_dims *d, int64_t tokens, const void *log_a) {
 
 int cuda_fail(const char *what, cudaError_t e) { return fail(GDN2_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e)); }
 
-// A run, with its cut sequences' piece states and join first.  The runs whose state can be a result
-// (the forward's, dv's) take it to the tensor cores in four bf16 terms, whether or not this call
-// asks for it: out must not depend on that.  The others only feed it to bf16 products: two terms.
-cudaError_t full_run(Run r, int terms, int32_t *status, bool tc, cudaStream_t s) {
+// Runs over one cut, their cut sequences' piece states and join first: the forward or one of the
+// gradients' on the tensor cores, all three of those there (n = 3), or any number in fp32.
+// The runs whose state can be a result (the forward's, dv's) take it to the tensor cores in four bf16
+// terms, whether or not this call asks for it: out must not depend on that.  The others only feed it
+// to bf16 products: two terms.
+cudaError_t full_runs(Run *r, int n, int terms, int32_t *status, bool tc, cudaStream_t s) {
   cudaError_t e;
-  auto launch = [&](const Run &run) {
-    return tc ? gdn2::lin::launch_run_tc(run, terms, status, s) : gdn2::lin::launch_run_simt(run, s);
+  auto launch = [&](const Run *run) {
+    if (!tc) return gdn2::lin::launch_run_simt(run, n, s);
+    return n > 1 ? gdn2::lin::launch_grads_tc(run, status, s) : gdn2::lin::launch_run_tc(*run, terms, status, s);
   };
-  if (has_cuts(r.cut)) {
-    Run first = r;
-    first.state_only = 1;
-    first.m = nullptr;
+  if (has_cuts(r->cut)) {
+    Run first[gdn2::lin::kMaxRuns];
+    for (int i = 0; i < n; ++i) {
+      first[i] = r[i];
+      first[i].state_only = 1;
+      first[i].m = nullptr;
+    }
     if ((e = launch(first)) != cudaSuccess) return e;
-    if ((e = gdn2::lin::launch_join(r, s)) != cudaSuccess) return e;
+    if ((e = gdn2::lin::launch_join(r, n, s)) != cudaSuccess) return e;
   } else {
-    r.piece_state = nullptr;
+    for (int i = 0; i < n; ++i) r[i].piece_state = nullptr;
   }
   return launch(r);
 }
@@ -182,79 +194,135 @@ Run base_run(const gdn2_linattn_dims *d, const void *log_a, const Cut &c, char *
   return r;
 }
 
-// gdn2_linattn_bwd's workspace: header, the cut, for dlog_a the final state (fp32 runs) or the marks
-// (tensor-core runs), the per-head parts of dq and dk where heads share q and k (one buffer, used
-// twice), the dots.
+// The three runs of the gradients go side by side in one launch in fp32 (3 ragged sequences, 1201
+// tokens, 4 heads of 48 x 80: 157 us, one after the other 312), and on the tensor cores where a run alone
+// would leave half of the SMs idle or need cuts, of which three need fewer (16 heads; 11 ragged
+// sequences, 9001 tokens: 222 us for 322; one of 4096: 160 for 190; where the pieces then divide badly
+// among the SMs it costs: 3 of 20246, 697 for 573).  Else one after the other (8 x 4096 tokens: 510 us,
+// in one launch 682): each run has a kernel of its own, smaller and faster, and with gradients of log_a
+// the second run's states need not be written and read again for the products.
+struct BwdPlan {
+  bool together;
+  Cut cut;
+};
+BwdPlan plan_bwd(const gdn2_linattn_dims *d, const int32_t *cu, bool packed) {
+  BwdPlan p;
+  p.cut = make_cut(d, cu, packed);
+  const bool idle = 2 * (int64_t)d->n_seqs * d->n_heads <= sm_count();
+  p.together = !tensor_core(d) || has_cuts(p.cut) || idle;
+  if (p.together) p.cut = make_cut(d, cu, packed, 3);
+  if (tensor_core(d) && p.together && 3 * (int64_t)p.cut.n_pieces * d->n_heads > INT32_MAX) {  // a grid's blocks
+    p.cut = make_cut(d, cu, packed);
+    p.together = false;
+  }
+  return p;
+}
+
+// gdn2_linattn_bwd's workspace: header, the cut, for dlog_a the final state (fp32 runs) or the marks of
+// one or two runs and their products (tensor-core runs), the per-head parts of dq and dk where heads
+// share q and k (one buffer after the other, two together), the dots.
 struct BwdLayout {
   CutLayout cut;
-  size_t off_fin, off_marks, off_mark_dots, off_part, off_dq, off_dk, off_restored[3], total;
+  size_t off_fin, off_marks[2], off_mark_dots, off_part[2], off_dq, off_dk, off_restored[3], total;
 };
-BwdLayout bwd_layout(const gdn2_linattn_dims *d, const Cut &c, bool ckpt8) {
+BwdLayout bwd_layout(const gdn2_linattn_dims *d, const BwdPlan &plan, bool ckpt8) {
   BwdLayout L;
-  const size_t state = (size_t)d->d_k * d->d_v, T = (size_t)c.t_total, H = d->n_heads;
+  const Cut &c = plan.cut;
+  const size_t state = (size_t)d->d_k * d->d_v, T = (size_t)c.t_total, H = d->n_heads, runs = plan.together ? 3 : 1;
   const bool dlog = !(d->flags & GDN2_LINATTN_HEAD_DECAY), tc = tensor_core(d);
   const size_t slots = dlog && tc ? gdn2::lin::mark_slots(c) * H : 0;
-  L.cut = cut_layout(c, kHeader, state);
-  L.off_fin = L.cut.end;
-  L.off_marks = L.off_fin + (dlog && !tc ? up256((size_t)d->n_seqs * H * state * sizeof(float)) : 0);
-  L.off_mark_dots = L.off_marks + slots * state * sizeof(float);
-  L.off_part = L.off_mark_dots + up256(slots * gdn2::lin::kMarkDots * sizeof(float));
-  L.off_dq = L.off_part + (d->n_qk_heads < d->n_heads ? up256(T * H * d->d_k * sizeof(float)) : 0);
-  const size_t dots = dlog ? up256(T * H * (tc ? 2 : gdn2::lin::simt_slices(d->d_k)) * sizeof(float)) : 0;
-  L.off_dk = L.off_dq + dots;
-  L.total = L.off_dk + dots;
+  L.cut = cut_layout(c, kHeader, state, runs);
+  size_t at = L.cut.end;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += up256(bytes);
+    return here;
+  };
+  L.off_fin = take(dlog && !tc ? (size_t)d->n_seqs * H * state * sizeof(float) : 0);
+  L.off_marks[0] = take(slots * state * sizeof(float));
+  L.off_marks[1] = take(plan.together ? slots * state * sizeof(float) : 0);
+  L.off_mark_dots = take(slots * gdn2::lin::kMarkDots * sizeof(float));
+  const size_t part = d->n_qk_heads < d->n_heads ? T * H * d->d_k * sizeof(float) : 0;
+  L.off_part[0] = take(part);
+  L.off_part[1] = plan.together ? take(part) : L.off_part[0];
+  const size_t dots = dlog ? T * H * (tc ? 2 : gdn2::lin::simt_slices(d->d_k)) * sizeof(float) : 0;
+  L.off_dq = take(dots);
+  L.off_dk = take(dots);
   const size_t es = d->dtype_in == GDN2_BF16 ? 2 : 4;
   const size_t rows[3] = {T * d->n_qk_heads * d->d_k * es, T * d->n_qk_heads * d->d_k * es, T * H * d->d_v * es};
-  for (int i = 0; i < 3; ++i) {
-    L.off_restored[i] = L.total;
-    if (ckpt8) L.total += up256(rows[i]);
-  }
+  for (int i = 0; i < 3; ++i) L.off_restored[i] = take(ckpt8 ? rows[i] : 0);
+  L.total = at;
   return L;
 }
 
 int bwd_runs(const void *q, const void *k, const void *v, const void *log_a, const float *S0,
              const void *dO, const float *dS_T, void *dq, void *dk, void *dv, void *dlog_a,
-             float *dS0, const gdn2_linattn_dims *d, Cut c, char *ws, const BwdLayout &L, cudaStream_t s) {
+             float *dS0, const gdn2_linattn_dims *d, const BwdPlan &plan, char *ws, const BwdLayout &L, cudaStream_t s) {
   const bool tc = tensor_core(d);
+  const Cut &c = plan.cut;
   int32_t *status = reinterpret_cast<int32_t *>(ws);
   const int H = d->n_heads, Hq = d->n_qk_heads;
   const bool shared = Hq < H;
-  float *part = reinterpret_cast<float *>(ws + L.off_part);
-  float *dots_q = reinterpret_cast<float *>(ws + L.off_dq), *dots_k = reinterpret_cast<float *>(ws + L.off_dk);
-  float *fin = dlog_a && dS_T && !tc ? reinterpret_cast<float *>(ws + L.off_fin) : nullptr;
-  float *marks = tc ? reinterpret_cast<float *>(ws + L.off_marks) : nullptr;
-  float *mark_dots = tc ? reinterpret_cast<float *>(ws + L.off_mark_dots) : nullptr;
-  const Run base = base_run(d, log_a, c, ws, L.cut);
+  auto floats = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
+  float *part_q = floats(L.off_part[0]), *part_k = floats(L.off_part[1]);
+  float *dots_q = floats(L.off_dq), *dots_k = floats(L.off_dk), *mark_dots = floats(L.off_mark_dots);
+  float *fin = dlog_a && dS_T && !tc ? floats(L.off_fin) : nullptr;
+  const bool marks = dlog_a && tc;
+  Run runs[3];
+  for (int i = 0; i < 3; ++i) {
+    runs[i] = base_run(d, log_a, c, ws, L.cut);
+    if (plan.together) {
+      const size_t units = (size_t)c.n_pieces * H;
+      runs[i].piece_log += i * units;
+      runs[i].piece_state += i * units * d->d_k * d->d_v;
+    }
+  }
+  {  // dq_i = sum_{j <= i} (dO_i . v_j) k_j: the state is the forward's, transposed
+    Run &r = runs[0];
+    r.x = dO; r.Hx = H; r.y = v; r.Hy = H; r.z = k; r.Hz = Hq;
+    r.dy = d->d_v; r.dz = d->d_k;
+    r.start = S0; r.start_t = 1; r.fin = fin; r.fin_t = 1;
+    r.out = shared ? part_q : dq; r.out_f32 = shared;
+    if (dlog_a) { r.m = q; r.Hm = Hq; r.dots = dots_q; }
+    if (marks) r.marks = floats(L.off_marks[0]);
+  }
+  {  // dv_j = sum_{i >= j} (k_j . q_i) dO_i: the state is dLoss/dS
+    Run &r = runs[1];
+    r.back = 1;
+    r.x = k; r.Hx = Hq; r.y = q; r.Hy = Hq; r.z = dO; r.Hz = H;
+    r.dy = d->d_k; r.dz = d->d_v;
+    r.start = dS_T; r.fin = dS0;
+    r.out = dv;
+  }
+  {  // dk_j = sum_{i >= j} (v_j . dO_i) q_i
+    Run &r = runs[2];
+    r.back = 1;
+    r.x = v; r.Hx = H; r.y = dO; r.Hy = H; r.z = q; r.Hz = Hq;
+    r.dy = d->d_v; r.dz = d->d_k;
+    r.start = dS_T; r.start_t = 1;
+    r.out = shared ? part_k : dk; r.out_f32 = shared;
+    if (dlog_a) { r.m = k; r.Hm = Hq; r.dots = dots_k; }
+    if (marks) {
+      r.marks = floats(L.off_marks[plan.together ? 1 : 0]);
+      if (!plan.together) r.mark_dots = mark_dots;
+    }
+  }
   cudaError_t e;
-
-  Run r = base;  // dq_i = sum_{j <= i} (dO_i . v_j) k_j: the state is the forward's, transposed
-  r.x = dO; r.Hx = H; r.y = v; r.Hy = H; r.z = k; r.Hz = Hq;
-  r.dy = d->d_v; r.dz = d->d_k;
-  r.start = S0; r.start_t = 1; r.fin = fin; r.fin_t = 1;
-  r.out = shared ? part : dq; r.out_f32 = shared;
-  if (dlog_a) { r.m = q; r.Hm = Hq; r.dots = dots_q; r.marks = marks; }
-  if ((e = full_run(r, 2, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dq run", e);
-  if (shared && (e = gdn2::lin::launch_group_sum(part, dq, c, Hq, d->d_k, d->dtype_in, s)) != cudaSuccess)
-    return cuda_fail("linattn dq head sum", e);
-
-  r = base;  // dv_j = sum_{i >= j} (k_j . q_i) dO_i: the state is dLoss/dS
-  r.back = 1;
-  r.x = k; r.Hx = Hq; r.y = q; r.Hy = Hq; r.z = dO; r.Hz = H;
-  r.dy = d->d_k; r.dz = d->d_v;
-  r.start = dS_T; r.fin = dS0;
-  r.out = dv;
-  if ((e = full_run(r, 4, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dv run", e);
-
-  r = base;  // dk_j = sum_{i >= j} (v_j . dO_i) q_i
-  r.back = 1;
-  r.x = v; r.Hx = H; r.y = dO; r.Hy = H; r.z = q; r.Hz = Hq;
-  r.dy = d->d_v; r.dz = d->d_k;
-  r.start = dS_T; r.start_t = 1;
-  r.out = shared ? part : dk; r.out_f32 = shared;
-  if (dlog_a) { r.m = k; r.Hm = Hq; r.dots = dots_k; r.marks = marks; r.mark_dots = mark_dots; }
-  if ((e = full_run(r, 2, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dk run", e);
-  if (shared && (e = gdn2::lin::launch_group_sum(part, dk, c, Hq, d->d_k, d->dtype_in, s)) != cudaSuccess)
-    return cuda_fail("linattn dk head sum", e);
+  auto sum = [&](const float *part, void *out) { return gdn2::lin::launch_group_sum(part, out, c, Hq, d->d_k, d->dtype_in, s); };
+  if (plan.together) {
+    if ((e = full_runs(runs, 3, 0, status, tc, s)) != cudaSuccess) return cuda_fail("linattn gradient runs", e);
+    if (marks && c.t_total > 0 &&
+        (e = gdn2::lin::launch_marks(floats(L.off_marks[0]), floats(L.off_marks[1]), mark_dots, c, s)) != cudaSuccess)
+      return cuda_fail("linattn states' products", e);
+    if (shared && ((e = sum(part_q, dq)) != cudaSuccess || (e = sum(part_k, dk)) != cudaSuccess))
+      return cuda_fail("linattn head sums", e);
+  } else {
+    if ((e = full_runs(&runs[0], 1, 2, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dq run", e);
+    if (shared && (e = sum(part_q, dq)) != cudaSuccess) return cuda_fail("linattn dq head sum", e);
+    if ((e = full_runs(&runs[1], 1, 4, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dv run", e);
+    if ((e = full_runs(&runs[2], 1, 2, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dk run", e);
+    if (shared && (e = sum(part_k, dk)) != cudaSuccess) return cuda_fail("linattn dk head sum", e);
+  }
   if (dlog_a) {
     const int n = gdn2::lin::simt_slices(d->d_k);
     e = tc ? gdn2::lin::launch_dlog_tc(dots_q, dots_k, mark_dots, c, !S0, dlog_a, s)
@@ -329,7 +397,7 @@ int gdn2_linattn_fwd(const void *q, const void *k, const void *v, const void *lo
   r.x = q; r.Hx = dims->n_qk_heads; r.y = k; r.Hy = dims->n_qk_heads; r.z = v; r.Hz = dims->n_heads;
   r.dy = dims->d_k; r.dz = dims->d_v;
   r.start = S0; r.fin = S_T; r.out = o;
-  if ((e = full_run(r, 4, reinterpret_cast<int32_t *>(ws), tensor_core(dims), s)) != cudaSuccess) return cuda_fail("linattn run", e);
+  if ((e = full_runs(&r, 1, 4, reinterpret_cast<int32_t *>(ws), tensor_core(dims), s)) != cudaSuccess) return cuda_fail("linattn run", e);
   return GDN2_OK;
 }
 
@@ -362,7 +430,7 @@ int gdn2_linattn_step(const void *q, const void *k, const void *v, const void *l
 size_t gdn2_linattn_bwd_workspace_size(const gdn2_linattn_dims *dims, int32_t packed) {
   clear_error();
   if (check_dims(dims, true) || check_sizes(dims, packed != 0)) return 0;
-  return bwd_layout(dims, make_cut(dims, nullptr, packed != 0), false).total;
+  return bwd_layout(dims, plan_bwd(dims, nullptr, packed != 0), false).total;
 }
 
 int gdn2_linattn_bwd(const void *q, const void *k, const void *v, const void *log_a, const float *S0,
@@ -377,15 +445,15 @@ int gdn2_linattn_bwd(const void *q, const void *k, const void *v, const void *lo
   rc = check_tensors(tokens_of(dims, cu_seqlens != nullptr), rows, 3);
   if (!rc) rc = check_bwd(dims, log_a, S0, cu_seqlens, dO, dS_T, dq, dk, dv, dlog_a, dS0);
   if (rc) return rc;
-  Cut c = make_cut(dims, cu_seqlens, cu_seqlens != nullptr);
-  const BwdLayout L = bwd_layout(dims, c, false);
+  BwdPlan plan = plan_bwd(dims, cu_seqlens, cu_seqlens != nullptr);
+  const BwdLayout L = bwd_layout(dims, plan, false);
   rc = check_workspace(workspace, workspace_bytes, L.total);
   if (rc) return rc;
   char *ws = static_cast<char *>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = prepare(c, ws, L.cut, s);
+  const cudaError_t e = prepare(plan.cut, ws, L.cut, s);
   if (e != cudaSuccess) return cuda_fail("linattn workspace", e);
-  return bwd_runs(q, k, v, log_a, S0, dO, dS_T, dq, dk, dv, dlog_a, dS0, dims, c, ws, L, s);
+  return bwd_runs(q, k, v, log_a, S0, dO, dS_T, dq, dk, dv, dlog_a, dS0, dims, plan, ws, L, s);
 }
 
 int gdn2_ckpt8_save(const void *x, int8_t *codes, uint8_t *scales, int64_t rows, int32_t cols, int32_t dtype,
@@ -410,7 +478,7 @@ int gdn2_ckpt8_restore(const int8_t *codes, const uint8_t *scales, void *x, int6
 size_t gdn2_linattn_bwd_ckpt8_workspace_size(const gdn2_linattn_dims *dims, int32_t packed) {
   clear_error();
   if (check_dims(dims, true) || check_sizes(dims, packed != 0)) return 0;
-  return bwd_layout(dims, make_cut(dims, nullptr, packed != 0), true).total;
+  return bwd_layout(dims, plan_bwd(dims, nullptr, packed != 0), true).total;
 }
 
 int gdn2_linattn_bwd_ckpt8(const int8_t *q_codes, const uint8_t *q_scales, const int8_t *k_codes,
@@ -429,13 +497,13 @@ int gdn2_linattn_bwd_ckpt8(const int8_t *q_codes, const uint8_t *q_scales, const
   if (T > 0 && (!q_scales || !k_scales || !v_scales)) return fail(GDN2_ERR_INVALID_ARG, "a scales pointer is NULL");
   rc = check_bwd(dims, log_a, S0, cu_seqlens, dO, dS_T, dq, dk, dv, dlog_a, dS0);
   if (rc) return rc;
-  Cut c = make_cut(dims, cu_seqlens, cu_seqlens != nullptr);
-  const BwdLayout L = bwd_layout(dims, c, true);
+  BwdPlan plan = plan_bwd(dims, cu_seqlens, cu_seqlens != nullptr);
+  const BwdLayout L = bwd_layout(dims, plan, true);
   rc = check_workspace(workspace, workspace_bytes, L.total);
   if (rc) return rc;
   char *ws = static_cast<char *>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = prepare(c, ws, L.cut, s);
+  cudaError_t e = prepare(plan.cut, ws, L.cut, s);
   if (e != cudaSuccess) return cuda_fail("linattn workspace", e);
   const int8_t *codes[3] = {q_codes, k_codes, v_codes};
   const uint8_t *scales[3] = {q_scales, k_scales, v_scales};
@@ -446,7 +514,7 @@ int gdn2_linattn_bwd_ckpt8(const int8_t *q_codes, const uint8_t *q_scales, const
     if (e != cudaSuccess) return cuda_fail("ckpt8 restore launch", e);
   }
   return bwd_runs(ws + L.off_restored[0], ws + L.off_restored[1], ws + L.off_restored[2], log_a, S0, dO,
-                  dS_T, dq, dk, dv, dlog_a, dS0, dims, c, ws, L, s);
+                  dS_T, dq, dk, dv, dlog_a, dS0, dims, plan, ws, L, s);
 }
 
 }  // extern "C"

@@ -177,17 +177,20 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile i
   return true;
 }
 
-template <bool BACK, int NT>
-__global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_constant__ TcRun P) {
+// WAY: 0 forward, 1 backward, 2 as the run says (97 KB of code for 78, and 3 to 9% more time a chunk:
+// only the launch that needs both ways at once takes it).
+template <int WAY, int NT>
+__device__ __forceinline__ void run_block(const TcRun &P, int block) {
   constexpr int SLICE = 128 / NT;     // tokens of a slice of w o Y: NT terms in 64 columns, two slots
   constexpr int SLICES = C / SLICE;
   extern __shared__ __align__(1024) uint8_t smem[];
   const Run &r = P.r;
+  const bool BACK = WAY == 2 ? r.back != 0 : WAY == 1;
   const uint32_t sb = ptx::smem_u32(smem);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int H = r.cut.H;
   Piece pc;
-  if (!find_unit(r.cut, blockIdx.x, &pc)) return;
+  if (!find_unit(r.cut, block, &pc)) return;
   const int unit = pc.unit, h = unit % H;
   const bool only = r.state_only != 0;
   if (only && (pc.count < 2 || pc.s == (BACK ? 0 : pc.count - 1))) return;
@@ -235,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
       const int hx = h / (H / r.Hx), hy = h / (H / r.Hy), hz = h / (H / r.Hz);
-      const bool skip = P.dbg_skip && blockIdx.x == 0;
+      const bool skip = P.dbg_skip && block == 0;
       int k_yz = 0, k_x = 0;  // loads asked for
       for (int k = 0; k < nch; ++k) {
         const int s = k & 1, t0 = pc.t0 + chunk_no(k) * C;
@@ -723,8 +726,6 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
       const int s = k & 1;
       const uint32_t par = (uint32_t)(k >> 1);
       const bool last = k == nch;
-      // the state before the k-th chunk walked: its copy for X S, and scaled back where due
-      // the first slice, while the last update still runs
       if (!last) {
         const int rows = rows_of(k);
         const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile;
@@ -743,10 +744,12 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
           if (lane == 0) ptx::mbar_arrive(bar(BAR_CLEAN));
           if (!wait_warp(BAR_CLEAN, 0u)) break;  // other warps' rows are read too
         }
+        // the first slice, while the last update still runs
         if (!weigh_slices(k, 0, 1)) break;
       } else if (!wait_warp(BAR_DEC + s, par)) {
         break;
       }
+      // the state before the k-th chunk walked: its copy for X S, and scaled back where due
       const uint32_t gs = dec + DEC_W + (uint32_t)s * DEC_STAGE + DEC_G;
       const float behind = lds_f32(gs), back = last ? 1.f : lds_f32(gs + 4);
       const float2 behind2 = make_float2(behind, behind);
@@ -771,10 +774,12 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
           const int no = chunk_no(k);  // forward: the group in front of chunk k is done; backward: k's begins
           if (BACK && !last && ends_group(no)) {
             mu = mark_unit(no / kGroup);
-            mark_in = r.marks + mu * (D * D) + 4 * yrow;
+            if (WAY == 1 || r.mark_dots) mark_in = r.marks + mu * (D * D) + 4 * yrow;
+            else mark_out = r.marks + mu * (D * D) + 4 * yrow;
           }
           if (!BACK && k && ends_group(k - 1)) mark_out = r.marks + mark_unit((k - 1) / kGroup) * (D * D) + 4 * yrow;
-          if (BACK && !last && no % kGroup == 1 && no > kGroup) {  // the next group's mark, two chunks ahead
+          // the next group's mark, two chunks ahead
+          if (BACK && (WAY == 1 || r.mark_dots) && !last && no % kGroup == 1 && no > kGroup) {
             const char *next = reinterpret_cast<const char *>(r.marks + mark_unit(no / kGroup - 1) * (D * D)) + stid * 128;
             prefetch_l2(next);
             prefetch_l2(next + 32768);
@@ -851,6 +856,42 @@ __global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_consta
   }
 }
 
+template <int WAY, int NT>
+__global__ void __launch_bounds__(kThreads, 1) run_tc_kernel(const __grid_constant__ TcRun P) {
+  run_block<WAY, NT>(P, blockIdx.x);
+}
+// The three runs of the gradients side by side (dq, dv, dk), where one alone leaves SMs idle or would
+// need its sequences cut.  All with the terms that dv needs: a body for each number of terms made the
+// kernel larger than the instruction caches hold, and every chunk slower.
+struct TcGrads {
+  TcRun run[3];
+};
+__global__ void __launch_bounds__(kThreads, 1) grads_tc_kernel(const __grid_constant__ TcGrads P) {
+  run_block<2, 4>(P.run[blockIdx.x % 3], blockIdx.x / 3);
+}
+
+// mark_dots of two runs' marks.
+__global__ void __launch_bounds__(256) marks_kernel(const float *a, const float *b, float *mark_dots, Cut c) {
+  static_assert(kMarkDots == 8, "a partial sum a warp");
+  const int H = c.H, unit = blockIdx.x, h = unit % H;
+  Piece pc;
+  if (!find_piece(c, unit / H, &pc)) return;
+  for (int g = blockIdx.y; g * kGroup * C < pc.len; g += gridDim.y) {
+    const size_t mu = (size_t)mark_slot(unit / H, pc.t0 + g * kGroup * C) * H + h;
+    const float4 *x = reinterpret_cast<const float4 *>(a + mu * (D * D)) + threadIdx.x;
+    const float4 *y = reinterpret_cast<const float4 *>(b + mu * (D * D)) + threadIdx.x;
+    float dot = 0.f;
+#pragma unroll 8
+    for (int j = 0; j < D * D / 1024; ++j) {
+      const float4 v = x[j * 256], w = y[j * 256];
+      dot = fmaf(v.x, w.x, fmaf(v.y, w.y, fmaf(v.z, w.z, fmaf(v.w, w.w, dot))));
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+    if ((threadIdx.x & 31) == 0) mark_dots[mu * kMarkDots + (threadIdx.x >> 5)] = dot;
+  }
+}
+
 // dlog_a_t = sum_{t <= i in the group} (q_i . dq_i - k_i . dk_i) + <S, dLoss/dS> behind the group.  The dots carry
 // bf16 products whose errors would add up along a sequence; the marks' product starts each group afresh.
 // A warp per group of kGroup chunks.
@@ -891,44 +932,69 @@ __global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *d
   }
 }
 
-template <bool BACK, int NT>
-cudaError_t launch_t(const TcRun &P, cudaStream_t s) {
-  auto kern = run_tc_kernel<BACK, NT>;
-  static std::atomic<uint64_t> ready{0};  // a bit for each device that has been told
+// Dynamic shared memory of a kernel, once for each device.
+template <typename Kernel>
+cudaError_t prepare_kernel(Kernel kern, std::atomic<uint64_t> &ready) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev <= 63 && (ready.load(std::memory_order_relaxed) >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e == cudaSuccess && dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
+
+template <int WAY, int NT>
+cudaError_t launch_t(const TcRun &P, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = prepare_kernel(run_tc_kernel<WAY, NT>, ready);
   if (e != cudaSuccess) return e;
-  if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-    if (e != cudaSuccess) return e;
-    if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-  }
-  kern<<<(unsigned)((int64_t)P.r.cut.n_pieces * P.r.cut.H), kThreads, kSmemBytes, s>>>(P);
+  run_tc_kernel<WAY, NT><<<(unsigned)((int64_t)P.r.cut.n_pieces * P.r.cut.H), kThreads, kSmemBytes, s>>>(P);
   return cudaGetLastError();
+}
+
+bool fill(TcRun *P, const Run &r, int32_t *status, uint64_t hook_ns) {
+  memset(P, 0, sizeof(*P));
+  P->r = r;
+  P->status = status;
+  P->wait_ns = hook_ns ? hook_ns : kWaitNs;
+  P->dbg_skip = hook_ns != 0;
+  const int64_t T = r.cut.t_total;
+  if (T == 0) return true;
+  bool ok = make_row_tile_map(&P->tm_y, r.y, T, r.Hy, C) && make_row_tile_map(&P->tm_z, r.z, T, r.Hz, C);
+  if (ok && !r.state_only) ok = make_row_tile_map(&P->tm_x, r.x, T, r.Hx, C);
+  if (ok && !r.state_only && !r.out_f32) ok = make_row_tile_map(&P->tm_o, r.out, T, r.cut.H, 32);
+  return ok;
 }
 
 }  // namespace
 
 cudaError_t launch_run_tc(const Run &r, int terms, int32_t *status, cudaStream_t s) {
-  TcRun P;
-  memset(&P, 0, sizeof(P));
-  P.r = r;
-  P.status = status;
-  P.wait_ns = kWaitNs;
-  const int64_t T = r.cut.t_total;
-  if (T > 0) {
-    bool ok = make_row_tile_map(&P.tm_y, r.y, T, r.Hy, C) && make_row_tile_map(&P.tm_z, r.z, T, r.Hz, C);
-    if (ok && !r.state_only) ok = make_row_tile_map(&P.tm_x, r.x, T, r.Hx, C);
-    if (ok && !r.state_only && !r.out_f32) ok = make_row_tile_map(&P.tm_o, r.out, T, r.cut.H, 32);
-    if (!ok) return cudaErrorInvalidValue;
-  }
   uint64_t hook_ns = 0;
-  if (take_debug_timeout(GDN2_DEBUG_LINATTN, &hook_ns)) {
-    P.dbg_skip = 1;
-    P.wait_ns = hook_ns;
-  }
-  if (r.back) return terms == 4 ? launch_t<true, 4>(P, s) : launch_t<true, 2>(P, s);
-  return terms == 4 ? launch_t<false, 4>(P, s) : launch_t<false, 2>(P, s);
+  if (!take_debug_timeout(GDN2_DEBUG_LINATTN, &hook_ns)) hook_ns = 0;
+  TcRun P;
+  if (!fill(&P, r, status, hook_ns)) return cudaErrorInvalidValue;
+  if (r.back) return terms == 4 ? launch_t<1, 4>(P, s) : launch_t<1, 2>(P, s);
+  return terms == 4 ? launch_t<0, 4>(P, s) : launch_t<0, 2>(P, s);
+}
+
+cudaError_t launch_grads_tc(const Run *r, int32_t *status, cudaStream_t s) {
+  uint64_t hook_ns = 0;
+  if (!take_debug_timeout(GDN2_DEBUG_LINATTN, &hook_ns)) hook_ns = 0;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = prepare_kernel(grads_tc_kernel, ready);
+  if (e != cudaSuccess) return e;
+  TcGrads P;
+  for (int i = 0; i < 3; ++i)
+    if (!fill(&P.run[i], r[i], status, hook_ns)) return cudaErrorInvalidValue;
+  grads_tc_kernel<<<(unsigned)(3 * (int64_t)r[0].cut.n_pieces * r[0].cut.H), kThreads, kSmemBytes, s>>>(P);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_marks(const float *a, const float *b, float *mark_dots, const Cut &c, cudaStream_t s) {
+  const int64_t groups = (int64_t)c.t_total / (kGroup * C) + 1;  // of the longest piece, at most
+  const dim3 grid((unsigned)((int64_t)c.n_pieces * c.H), (unsigned)(groups < 32 ? groups : 32));
+  marks_kernel<<<grid, 256, 0, s>>>(a, b, mark_dots, c);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_dlog_tc(const float *dots_q, const float *dots_k, const float *mark_dots, const Cut &c, bool no_start,
