@@ -211,10 +211,6 @@ BwdPlan plan_bwd(const gdn2_linattn_dims *d, const int32_t *cu, bool packed) {
   const bool idle = 2 * (int64_t)d->n_seqs * d->n_heads <= sm_count();
   p.together = !tensor_core(d) || has_cuts(p.cut) || idle;
   if (p.together) p.cut = make_cut(d, cu, packed, 3);
-  if (tensor_core(d) && p.together && 3 * (int64_t)p.cut.n_pieces * d->n_heads > INT32_MAX) {  // a grid's blocks
-    p.cut = make_cut(d, cu, packed);
-    p.together = false;
-  }
   return p;
 }
 

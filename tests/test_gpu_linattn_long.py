@@ -64,6 +64,14 @@ def test_ragged_batch_of_more_units_than_blocks_run_at_once(g, dtype, dk, dv):
     _check_units(g, p, cu, 32, 16, dtype == BF, [(1, 0), (4, 31), (6, 7), (11, 16)])
 
 
+@pytest.mark.parametrize("decay", ["token", "head"])
+@pytest.mark.parametrize("lens", [(1700, 900, 40, 0, 1), (129, 300, 0, 7)])
+def test_gradients_side_by_side(g, lens, decay):
+    """Few units: the three gradients share a launch, with sequences cut and uncut, of shared q and k."""
+    p, cu = ref.problem(lens, 4, 2, 128, 128, BF, decay, True, seed=39)
+    _check_units(g, p, cu, 4, 2, True, [(0, 0), (1, 2), (3, 0), (len(lens) - 1, 2)])
+
+
 @pytest.mark.parametrize("la", [-0.05, -0.17, -0.18, -0.36, -103.0, -104.5])
 def test_decays_on_both_sides_of_the_limits(g, la):
     """A chunk of 128 tokens decays by 2^-32 at log_a = -0.1733: below it the state's accumulator is
@@ -95,6 +103,22 @@ def test_wait_times_out_then_recovers(g):
     want = ref.forward(p, cu, 2, 2, True)
     ref.check("o", o, *want["o"])
     ref.check("S_T", S, *want["S_T"])
+
+
+@pytest.mark.parametrize("heads", [2, 80])
+def test_wait_of_the_gradients_times_out_then_recovers(g, heads):
+    """The same with the three runs in one launch (2 heads), and one after the other (80)."""
+    p, cu = ref.problem((300, 40), heads, heads, 128, 128, BF, "token", True, seed=40)
+    args = [p[x] for x in ("q", "k", "v", "log_a", "dO", "S0", "dS_T", "cu")]
+    want = g.linattn_bwd(*args)
+    assert g.check_status(want["workspace"]) == g.OK
+    g.debug_timeout_once(g.DEBUG_LINATTN, 1_000_000)
+    ws = g.linattn_bwd(*args)["workspace"]
+    assert g.check_status(ws) == g.ERR_TIMEOUT
+    got = g.linattn_bwd(*args, workspace=ws)
+    assert g.check_status(ws) == g.OK
+    for name in ("dq", "dk", "dv", "dlog_a", "dS0"):
+        assert torch.equal(got[name], want[name])
 
 
 def test_two_graphs_and_their_workspaces(g):
