@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(Cut c, int32_t *seg_off, int
     if (n < c.n_seqs) {
       int t0, len;
       seq_bounds(c, n, &t0, &len);
-      v = piece_count(len, c.target);
+      v = piece_count(len, c.target, c.grain);
     }
     int incl = v;
 #pragma unroll
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Runs 
 // bytes, and they bound it about alike (token by token, a chain of shuffles and dependent sums
 // for each, it took 54 us for 32 tokens).  The decays are summed in whole numbers of 2^-32: a tile may
 // hold resets beside weak decays, and differences of their sums have to stay exact.
-constexpr int TB = 32;
+constexpr int TB = kTile32;
 constexpr int COLS = 64;
 constexpr int kRunThreads = 256;
 

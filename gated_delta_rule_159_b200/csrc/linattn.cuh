@@ -8,9 +8,10 @@
 namespace gdn2 {
 namespace lin {
 
-// Sequences cut into pieces of whole 128-token chunks.  A sequence of at least two `target`s of
-// tokens is cut into len / target pieces; the rest stay whole.
+// Sequences cut into pieces of whole steps (chunks of the tensor-core run, tiles of the fp32 run).  A
+// sequence of at least two `target`s of tokens is cut into len / target pieces; the rest stay whole.
 constexpr int kChunk = 128;
+constexpr int kTile32 = 32;  // tokens of a step of the fp32 run
 constexpr int kNoCut = 0x7fffffff;
 struct Cut {
   const int32_t *cu;       // device [n_seqs + 1] token offsets, or NULL: n_seqs x seq_len tokens
@@ -22,20 +23,20 @@ struct Cut {
   int n_seqs, seq_len, H;
   int per_seq;             // pieces per sequence without seg_off
   int n_pieces;            // pieces in all (an upper bound with seg_off)
-  int target;
+  int target, grain;       // pieces are cut at multiples of grain
   int t_total;
   int sorted;              // the call asks for an order
 };
 
 // Length of the pieces of a sequence of `len` tokens, and their number.
-__host__ __device__ inline int piece_len(int len, int target) {
+__host__ __device__ inline int piece_len(int len, int target, int grain) {
   const int count = len / target;
   if (count < 2) return len > 0 ? len : 1;
   const int each = (len + count - 1) / count;
-  return (each + kChunk - 1) / kChunk * kChunk;
+  return (each + grain - 1) / grain * grain;
 }
-__host__ __device__ inline int piece_count(int len, int target) {
-  const int pl = piece_len(len, target);
+__host__ __device__ inline int piece_count(int len, int target, int grain) {
+  const int pl = piece_len(len, target, grain);
   return len > 0 ? (len + pl - 1) / pl : 1;
 }
 
@@ -77,7 +78,7 @@ __device__ __forceinline__ bool find_piece(const Cut &c, int g, Piece *p) {
   }
   int t0, len;
   seq_bounds(c, n, &t0, &len);
-  const int pl = piece_len(len, c.target);
+  const int pl = piece_len(len, c.target, c.grain);
   p->n = n;
   p->s = g - first;
   p->count = c.seg_off ? c.seg_off[n + 1] - first : c.per_seq;

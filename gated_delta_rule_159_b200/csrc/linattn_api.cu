@@ -81,7 +81,10 @@ Cut make_cut(const gdn2_linattn_dims *d, const int32_t *cu, bool packed, int run
   const int slices = tc ? 1 : gdn2::lin::simt_slices(d->d_k < d->d_v ? d->d_k : d->d_v);
   const int64_t workers = tc ? sms : 2 * (int64_t)sms;
   int64_t target = (T * d->n_heads * slices * runs + workers - 1) / workers;
-  const int64_t least = tc ? 512 : 128;
+  // Pieces no shorter than what a pass over their states costs: 512 tokens on the tensor cores; in fp32,
+  // where a step of 32 tokens is long, one step (4 heads of 32 x 32, 600 tokens: 37 us, from pieces of
+  // 64 on 43, of 128 on 78; 3 ragged sequences' gradients, 1201 tokens, 48 x 80: 111, 115 and 162 us).
+  const int64_t least = tc ? 512 : gdn2::lin::kTile32;
   if (target < least) target = least;
   Cut c;
   memset(&c, 0, sizeof(c));
@@ -91,13 +94,14 @@ Cut make_cut(const gdn2_linattn_dims *d, const int32_t *cu, bool packed, int run
   c.H = d->n_heads;
   c.t_total = (int)T;
   c.target = target < gdn2::lin::kNoCut / 2 ? (int)target : gdn2::lin::kNoCut;
+  c.grain = tc ? gdn2::lin::kChunk : gdn2::lin::kTile32;
   if (packed) {
     const bool any = T / c.target >= 2;
     if (!any) c.target = gdn2::lin::kNoCut;
     c.per_seq = 1;
     c.n_pieces = any ? (int)(d->n_seqs + T / c.target) : d->n_seqs;
   } else {
-    c.per_seq = gdn2::lin::piece_count(d->seq_len, c.target);
+    c.per_seq = gdn2::lin::piece_count(d->seq_len, c.target, c.grain);
     c.n_pieces = d->n_seqs * c.per_seq;
   }
   c.sorted = packed && c.n_pieces > 1 && c.n_pieces <= gdn2::lin::kMaxSorted && (int64_t)c.n_pieces * c.H * slices * runs > workers;
