@@ -349,6 +349,18 @@ int check_bwd(const gdn2_linattn_dims *d, const void *log_a, const float *S0, co
   return GDN2_OK;
 }
 
+// Outputs are written while inputs are still read, and not in one order for all sizes.
+int check_apart(const void *const *out, int n_out, const void *const *in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    if (!out[i]) continue;
+    for (int j = 0; j < i; ++j)
+      if (out[i] == out[j]) return fail(GDN2_ERR_INVALID_ARG, "two outputs share the address %p", out[i]);
+    for (int j = 0; j < n_in; ++j)
+      if (out[i] == in[j]) return fail(GDN2_ERR_INVALID_ARG, "an output has an input's address %p", out[i]);
+  }
+  return GDN2_OK;
+}
+
 int check_ckpt8(const void *x, const int8_t *codes, const uint8_t *scales, int64_t rows, int32_t cols, int32_t dtype) {
   if (rows < 0 || cols < 1) return fail(GDN2_ERR_INVALID_ARG, "bad shape (rows=%lld cols=%d)", (long long)rows, cols);
   if (dtype != GDN2_BF16 && dtype != GDN2_F32) return fail(GDN2_ERR_INVALID_ARG, "bad dtype=%d", dtype);
@@ -388,6 +400,8 @@ int gdn2_linattn_fwd(const void *q, const void *k, const void *v, const void *lo
   Cut c = make_cut(dims, cu_seqlens, cu_seqlens != nullptr);
   const CutLayout L = cut_layout(c, kHeader, (size_t)dims->d_k * dims->d_v);
   rc = check_workspace(workspace, workspace_bytes, L.end);
+  const void *in[4] = {q, k, v, log_a}, *out[1] = {o};
+  if (!rc) rc = check_apart(out, 1, in, 4);
   if (rc) return rc;
   char *ws = static_cast<char *>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -415,6 +429,9 @@ int gdn2_linattn_step(const void *q, const void *k, const void *v, const void *l
   if (!S || !aligned(S, 16)) return fail(GDN2_ERR_INVALID_ARG, "S must be non-NULL and 16-byte aligned");
   if (state_idx && n_slots < 1) return fail(GDN2_ERR_INVALID_ARG, "n_slots must be at least 1 (got %d)", n_slots);
   if (!aligned(state_idx, 4)) return fail(GDN2_ERR_INVALID_ARG, "state_idx is misaligned");
+  const void *in[4] = {q, k, v, log_a}, *out[2] = {o, S};
+  rc = check_apart(out, 2, in, 4);
+  if (rc) return rc;
   gdn2::lin::StepProblem p;
   memset(&p, 0, sizeof(p));
   p.q = q; p.k = k; p.v = v; p.log_a = log_a; p.S = S; p.state_idx = state_idx; p.o = o;
@@ -448,6 +465,8 @@ int gdn2_linattn_bwd(const void *q, const void *k, const void *v, const void *lo
   BwdPlan plan = plan_bwd(dims, cu_seqlens, cu_seqlens != nullptr);
   const BwdLayout L = bwd_layout(dims, plan, false);
   rc = check_workspace(workspace, workspace_bytes, L.total);
+  const void *in[7] = {q, k, v, log_a, dO, S0, dS_T}, *out[5] = {dq, dk, dv, dlog_a, dS0};
+  if (!rc) rc = check_apart(out, 5, in, 7);
   if (rc) return rc;
   char *ws = static_cast<char *>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -461,6 +480,9 @@ int gdn2_ckpt8_save(const void *x, int8_t *codes, uint8_t *scales, int64_t rows,
   clear_error();
   int rc = check_ckpt8(x, codes, scales, rows, cols, dtype);
   if (rc || rows == 0) return rc;
+  const void *out[2] = {codes, scales}, *in[1] = {x};
+  rc = check_apart(out, 2, in, 1);
+  if (rc) return rc;
   const cudaError_t e = gdn2::launch_ckpt8_save(x, codes, scales, rows, cols, dtype, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GDN2_OK : cuda_fail("ckpt8 save launch", e);
 }
@@ -470,6 +492,9 @@ int gdn2_ckpt8_restore(const int8_t *codes, const uint8_t *scales, void *x, int6
   clear_error();
   int rc = check_ckpt8(x, codes, scales, rows, cols, dtype);
   if (rc || rows == 0) return rc;
+  const void *out[1] = {x}, *in[2] = {codes, scales};
+  rc = check_apart(out, 1, in, 2);
+  if (rc) return rc;
   const cudaError_t e =
       gdn2::launch_ckpt8_restore(codes, scales, x, rows, cols, dtype, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GDN2_OK : cuda_fail("ckpt8 restore launch", e);
@@ -500,6 +525,9 @@ int gdn2_linattn_bwd_ckpt8(const int8_t *q_codes, const uint8_t *q_scales, const
   BwdPlan plan = plan_bwd(dims, cu_seqlens, cu_seqlens != nullptr);
   const BwdLayout L = bwd_layout(dims, plan, true);
   rc = check_workspace(workspace, workspace_bytes, L.total);
+  const void *in[10] = {q_codes, q_scales, k_codes, k_scales, v_codes, v_scales, log_a, dO, S0, dS_T};
+  const void *out[5] = {dq, dk, dv, dlog_a, dS0};
+  if (!rc) rc = check_apart(out, 5, in, 10);
   if (rc) return rc;
   char *ws = static_cast<char *>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

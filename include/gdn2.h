@@ -485,7 +485,8 @@ typedef struct gdn2_linattn_dims {
  *   log_a        [T_tot, H] dtype_in, or fp32 [H] with GDN2_LINATTN_HEAD_DECAY
  *   S0           [N, H, d_k, d_v] fp32 or NULL for zeros.  May alias S_T.
  *   cu_seqlens   device int32 [N + 1] token offsets, or NULL: N sequences of seq_len tokens
- *   o            [T_tot, H, d_v] dtype_out = dtype_in (written; rows outside every sequence stay)
+ *   o            [T_tot, H, d_v] dtype_out = dtype_in (written; rows outside every sequence stay);
+ *                must not alias an input
  *   S_T          [N, H, d_k, d_v] fp32 or NULL
  *   workspace    at least gdn2_linattn_fwd_workspace_size(dims, cu_seqlens != NULL) bytes, 256-byte
  *                aligned, uninitialised; one call at a time.  The size depends on the current
@@ -507,7 +508,7 @@ size_t gdn2_linattn_fwd_workspace_size(const gdn2_linattn_dims *dims, int32_t pa
  *   state_idx  device int32 [N] or NULL, as gdn2_decode_step_indexed: an entry outside
  *              [0, n_slots) is a padding row (o row zero, no state touched); two rows naming one
  *              slot race on it.
- *   o          [N, H, d_v] dtype_out
+ *   o          [N, H, d_v] dtype_out; must not alias an input
  * dims.seq_len must be 1.
  * Errors: GDN2_ERR_INVALID_ARG, GDN2_ERR_UNSUPPORTED, GDN2_ERR_CUDA.
  */
@@ -525,6 +526,7 @@ int gdn2_linattn_step(const void *q, const void *k, const void *v, const void *l
  *                   gradient here)
  *   dS0             [N, H, d_k, d_v] fp32 or NULL to skip
  *   workspace       at least gdn2_linattn_bwd_workspace_size bytes, as for gdn2_linattn_fwd
+ * No output may alias an input or another output.
  * Errors as gdn2_linattn_fwd.
  */
 int gdn2_linattn_bwd(const void *q, const void *k, const void *v, const void *log_a, const float *S0,
@@ -542,7 +544,8 @@ size_t gdn2_linattn_bwd_workspace_size(const gdn2_linattn_dims *dims, int32_t pa
  *   scales  [rows, ceil(cols / 32)] uint8: e + 127; 255 for a block with an infinity or a NaN,
  *           which restores as NaN
  * The error is at most 2^(e-1), below max|x| / 127.  A restored value code * 2^e is exact in bf16.
- * dtype is x's (GDN2_BF16 or GDN2_F32).  x and codes are 16-byte aligned; rows may be 0.
+ * dtype is x's (GDN2_BF16 or GDN2_F32).  x and codes are 16-byte aligned; rows may be 0.  Neither
+ * works in place.
  * Errors: GDN2_ERR_INVALID_ARG, GDN2_ERR_UNSUPPORTED, GDN2_ERR_CUDA.
  */
 int gdn2_ckpt8_save(const void *x, int8_t *codes, uint8_t *scales, int64_t rows, int32_t cols,

@@ -117,6 +117,30 @@ def test_ckpt8_refusals(g):
     assert call(x=None, codes=None, scales=None, rows=0) == (g.OK,) * 2
 
 
+def test_outputs_apart_from_inputs(g):
+    """An output at an input's address, or at another output's, is refused."""
+    at = [ctypes.c_void_p((i + 1) << 20) for i in range(16)]
+    ins = dict(zip(("q", "k", "v", "log_a", "dO", "S0", "dS_T"), at))
+    outs = dict(zip(("dq", "dk", "dv", "dlog_a", "dS0"), at[8:]))
+    ws = ctypes.c_void_p(1 << 30)
+    d = _dims(g)
+    for name in ("q", "k", "v", "log_a"):
+        rc, msg = _fwd(g, d, ws=ws, q=at[0], k=at[1], v=at[2], log_a=at[3], o=ins[name])
+        assert rc == g.ERR_INVALID_ARG and "address" in msg
+        rc, msg = _step(g, _dims(g, seq_len=1), q=at[0], k=at[1], v=at[2], log_a=at[3], S=at[9], o=ins[name])
+        assert rc == g.ERR_INVALID_ARG and "address" in msg
+    for out in outs:
+        for other in [n for n in {**ins, **outs} if n != out]:
+            rc, msg = _bwd(g, d, ws=ws, **{**ins, **outs, out: {**ins, **outs}[other]})
+            assert rc == g.ERR_INVALID_ARG and "address" in msg, (out, other)
+    rc, msg = _bwd(g, d, ws=ws, ckpt8=True, qs=at[13], ks=at[14], vs=at[15], **{**ins, **outs, "dq": at[13]})
+    assert rc == g.ERR_INVALID_ARG and "address" in msg
+    for fn in (lambda a, b: g.lib.gdn2_ckpt8_save(at[0], a, b, 4, 64, g.BF16, None),
+               lambda a, b: g.lib.gdn2_ckpt8_restore(a, b, at[0], 4, 64, g.BF16, None)):
+        assert fn(at[0], at[1]) == g.ERR_INVALID_ARG and "address" in g.lib.gdn2_last_error().decode()
+        assert fn(at[1], at[0]) == g.ERR_INVALID_ARG
+
+
 def test_workspace_sizes(g):
     size = lambda d, packed=0: g.lib.gdn2_linattn_fwd_workspace_size(ctypes.byref(d), packed)  # noqa: E731
     assert size(_dims(g)) == 256                       # nothing to cut
