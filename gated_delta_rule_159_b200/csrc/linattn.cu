@@ -118,8 +118,11 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Runs 
 // Tiles of 32 tokens: G = X Y^T, P = G o D, out = P Z + f o (X S), S <- g S + (w o Y)^T Z, all in fp32 on
 // the CUDA cores.  A block takes a (piece, head) and 64 of the state's columns, which do not mix.
 // Per tile and token a block does 64 (2 dy + 64) + 32 dy multiply-adds; shared memory, read by 16
-// bytes, and they bound it about alike (token by token, a chain of shuffles and dependent sums
-// for each, it took 54 us for 32 tokens).  The decays are summed in whole numbers of 2^-32: a tile may
+// bytes, bounds it (79% of its rate with two blocks on an SM).  So a thread takes 2 x 4 of P and 4 x 4 of
+// out, over half of the sums each, which a shuffle joins: 8 x 2048 tokens' gradients of 16 heads of
+// 64 x 64 took 1580 us with 1 x 4 and 2 x 4 over whole sums and take 1260.  (Token by token, a chain of
+// shuffles and dependent sums
+// for each, it took 54 us for 32 tokens.)  The decays are summed in whole numbers of 2^-32: a tile may
 // hold resets beside weak decays, and differences of their sums have to stay exact.
 constexpr int TB = kTile32;
 constexpr int COLS = 64;
@@ -148,9 +151,9 @@ __device__ __forceinline__ void fma4(float (&acc)[4], float a, const float4 &b) 
   acc[3] = fmaf(a, b.w, acc[3]);
 }
 
-// ROWS rows of out a thread: 1 where the slice has at most 32 columns, else 2.
+// ROWS rows of out a thread: 2 where the slice has at most 32 columns, else 4.
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(kRunThreads) run_kernel(const __grid_constant__ Runs P) {
+__global__ void __launch_bounds__(kRunThreads, 2) run_kernel(const __grid_constant__ Runs P) {
   const Run &p = P.run[blockIdx.z];
   extern __shared__ __align__(16) float sm[];
   __shared__ __align__(16) float ps[TB][TB + 4];
@@ -253,79 +256,91 @@ __global__ void __launch_bounds__(kRunThreads) run_kernel(const __grid_constant_
     const float g = expf(__ll2float_rn(cum[TB - 1]) * 0x1p-32f);
 
     if (!p.state_only) {
-      {  // P: row i, columns j = c + 8 q
-        const int i = tid >> 3, c = tid & 7;
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int k = 0; k < dyp; k += 4) {
-          const float4 a = ld4(xs + i * L.ys + k);
+      {  // P: rows i, i + 1 and columns j = c + 8 q, half of the sum over k a thread
+        const int c = tid & 7, kh = tid >> 3 & 1, i0 = tid >> 4 << 1, k0 = kh * (dyp / 2);
+        float acc[2][4] = {};
+#pragma unroll 2
+        for (int k = k0; k < k0 + dyp / 2; k += 4) {
+          const float4 a0 = ld4(xs + i0 * L.ys + k), a1 = ld4(xs + (i0 + 1) * L.ys + k);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float4 b = ld4(yv + (c + 8 * q) * L.ys + k);
-            acc[q] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, acc[q]))));
+            acc[0][q] = fmaf(a0.x, b.x, fmaf(a0.y, b.y, fmaf(a0.z, b.z, fmaf(a0.w, b.w, acc[0][q]))));
+            acc[1][q] = fmaf(a1.x, b.x, fmaf(a1.y, b.y, fmaf(a1.z, b.z, fmaf(a1.w, b.w, acc[1][q]))));
           }
         }
+        const int i = i0 + kh;  // the row that this thread adds up
         const long long mine = cum[i];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          const float other = __shfl_xor_sync(0xffffffffu, kh ? acc[0][q] : acc[1][q], 8);
+          const float sum = (kh ? acc[1][q] : acc[0][q]) + other;
           const int j = c + 8 * q;
           const bool in = (p.back ? j >= i : j <= i) && j < cnt;
           const long long d = p.back ? cum[j] - mine : mine - cum[j];
-          ps[i][j] = in ? acc[q] * expf(__ll2float_rn(d) * 0x1p-32f) : 0.f;
+          ps[i][j] = in ? sum * expf(__ll2float_rn(d) * 0x1p-32f) : 0.f;
         }
       }
       __syncthreads();
-      const int rg = tid / groups;  // rows rg * ROWS ..
-      if (rg * ROWS < TB) {
+      {  // out: ROWS rows by 4 columns, half of the sums over k a thread
+        const int lane = tid & 31, half = tid >> 5 << 4 | (lane & 15), kh = lane >> 4;
+        const int oc = half % groups, og = half / groups, r0 = min(og * ROWS, TB - ROWS);
         float acc[ROWS][4];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
 #pragma unroll 2
-        for (int k = 0; k < dyp; k += 4) {
+        for (int k = kh * (dyp / 2); k < (kh + 1) * (dyp / 2); k += 4) {
           float4 a[ROWS];
 #pragma unroll
-          for (int r = 0; r < ROWS; ++r) a[r] = ld4(xs + (rg * ROWS + r) * L.ys + k);
+          for (int r = 0; r < ROWS; ++r) a[r] = ld4(xs + (r0 + r) * L.ys + k);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float4 b = ld4(ss + (k + q) * COLS + cg * 4);
+            const float4 b = ld4(ss + (k + q) * COLS + oc * 4);
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) fma4(acc[r], part4(a[r], q), b);
           }
         }
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-          const float f = fs[rg * ROWS + r];
+          const float f = fs[r0 + r];
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[r][c] *= f;
         }
 #pragma unroll 2
-        for (int k = 0; k < TB; k += 4) {
+        for (int k = kh * (TB / 2); k < (kh + 1) * (TB / 2); k += 4) {
           float4 a[ROWS];
 #pragma unroll
-          for (int r = 0; r < ROWS; ++r) a[r] = ld4(&ps[rg * ROWS + r][k]);
+          for (int r = 0; r < ROWS; ++r) a[r] = ld4(&ps[r0 + r][k]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float4 b = ld4(zs + (k + q) * COLS + cg * 4);
+            const float4 b = ld4(zs + (k + q) * COLS + oc * 4);
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) fma4(acc[r], part4(a[r], q), b);
           }
         }
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          const int t = rg * ROWS + r;
+        for (int r = 0; r < ROWS / 2; ++r) {
+          float o[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float other = __shfl_xor_sync(0xffffffffu, kh ? acc[r][c] : acc[r + ROWS / 2][c], 16);
+            o[c] = (kh ? acc[r + ROWS / 2][c] : acc[r][c]) + other;
+          }
+          const int t = r0 + kh * (ROWS / 2) + r;
+          if (og * ROWS >= TB) continue;  // the last threads of widths that do not divide them evenly
           if (m) {
-            const float4 b = ld4(ms + t * COLS + cg * 4);
-            dot[t][cg] = fmaf(acc[r][0], b.x, fmaf(acc[r][1], b.y, fmaf(acc[r][2], b.z, acc[r][3] * b.w)));
+            const float4 b = ld4(ms + t * COLS + oc * 4);
+            dot[t][oc] = fmaf(o[0], b.x, fmaf(o[1], b.y, fmaf(o[2], b.z, o[3] * b.w)));
           }
           if (t >= cnt) continue;
-          const size_t at = ((tok0 + t) * H + h) * p.dz + col0 + cg * 4;
+          const size_t at = ((tok0 + t) * H + h) * p.dz + col0 + oc * 4;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (cg * 4 + c < width) {
-              if (p.out_f32) static_cast<float *>(p.out)[at + c] = acc[r][c];
-              else static_cast<T *>(p.out)[at + c] = from_f32<T>(acc[r][c]);
+            if (oc * 4 + c < width) {
+              if (p.out_f32) static_cast<float *>(p.out)[at + c] = o[c];
+              else static_cast<T *>(p.out)[at + c] = from_f32<T>(o[c]);
             }
         }
       }
@@ -600,8 +615,8 @@ cudaError_t launch_run_simt(const Run *r, int n, cudaStream_t s) {
     if (r[i].dz > widest) widest = r[i].dz;
   const bool bf16 = r->dtype == GDN2_BF16;
   if (widest <= 32)
-    return bf16 ? launch_run_t<__nv_bfloat16, 1>(r, n, widest, s) : launch_run_t<float, 1>(r, n, widest, s);
-  return bf16 ? launch_run_t<__nv_bfloat16, 2>(r, n, widest, s) : launch_run_t<float, 2>(r, n, widest, s);
+    return bf16 ? launch_run_t<__nv_bfloat16, 2>(r, n, widest, s) : launch_run_t<float, 2>(r, n, widest, s);
+  return bf16 ? launch_run_t<__nv_bfloat16, 4>(r, n, widest, s) : launch_run_t<float, 4>(r, n, widest, s);
 }
 
 cudaError_t launch_dlog_simt(const float *dots_q, int nq, const float *dots_k, int nk, const float *S_T,
