@@ -121,9 +121,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Runs 
 // bytes, bounds it (79% of its rate with two blocks on an SM).  So a thread takes 2 x 4 of P and 4 x 4 of
 // out, over half of the sums each, which a shuffle joins: 8 x 2048 tokens' gradients of 16 heads of
 // 64 x 64 took 1580 us with 1 x 4 and 2 x 4 over whole sums and take 1260.  (Token by token, a chain of
-// shuffles and dependent sums
-// for each, it took 54 us for 32 tokens.)  The decays are summed in whole numbers of 2^-32: a tile may
-// hold resets beside weak decays, and differences of their sums have to stay exact.
+// shuffles and dependent sums for each, it took 54 us for 32 tokens.)  The decays are summed in whole
+// numbers of 2^-32: a tile may hold resets beside weak decays, and differences of their sums have to
+// stay exact.
 constexpr int TB = kTile32;
 constexpr int COLS = 64;
 constexpr int kRunThreads = 256;
@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(kScan) dlog_kernel(const float *dq, int nq, co
   if (dS_T && S_T) {
     const size_t at = (size_t)blockIdx.x * size;
     double v = 0.0;
+#pragma unroll 8
     for (int i = threadIdx.x; i < size; i += kScan) v += (double)S_T[at + i] * (double)dS_T[at + i];
     for (int b = 16; b; b >>= 1) v += __shfl_xor_sync(0xffffffffu, v, b);
     if (lane == 0) sums[warp] = v;
@@ -454,9 +455,15 @@ __global__ void __launch_bounds__(kScan) dlog_kernel(const float *dq, int nq, co
 
 // ---------------------------------------------------------------- heads that share q and k
 // A thread sums VEC columns: 16-byte loads of the parts, which are most of what it moves.
+struct Sums {
+  const float *part[2];
+  void *out[2];
+};
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) group_sum_kernel(const float *part, T *out, int64_t total, int share, int d,
+__global__ void __launch_bounds__(256) group_sum_kernel(const __grid_constant__ Sums P, int64_t total, int share, int d,
                                                         const int32_t *cu, int n_seqs, int Hg) {
+  const float *part = P.part[blockIdx.y];
+  T *out = static_cast<T *>(P.out[blockIdx.y]);
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;  // over [T, Hg, d]
   if (i >= total) return;
   const int64_t row = i / d, t = row / Hg;
@@ -630,19 +637,25 @@ cudaError_t launch_dlog_simt(const float *dots_q, int nq, const float *dots_k, i
   return cudaGetLastError();
 }
 
-cudaError_t launch_group_sum(const float *part, void *out, const Cut &c, int Hg, int d, int dtype, cudaStream_t s) {
+cudaError_t launch_group_sum(const float *const *part, void *const *out, int n, const Cut &c, int Hg, int d, int dtype,
+                             cudaStream_t s) {
   const int64_t total = (int64_t)c.t_total * Hg * d;
   const int share = c.H / Hg;
   if (total == 0) return cudaSuccess;
+  Sums P;
+  for (int i = 0; i < 2; ++i) {
+    P.part[i] = part[i < n ? i : 0];
+    P.out[i] = out[i < n ? i : 0];
+  }
   const int vec = d % 4 == 0 ? 4 : 1;
-  const unsigned grid = (unsigned)((total + 256 * vec - 1) / (256 * vec));
-  auto go = [&](auto *o) {
-    using T = std::remove_pointer_t<decltype(o)>;
-    if (vec == 4) group_sum_kernel<T, 4><<<grid, 256, 0, s>>>(part, o, total, share, d, c.cu, c.n_seqs, Hg);
-    else group_sum_kernel<T, 1><<<grid, 256, 0, s>>>(part, o, total, share, d, c.cu, c.n_seqs, Hg);
+  const dim3 grid((unsigned)((total + 256 * vec - 1) / (256 * vec)), (unsigned)n);
+  auto go = [&](auto zero) {
+    using T = decltype(zero);
+    if (vec == 4) group_sum_kernel<T, 4><<<grid, 256, 0, s>>>(P, total, share, d, c.cu, c.n_seqs, Hg);
+    else group_sum_kernel<T, 1><<<grid, 256, 0, s>>>(P, total, share, d, c.cu, c.n_seqs, Hg);
   };
-  if (dtype == GDN2_BF16) go(static_cast<__nv_bfloat16 *>(out));
-  else go(static_cast<float *>(out));
+  if (dtype == GDN2_BF16) go(__nv_bfloat16());
+  else go(0.f);
   return cudaGetLastError();
 }
 

@@ -168,8 +168,8 @@ cudaError_t launch_dlog_simt(const float *dots_q, int nq, const float *dots_k, i
 // dlog_a of the tensor-core runs (linattn_tc.cu).
 cudaError_t launch_dlog_tc(const float *dots_q, const float *dots_k, const float *mark_dots, const Cut &c, bool no_start,
                            void *dlog, cudaStream_t stream);
-// out[t, g, :] = sum over the heads of group g of part[t, h, :]
-cudaError_t launch_group_sum(const float *part, void *out, const Cut &c, int Hg, int d, int dtype,
+// out[t, g, :] = sum over the heads of group g of part[t, h, :], for n (1 or 2) of them
+cudaError_t launch_group_sum(const float *const *part, void *const *out, int n, const Cut &c, int Hg, int d, int dtype,
                              cudaStream_t stream);
 
 struct StepProblem {

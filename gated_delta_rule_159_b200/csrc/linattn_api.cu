@@ -308,20 +308,23 @@ int bwd_runs(const void *q, const void *k, const void *v, const void *log_a, con
     }
   }
   cudaError_t e;
-  auto sum = [&](const float *part, void *out) { return gdn2::lin::launch_group_sum(part, out, c, Hq, d->d_k, d->dtype_in, s); };
+  const float *parts[2] = {part_q, part_k};
+  void *outs[2] = {dq, dk};
+  auto sum = [&](int first, int n) {
+    return gdn2::lin::launch_group_sum(parts + first, outs + first, n, c, Hq, d->d_k, d->dtype_in, s);
+  };
   if (plan.together) {
     if ((e = full_runs(runs, 3, 0, status, tc, s)) != cudaSuccess) return cuda_fail("linattn gradient runs", e);
     if (marks && c.t_total > 0 &&
         (e = gdn2::lin::launch_marks(floats(L.off_marks[0]), floats(L.off_marks[1]), mark_dots, c, s)) != cudaSuccess)
       return cuda_fail("linattn states' products", e);
-    if (shared && ((e = sum(part_q, dq)) != cudaSuccess || (e = sum(part_k, dk)) != cudaSuccess))
-      return cuda_fail("linattn head sums", e);
+    if (shared && (e = sum(0, 2)) != cudaSuccess) return cuda_fail("linattn head sums", e);
   } else {
     if ((e = full_runs(&runs[0], 1, 2, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dq run", e);
-    if (shared && (e = sum(part_q, dq)) != cudaSuccess) return cuda_fail("linattn dq head sum", e);
+    if (shared && (e = sum(0, 1)) != cudaSuccess) return cuda_fail("linattn dq head sum", e);
     if ((e = full_runs(&runs[1], 1, 4, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dv run", e);
     if ((e = full_runs(&runs[2], 1, 2, status, tc, s)) != cudaSuccess) return cuda_fail("linattn dk run", e);
-    if (shared && (e = sum(part_k, dk)) != cudaSuccess) return cuda_fail("linattn dk head sum", e);
+    if (shared && (e = sum(1, 1)) != cudaSuccess) return cuda_fail("linattn dk head sum", e);
   }
   if (dlog_a) {
     const int n = gdn2::lin::simt_slices(d->d_k);
