@@ -118,9 +118,10 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Runs 
 // Tiles of 32 tokens: G = X Y^T, P = G o D, out = P Z + f o (X S), S <- g S + (w o Y)^T Z, all in fp32 on
 // the CUDA cores.  A block takes a (piece, head) and 64 of the state's columns, which do not mix.
 // Per tile and token a block does 64 (2 dy + 64) + 32 dy multiply-adds; shared memory, read by 16
-// bytes, bounds it (79% of its rate with two blocks on an SM).  So a thread takes 2 x 4 of P and 4 x 4 of
+// bytes, bounds it (79% of its rate with two blocks on an SM, now 70%).  So a thread takes 2 x 4 of P and 4 x 4 of
 // out, over half of the sums each, which a shuffle joins: 8 x 2048 tokens' gradients of 16 heads of
-// 64 x 64 took 1580 us with 1 x 4 and 2 x 4 over whole sums and take 1260.  (Token by token, a chain of
+// 64 x 64 took 1580 us with 1 x 4 and 2 x 4 over whole sums, then 1200, and with two multiply-adds an
+// instruction 1126.  (Token by token, a chain of
 // shuffles and dependent sums for each, it took 54 us for 32 tokens.)  The decays are summed in whole
 // numbers of 2^-32: a tile may hold resets beside weak decays, and differences of their sums have to
 // stay exact.
@@ -145,10 +146,10 @@ struct RunSmem {
 __device__ __forceinline__ float4 ld4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ float part4(const float4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ void fma4(float (&acc)[4], float a, const float4 &b) {
-  acc[0] = fmaf(a, b.x, acc[0]);
-  acc[1] = fmaf(a, b.y, acc[1]);
-  acc[2] = fmaf(a, b.z, acc[2]);
-  acc[3] = fmaf(a, b.w, acc[3]);
+  const float2 aa = make_float2(a, a);
+  const float2 lo = __ffma2_rn(aa, make_float2(b.x, b.y), make_float2(acc[0], acc[1]));
+  const float2 hi = __ffma2_rn(aa, make_float2(b.z, b.w), make_float2(acc[2], acc[3]));
+  acc[0] = lo.x; acc[1] = lo.y; acc[2] = hi.x; acc[3] = hi.y;
 }
 
 // ROWS rows of out a thread: 2 where the slice has at most 32 columns, else 4.
