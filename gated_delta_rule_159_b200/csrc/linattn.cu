@@ -397,7 +397,8 @@ cudaError_t launch_run_t(const Run *r, int n, int widest, cudaStream_t s) {
     const int mine = RunSmem(r[i].dy, r[i].m != nullptr).total * (int)sizeof(float);
     if (mine > bytes) bytes = mine;
   }
-  const cudaError_t e = cudaFuncSetAttribute(run_kernel<T, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = prepare_kernel(run_kernel<T, ROWS>, RunSmem(128, true).total * (int)sizeof(float), ready);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((int64_t)r->cut.n_pieces * r->cut.H), (unsigned)simt_slices(widest), (unsigned)n);
   run_kernel<T, ROWS><<<grid, kRunThreads, bytes, s>>>(P);

@@ -2,6 +2,8 @@
 // one run, the cut of long sequences into pieces, and the launchers.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -171,6 +173,19 @@ cudaError_t launch_dlog_tc(const float *dots_q, const float *dots_k, const float
 // out[t, g, :] = sum over the heads of group g of part[t, h, :], for n (1 or 2) of them
 cudaError_t launch_group_sum(const float *const *part, void *const *out, int n, const Cut &c, int Hg, int d, int dtype,
                              cudaStream_t stream);
+
+// The largest dynamic shared memory that any launch of a kernel asks for, set once for each device.  It
+// belongs to the process: set anew for every call's own size, another thread's would come between the
+// setting and the launch.
+template <typename Kernel>
+cudaError_t prepare_kernel(Kernel kern, int bytes, std::atomic<uint64_t> &ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev <= 63 && (ready.load(std::memory_order_relaxed) >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 struct StepProblem {
   const void *q, *k, *v, *log_a;

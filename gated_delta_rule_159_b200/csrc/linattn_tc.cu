@@ -26,7 +26,6 @@
 // (every term written, and read with Z) that memory's 128 bytes a cycle were short, and they still
 // are what the CUDA cores wait for while products run.  X has one tile, Y and Z two stages.  The
 // loops stay rolled: unrolled, the roles together ran out of the instruction cache.
-#include <atomic>
 #include <cstring>
 
 #include "linattn.cuh"
@@ -932,21 +931,10 @@ __global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *d
   }
 }
 
-// Dynamic shared memory of a kernel, once for each device.
-template <typename Kernel>
-cudaError_t prepare_kernel(Kernel kern, std::atomic<uint64_t> &ready) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (dev <= 63 && (ready.load(std::memory_order_relaxed) >> dev & 1))) return e;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-  if (e == cudaSuccess && dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-  return e;
-}
-
 template <int WAY, int NT>
 cudaError_t launch_t(const TcRun &P, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = prepare_kernel(run_tc_kernel<WAY, NT>, ready);
+  const cudaError_t e = prepare_kernel(run_tc_kernel<WAY, NT>, (int)kSmemBytes, ready);
   if (e != cudaSuccess) return e;
   run_tc_kernel<WAY, NT><<<(unsigned)((int64_t)P.r.cut.n_pieces * P.r.cut.H), kThreads, kSmemBytes, s>>>(P);
   return cudaGetLastError();
@@ -981,7 +969,7 @@ cudaError_t launch_grads_tc(const Run *r, int32_t *status, cudaStream_t s) {
   uint64_t hook_ns = 0;
   if (!take_debug_timeout(GDN2_DEBUG_LINATTN, &hook_ns)) hook_ns = 0;
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = prepare_kernel(grads_tc_kernel, ready);
+  const cudaError_t e = prepare_kernel(grads_tc_kernel, (int)kSmemBytes, ready);
   if (e != cudaSuccess) return e;
   TcGrads P;
   for (int i = 0; i < 3; ++i)
