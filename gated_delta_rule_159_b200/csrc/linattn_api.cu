@@ -50,9 +50,12 @@ int64_t tokens_of(const gdn2_linattn_dims *d, bool packed) {
   return packed ? (int64_t)d->seq_len : (int64_t)d->n_seqs * d->seq_len;
 }
 
-// Limits of the launches: 32-bit token numbers, (piece, head) units in one grid dimension.
+// Limits of the launches: 32-bit token numbers, (piece, head) units in one grid dimension.  Loops over
+// tokens step up to 2^14 past a sequence's end before they look (the groups of dlog_a, 64 of them 256
+// tokens each): the numbers must not wrap there.
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - (1 << 15);
 int check_sizes(const gdn2_linattn_dims *d, bool packed) {
-  if (tokens_of(d, packed) >= ((int64_t)1 << 31)) return fail(GDN2_ERR_UNSUPPORTED, "T_tot must be below 2^31");
+  if (tokens_of(d, packed) > kMaxTokens) return fail(GDN2_ERR_UNSUPPORTED, "T_tot must be at most 2^31 - 2^15");
   if ((int64_t)d->n_seqs * d->n_heads >= ((int64_t)1 << 30))
     return fail(GDN2_ERR_UNSUPPORTED, "n_seqs * n_heads must be below 2^30");
   return GDN2_OK;

@@ -454,7 +454,7 @@ int gdn2_chunk_fwd_noalloc_status(gdn2_stream_t stream);
  *   n_heads     H, the heads of v, o, log_a and the state.
  *   n_qk_heads  heads of q and k, a divisor of H: head h reads q and k head h / (H / n_qk_heads).
  *               Their gradients are summed over the heads that share them.
- *   seq_len     as in gdn2_dims.
+ *   seq_len     as in gdn2_dims.  T_tot is at most 2^31 - 2^15.
  *   flags       GDN2_LINATTN_HEAD_DECAY: log_a is fp32 [H], one fixed decay per head; else log_a is
  *               [T_tot, H] of dtype_in.
  * log_a <= 0 (not checked); -infinity (a reset) is allowed; in the prompt and gradient calls log_a below
