@@ -6,26 +6,31 @@
 // from token j to the chunk's far end, f_i the decay from its near end to token i, g the chunk's:
 //   G = X Y^T,  P = bf16(G o D)           (rows = tokens; P becomes a TMEM operand)
 //   out = P Z + f o (X S)
-//   S <- g S + (w o Y)^T Z                (S is the fp32 accumulator itself)
+//   U = (w o Y)^T Z,  S <- g S + U        (fp32, rounded to nearest)
 // Where the chunk's decay stays above 2^-32, D_ij = f_i / f_j is not needed: out = f o (X S + P' Z)
 // with P' = bf16(G_ij / f_j), one accumulator and one product a weight.  (Not where the rows' dots with
 // m are asked for: dlog_a is a difference of the dots of two runs, and the same P, rounded the same
-// way in both, falls out of it; with P' it was off by 1% over 4096 tokens.)  And S is kept as 2^rho S
-// for as long as rho <= 32, so that the update of one chunk follows the last one's without a pass
-// over the accumulator; only past that is it scaled back.  Chunks of stronger decay (resets) take
-// D block by block and scale S every time.
-// The state is exact to fp32: w o Y goes to the tensor cores as a sum of NT bf16 values (4 give 26
-// bits, 2 give 17, for runs whose state only feeds bf16 products), Z is bf16 already.
+// way in both, falls out of it; with P' it was off by 1% over 4096 tokens.)  Chunks of stronger decay
+// (resets) take D block by block.
+// The state is held in fp32: w o Y goes to the tensor cores as a sum of NT bf16 values (4 give 26
+// bits, 2 give 17, for runs whose state only feeds bf16 products), Z is bf16 already, and g is a sum of two
+// floats.  The tensor cores cut sums toward zero.  With S as the accumulator itself that loss added up
+// over the chunks, by an amount that depends on the inputs; giving its average back left 8e-6 at 65000 tokens
+// without a decay, and states that nothing was written to grew by it.  So every chunk's sum starts from
+// zero and is added to S on the CUDA cores: S is off by what one chunk's products lose, at most 6e-7 in
+// the norm (100 to 65000 tokens), and a chunk that writes nothing leaves it as it was.
 //
-// Memory is what bounds it: 4 tiles of 32 KB a chunk, 128 KB against 2.9 us of 6.6 TB/s / 148 SMs;
-// the products take 5 x 512 (NT = 2) or 7 x 512 tensor cycles.  What costs time is the chains of
-// short steps on the CUDA cores, so they run side by side, each a group of warps of its own: warp 0
-// loads; warp 1 issues the state's products, warp 3 the rows' (G, X S, P Z); warp 2 sums the decays;
-// warps 4-11 write P, half a token row a thread, and warps 12-19 out; warps 20-27 copy the state to
-// bf16 for X S (and scale it) and weight Y, transposed into tensor memory: with w o Y in shared memory
-// (every term written, and read with Z) that memory's 128 bytes a cycle were short, and they still
-// are what the CUDA cores wait for while products run.  X has one tile, Y and Z two stages.  The
-// loops stay rolled: unrolled, the roles together ran out of the instruction cache.
+// Memory is its floor: 4 tiles of 32 KB a chunk, 128 KB against 2.9 us of 6.6 TB/s / 148 SMs; the products
+// take 5 x 512 (NT = 2) or 7 x 512 tensor cycles.  What a chunk takes is one round of its chain, 7100 cycles in
+// the forward: G (570 until it is seen), P's warps read it (1050), U (3000: a slice waits for its slot of tensor
+// memory, which is full), U is added to S (1050 and 550 to see it), then the next G.  The other steps run beside it,
+// each in a group of warps of its own: warp 0 loads; warp 1 issues the state's products, warp 3 the rows' (G,
+// X S, P Z); warp 2 sums the decays; warps 4-11 write P, half a token row a thread, and warps 12-19 out;
+// warps 20-27 add U to the state, copy it to bf16 for X S and weight Y, transposed into tensor memory: with
+// w o Y in shared memory (every term written, and read with Z) that memory's 128 bytes a cycle were short,
+// and they still are what the CUDA cores wait for while products run.  X has one tile, Y and Z two stages.
+// The loops stay rolled, and what few calls need stands outside them or is compiled out: unrolled, or with such
+// code to jump over, the roles ran out of the instruction cache (8 x 4096 tokens: 182 us for 162).
 #include <cstring>
 
 #include "linattn.cuh"
@@ -49,16 +54,11 @@ constexpr uint32_t OFF_O = 6 * kTile;       // out
 constexpr uint32_t OFF_MISC = 7 * kTile;
 // For the rows, mild chunks: f and 1 / f of each token, and 1; others: the decay from each token to
 // the edge of its 32-token block (log2), 2^(block total - that), the four block totals (not above
-// 0).  For the state (two stages): for each pair of tokens their weights as three bf16 pairs, then
-// 2^-rho and the factor that scales the accumulator back (1: none).
+// 0).  For the state (two stages): for each pair of tokens their weights as three bf16 pairs, then the
+// chunk's decay as a sum of two floats.
 constexpr uint32_t DEC_EDGE = 0, DEC_BETA = 512, DEC_TOT = 1024, DEC_W = 1040, DEC_G = 64 * 12, DEC_STAGE = 64 * 12 + 16;
 constexpr uint32_t MISC_BAR = DEC_W + 2 * DEC_STAGE;
 constexpr long long kMild = 32ll << 32;  // 2^-32, in the decays' units
-// The tensor cores cut sums toward zero: over a chunk's 32 (NT = 4) products the accumulator loses
-// 8.8e-7 of itself on average, 5.1e-7 where nothing decays (measured over memories of 1 to 64 chunks; the
-// loss of an element varies by about as much as that).  The bookkeeping of rho gives the average
-// back.  In units of 2^-32 in log2:
-constexpr long long kCut = 5480, kCutNone = 3179;
 // A waiter must not look so late that the phase after next is over: where nothing else keeps it, a
 // barrier of each parity of the chunk does.
 enum {
@@ -69,17 +69,18 @@ enum {
   BAR_WFREE = 8,    // + stage: and used
   BAR_FULL = 10,    // + slot: a slice of w o Y written
   BAR_EMPTY = 12,   // + slot: its products done
-  BAR_U = 14,       // + parity: update done
-  BAR_ROWDEC = 16,  // the rows' decays there
+  BAR_U = 14,       // + parity: U done
+  BAR_UREAD = 16,   // + parity: and read
+  BAR_ROWDEC = 18,  // the rows' decays there
   BAR_ROWFREE,      // and used
   BAR_X,            // X loaded
   BAR_XS,           // X S done, X and the state's copy free
   BAR_G,            // X Y^T done
+  BAR_GREAD,        // and read
   BAR_P,            // P written, and X S scaled where it has to be
   BAR_PZ,           // P Z done
   BAR_OREAD,        // out read
   BAR_S,            // the state's copy written
-  BAR_SREAD,        // the state read (and scaled)
   BAR_CLEAN,        // Y's and Z's rows behind the sequence cleared
   BAR_DRAIN,        // + 0, 1
   N_BARS = BAR_DRAIN + 2
@@ -88,8 +89,10 @@ constexpr uint32_t MISC_TMEM = MISC_BAR + N_BARS * 8, MISC_ABORT = MISC_TMEM + 4
 constexpr uint32_t MISC_BYTES = MISC_ABORT + 4;
 constexpr uint32_t kSmemBytes = OFF_MISC + MISC_BYTES;
 static_assert(kSmemBytes <= 232448, "shared memory over the sm_100 limit per CTA");
-constexpr uint32_t TM_G = 0, TM_OUT = 128, TM_S = 256, TM_W = 384;  // TMEM columns; TM_W: two slices of w o Y
-constexpr uint32_t TM_P = TM_G + 32;  // P takes the place of the middle half of G
+// TMEM columns.  U takes G's place once P's warps have read G (all 512 are taken); runs without rows have
+// it there and in out's place in turn.  TM_W: two slices of w o Y.
+constexpr uint32_t TM_G = 0, TM_OUT = 128, TM_S = 256, TM_P = 384, TM_W = 448;
+constexpr uint32_t kSlot = 32;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint32_t kSleepNs = 20000;  // between two looks at the clock: busy waits take issue slots from the workers
 constexpr float kLog2 = 1.4426950408889634f;
@@ -160,6 +163,30 @@ __device__ __forceinline__ void weigh(__nv_bfloat162 y, __nv_bfloat162 w0, __nv_
     part[3] = bits(__hfma2(w2, y, __hfma2(w1, y, __hneg2(q))));
   }
 }
+// 2^x for x <= 0 in units of 2^-32, as a sum of two floats: the states keep a chunk's factor for as long as
+// they remember, so one float's error would add up over the chunks.  2^x = 2^n e^r, r = f ln 2, |f| <= 1/2; r in
+// two parts, the Taylor series' terms from the square on in one float: off by about r^2 2^-23, 2^-25 at
+// most, and by far less for the weak decays that are remembered long.
+__device__ __forceinline__ float2 power2(long long x) {
+  x = max(x, -(300ll << 32));
+  const int n = (int)((x + (1ll << 31)) >> 32);
+  const int d = (int)(x - ((long long)n << 32));            // f in the same units
+  const float top = __int2float_rz(d), low = __int2float_rn(d - __float2int_rz(top));
+  constexpr float kLn2 = 0.693147182f * 0x1p-32f, kLn2Lo = -1.90465421e-9f * 0x1p-32f;
+  const float r = top * kLn2;
+  const float r_lo = fmaf(top, kLn2, -r) + fmaf(top, kLn2Lo, low * kLn2);
+  float e = 1.f / 40320.f;
+  e = fmaf(e, r, 1.f / 5040.f);
+  e = fmaf(e, r, 1.f / 720.f);
+  e = fmaf(e, r, 1.f / 120.f);
+  e = fmaf(e, r, 1.f / 24.f);
+  e = fmaf(e, r, 1.f / 6.f);
+  e = fmaf(e, r, 0.5f);
+  const float rest = fmaf(e * r, r, r_lo);
+  const float a = 1.f + r, b = r - (a - 1.f);               // 1 + r
+  const float hi = a + (rest + b), lo = (rest + b) - (hi - a);
+  return make_float2(ldexpf(hi, n), ldexpf(lo, n));
+}
 // One copy of the waiting loop for all waits: some thirty inlined ones filled the instruction cache.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status,
                                        uint64_t limit_ns) {
@@ -180,7 +207,7 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile i
 // only the launch that needs both ways at once takes it).
 template <int WAY, int NT>
 __device__ __forceinline__ void run_block(const TcRun &P, int block) {
-  constexpr int SLICE = 128 / NT;     // tokens of a slice of w o Y: NT terms in 64 columns, two slots
+  constexpr int SLICE = 64 / NT;      // tokens of a slice of w o Y: NT terms in 32 columns, two slots
   constexpr int SLICES = C / SLICE;
   extern __shared__ __align__(1024) uint8_t smem[];
   const Run &r = P.r;
@@ -192,6 +219,10 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
   if (!find_unit(r.cut, block, &pc)) return;
   const int unit = pc.unit, h = unit % H;
   const bool only = r.state_only != 0;
+  // the runs with four terms that have a launch of their own (the forward's, dv's) have no dots, marks or fp32 rows
+  constexpr bool PLAIN = WAY != 2 && NT == 4;
+  const bool marks = !PLAIN && !only && r.marks, out_f32 = !PLAIN && r.out_f32;
+  const __nv_bfloat16 *const m_all = PLAIN ? nullptr : static_cast<const __nv_bfloat16 *>(r.m);
   if (only && (pc.count < 2 || pc.s == (BACK ? 0 : pc.count - 1))) return;
   if (sb & 1023u) {  // the swizzled tiles need it; dynamic shared memory starts on it
     if (tid == 0) atomicExch(P.status, kStatusTimeout);
@@ -216,11 +247,12 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
   if (tid == 0) {
     *abort_flag = 0;
     for (int b = 0; b < N_BARS; ++b) {
-      const bool group = b == BAR_OREAD || b == BAR_WFREE || b == BAR_WFREE + 1 || b == BAR_S || b == BAR_SREAD ||
-                         b == BAR_CLEAN || b == BAR_FULL || b == BAR_FULL + 1;
+      const bool group = b == BAR_OREAD || b == BAR_WFREE || b == BAR_WFREE + 1 || b == BAR_S || b == BAR_UREAD ||
+                         b == BAR_UREAD + 1 || b == BAR_CLEAN || b == BAR_GREAD;
+      const bool four = b == BAR_FULL || b == BAR_FULL + 1;                      // half a group
       const bool two = b == BAR_P || b == BAR_ROWFREE;                           // groups
       const bool both = (b == BAR_FREE || b == BAR_FREE + 1) && !only;           // issuers
-      ptx::mbar_init(bar(b), group ? 8 : two ? 16 : both ? 2 : 1);
+      ptx::mbar_init(bar(b), group ? 8 : four ? 4 : two ? 16 : both ? 2 : 1);
     }
     ptx::fence_mbar_init();
   }
@@ -272,7 +304,11 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
     bool ok = true;
     for (int k = 0; k < nch && ok; ++k) {
       const int s = k & 1;
-      ok = wait_warp(BAR_Z + s, (uint32_t)(k >> 1)) && wait_warp(BAR_SREAD, (uint32_t)k);
+      // where U goes is free: G has been read, which was formed after the last U had been read; without
+      // rows, the last but one U has been read
+      const uint32_t tu = tm + (only && s ? TM_OUT : TM_G);
+      ok = wait_warp(BAR_Z + s, (uint32_t)(k >> 1));
+      if (ok) ok = !only ? wait_warp(BAR_GREAD, (uint32_t)k) : k < 2 || wait_warp(BAR_UREAD + s, (uint32_t)(k >> 1) + 1u);
 #pragma unroll 1
       for (int i = 0; i < SLICES && ok; ++i) {
         const int n = SLICES * k + i, slot = n & 1, t0 = (BACK ? SLICES - 1 - i : i) * SLICE;
@@ -284,8 +320,8 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
         for (int part = 0; part < NT; ++part)
 #pragma unroll
           for (int kk = 0; kk < SLICE / 16; ++kk)
-            ptx::umma_bf16_ts_if(lead, tm + TM_S, tm + TM_W + (uint32_t)(slot * 64 + part * (SLICE / 2) + kk * 8),
-                                 zd + kk * kMnStep, idKN, 1u);
+            ptx::umma_bf16_ts_if(lead, tu, tm + TM_W + (uint32_t)slot * kSlot + (uint32_t)(part * (SLICE / 2) + kk * 8),
+                                 zd + kk * kMnStep, idKN, part > 0 || kk > 0 || i > 0);
         ptx::umma_commit_if(lead, bar(BAR_EMPTY + slot));
       }
       if (!ok) break;
@@ -306,6 +342,7 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
         const uint64_t z = mnmaj(sb + OFF_Z + (uint32_t)s * kTile), st = mnmaj(sb + OFF_S);
         if (!wait_warp(BAR_X, (uint32_t)k) || !wait_warp(BAR_Y + s, (uint32_t)(k >> 1))) break;
         if (rows_of(k) < C && !wait_warp(BAR_CLEAN, 0u)) break;
+        if (k && !wait_warp(BAR_UREAD + (s ^ 1), (uint32_t)((k - 1) >> 1))) break;
         ptx::tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) ptx::umma_bf16_if(lead, tm + TM_G, x + k_step(kk), y + k_step(kk), idKK, kk > 0);
@@ -356,18 +393,8 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
     float a[4];
     if (nch > 0) load(0, a);
     bool ok = true;
-    fix rho = 0;  // the accumulator holds 2^rho times the state
-    for (int k = 0; k <= nch && ok; ++k) {
+    for (int k = 0; k < nch && ok; ++k) {
       const uint32_t stage = dec + DEC_W + (uint32_t)(k & 1) * DEC_STAGE;
-      if (k == nch) {
-        if (k >= 2) ok = wait_warp(BAR_WFREE + (k & 1), (uint32_t)(k >> 1) + 1u);
-        if (!ok) break;
-        if (lane == 0) {
-          sts_f32(stage + DEC_G, power(-rho));
-          ptx::mbar_arrive(bar(BAR_DEC + (k & 1)));
-        }
-        break;
-      }
       fix own[4];  // inclusive sums inside the lane
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -388,10 +415,8 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
         if (BACK ? b < (lane >> 3) : b > (lane >> 3)) far += t;
       }
       logs += all;
-      const bool mild = all >= -kMild, keep = rho - all <= kMild;
-      const float behind = power(-rho), back = keep ? 1.f : power(all - rho);
-      rho = keep ? rho - all : 0;
-      const fix cut = NT == 4 ? all != 0 ? kCut : kCutNone : 0;
+      const bool mild = all >= -kMild;
+      const float2 g = power2(all);
       float one[4], two[4];
       uint32_t w[2][3];
 #pragma unroll
@@ -400,8 +425,7 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
         const float first = value(mild ? all - rest - far : BACK ? total - in : in);
         one[j] = mild ? ptx::ex2(first) : first;
         two[j] = ptx::ex2(mild ? -first : value(rest));
-        const int before_it = BACK ? C - 1 - (4 * lane + j) : 4 * lane + j;  // tokens of the chunk
-        float left = power(rest + far + rho - cut * before_it / C);
+        float left = power(rest + far);
 #pragma unroll
         for (int n = 0; n < 3; ++n) {
           const uint32_t b = bf16_bits(left);
@@ -409,14 +433,13 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
           w[j >> 1][n] = j & 1 ? w[j >> 1][n] | b << 16 : b;
         }
       }
-      rho -= cut;
       if (k >= 2) ok = wait_warp(BAR_WFREE + (k & 1), (uint32_t)(k >> 1) + 1u);
       if (!ok) break;
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int n = 0; n < 3; ++n) sts_u32(stage + 24 * lane + 12 * q + 4 * n, w[q][n]);
-      if (lane == 0) sts_v2(stage + DEC_G, make_uint2(__float_as_uint(behind), __float_as_uint(back)));
+      if (lane == 0) sts_v2(stage + DEC_G, make_uint2(__float_as_uint(g.x), __float_as_uint(g.y)));
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(BAR_DEC + (k & 1)));
       if (!only) {
@@ -442,21 +465,27 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
       const bool mild = lds_f32(dec + DEC_TOT) > 0.f;
       if (!wait_warp(BAR_G, (uint32_t)k)) break;
       ptx::tc_fence_after();
-      // two of the four blocks of 32 columns each; P's 16 columns of a block lie where this warp has
-      // read G already: blocks 1 and 0 write G columns 48.. and 32.., blocks 2 and 3 write 64.. and 80..
+      // two of the four blocks of 32 columns each
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
-        const int cb = half ? 2 + i : 1 - i;
-        uint32_t out[16];
-        if (BACK ? cb < wq : cb > wq) {
+        const int cb = 2 * half + i;
+        const bool none = BACK ? cb < wq : cb > wq;
+        uint32_t out[16], g[32];
+        if (!none) {
+          ptx::tmem_ld32(lanes + TM_G + cb * 32, g);
+          ptx::tmem_wait_ld();
+        }
+        if (i) {  // U may take G's place
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(BAR_GREAD));
+        }
+        if (none) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) out[j] = 0u;
         } else {
-          uint32_t g[32];
-          ptx::tmem_ld32(lanes + TM_G + cb * 32, g);
           if (mild) {
-            const float2 f2 = r.m ? make_float2(edge, edge) : make_float2(1.f, 1.f);
-            ptx::tmem_wait_ld();
+            const float2 f2 = m_all ? make_float2(edge, edge) : make_float2(1.f, 1.f);
 #pragma unroll
             for (int j4 = 0; j4 < 8; ++j4) {
               const float4 be = lds_f4(dec + DEC_BETA + cb * 128 + j4 * 16);
@@ -473,7 +502,6 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
           } else if (cb == wq) {
             // both tokens in one block: the decay between them, pair by pair
             const float2 minus = make_float2(-1.f, -1.f), e2 = make_float2(edge, edge);
-            ptx::tmem_wait_ld();
 #pragma unroll
             for (int j4 = 0; j4 < 8; ++j4) {
               const float4 e = lds_f4(dec + DEC_EDGE + cb * 128 + j4 * 16);
@@ -492,7 +520,6 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
             for (int b = BACK ? wq + 1 : cb + 1; b < (BACK ? cb : wq); ++b) between += lds_f32(dec + DEC_TOT + b * 4);
             const float alpha = ptx::ex2(between);
             const float2 a2 = make_float2(alpha, alpha);
-            ptx::tmem_wait_ld();
 #pragma unroll
             for (int j4 = 0; j4 < 8; ++j4) {
               const float4 be = lds_f4(dec + DEC_BETA + cb * 128 + j4 * 16);
@@ -522,8 +549,8 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
       const bool in = row < rows_of(k);
       const size_t tok = (size_t)pc.t0 + (size_t)chunk_no(k) * C + row;
       const __nv_bfloat16 *m = nullptr;
-      if (r.m && in) {
-        m = static_cast<const __nv_bfloat16 *>(r.m) + (tok * r.Hm + h / (H / r.Hm)) * D + half * 64;
+      if (m_all && in) {
+        m = m_all + (tok * r.Hm + h / (H / r.Hm)) * D + half * 64;
         prefetch_l2(m);
       }
       if (!wait_warp(BAR_ROWDEC, (uint32_t)k)) break;
@@ -536,7 +563,7 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
       float2 f2 = make_float2(f, f);
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(BAR_ROWFREE));
-      if (!mild || r.m) {
+      if (!mild || m_all) {
         if (!wait_warp(BAR_XS, (uint32_t)k)) break;
         ptx::tc_fence_after();
 #pragma unroll 1
@@ -558,7 +585,7 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
         ptx::bulk_wait_group_read0();  // this warp's rows of the tile
       }
       float2 dot = make_float2(0.f, 0.f);
-      const bool whole = wq * 32 + 32 <= rows_of(k) && !r.out_f32;
+      const bool whole = wq * 32 + 32 <= rows_of(k) && !out_f32;
       uint4 mw[2];  // 16 values of m's row, asked for one step ahead
       if (m)
 #pragma unroll
@@ -583,7 +610,7 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) dot = fma2(pair(w[i] << 16, w[i] & 0xffff0000u), o[4 * j + i], dot);
           }
-        if (r.out_f32) {
+        if (out_f32) {
           if (in) {
             float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(r.out) + at_out + cb * 16);
 #pragma unroll
@@ -614,7 +641,7 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
     if (lane == 0) ptx::bulk_wait_group0();
   } else {
     // ---------------------------------------------------------------- state (warp: 32 y rows x 64 z columns) and w o Y
-    // (warp: 32 y columns, half the tokens of a slice)
+    // (warp: 32 y columns, every other slice)
     const int wq = warp & 3, half = (warp - kState0) >> 2, yrow = wq * 32 + lane, stid = tid - 32 * kState0;
     const uint32_t quad = tm + ((uint32_t)(wq * 32) << 16);
     // 16 columns of a state in memory: [dy][dz], or [dz][dy] with `flip`
@@ -630,60 +657,105 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
         for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(p[(z0 + j) * D + yrow]);
       }
     };
-    auto store_state = [&](float *p, bool flip, int z0, const uint32_t (&v)[16]) {
-      if (!flip) {
+    // this thread's 64 columns of the state in tensor memory: to memory, to a mark, and multiplied with one
+    auto put_state = [&](float *p, bool flip) {
+#pragma unroll 1
+      for (int z0 = 64 * half; z0 < 64 * half + 64; z0 += 16) {
+        uint32_t v[16];
+        ptx::tmem_ld16(quad + TM_S + z0, v);
+        ptx::tmem_wait_ld();
+        if (!flip) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(p + yrow * D + z0 + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) p[(z0 + j) * D + yrow] = __uint_as_float(v[j]);
+        }
+      }
+    };
+    auto put_mark = [&](size_t mu) {
+      float *p = r.marks + mu * (D * D) + 4 * yrow;
+#pragma unroll 1
+      for (int z0 = 64 * half; z0 < 64 * half + 64; z0 += 16) {
+        uint32_t v[16];
+        ptx::tmem_ld16(quad + TM_S + z0, v);
+        ptx::tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4 *>(p + yrow * D + z0 + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) p[(z0 + j) * D + yrow] = __uint_as_float(v[j]);
+          *reinterpret_cast<uint4 *>(p + (z0 / 4 + j) * 512) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
       }
+    };
+    auto dot_mark = [&](size_t mu) {
+      const float *p = r.marks + mu * (D * D) + 4 * yrow;
+      float dot = 0.f;
+#pragma unroll 1
+      for (int z0 = 64 * half; z0 < 64 * half + 64; z0 += 16) {
+        uint32_t v[16];
+        float4 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const float4 *>(p + (z0 / 4 + j) * 512);
+        ptx::tmem_ld16(quad + TM_S + z0, v);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          dot = fmaf(w[j].x, __uint_as_float(v[4 * j]), fmaf(w[j].y, __uint_as_float(v[4 * j + 1]),
+                fmaf(w[j].z, __uint_as_float(v[4 * j + 2]), fmaf(w[j].w, __uint_as_float(v[4 * j + 3]), dot))));
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+      if (lane == 0) r.mark_dots[mu * kMarkDots + (warp - kState0)] = dot;
     };
     // this lane's row of the four matrices (8 columns x 8 tokens) of 16 columns and 16 tokens
     const int row = ((lane >> 4) << 3) | (lane & 7);
     const uint32_t chunk = (uint32_t)(wq & 1) * 4u + (uint32_t)(lane >> 3 & 1);
     const uint32_t mine = (uint32_t)(wq >> 1) * kBlock;
-    // slices first .. last - 1 (in the order of the walk) of chunk k's w o Y, two tokens to a word,
-    // transposed into tensor memory
+    // this half's slices first .. last - 1 (in the order of the walk) of chunk k's w o Y, two tokens to a word,
+    // transposed into the half's own slot of tensor memory
     auto weigh_slices = [&](int k, int first, int last) {
       const int s = k & 1;
       const uint32_t y = sb + OFF_Y + (uint32_t)s * kTile;
 #pragma unroll 1
       for (int i = first; i < last; ++i) {
-        const int n = SLICES * k + i, slot = n & 1, t0 = (BACK ? SLICES - 1 - i : i) * SLICE + half * (SLICE / 2);
-        if (n >= 2 && !wait_warp(BAR_EMPTY + slot, (uint32_t)(n >> 1) + 1u)) return false;
-        ptx::tc_fence_after();
-#pragma unroll 1
-        for (int t = 0; t < SLICE / 2; t += 16) {
+        const int n = SLICES / 2 * k + i, t0 = (BACK ? SLICES - 1 - (2 * i + half) : 2 * i + half) * SLICE;
+        uint32_t terms[SLICE / 16][2][NT][4];
+#pragma unroll
+        for (int t = 0; t < SLICE / 16; ++t) {
           // weights of the pairs of tokens that this lane's columns of the matrices are
-          const uint32_t ws = dec + DEC_W + (uint32_t)s * DEC_STAGE + (uint32_t)((t0 + t) / 2 + (lane & 3)) * 12u;
+          const uint32_t ws = dec + DEC_W + (uint32_t)s * DEC_STAGE + (uint32_t)(t0 / 2 + 8 * t + (lane & 3)) * 12u;
           __nv_bfloat162 w[2][3];
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int j = 0; j < (NT == 2 ? 2 : 3); ++j) w[q][j] = bf2(__float_as_uint(lds_f32(ws + 48 * q + 4 * j)));
-          const uint32_t to = quad + TM_W + (uint32_t)(slot * 64 + half * (SLICE / 4) + t / 2);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint32_t yw[4], terms[NT][4];
-            ptx::ldmatrix4_trans(y + mine + (uint32_t)(t0 + t) * 128u + swz(row, chunk + 2u * c), yw);
+            uint32_t yw[4];
+            ptx::ldmatrix4_trans(y + mine + (uint32_t)(t0 + 16 * t) * 128u + swz(row, chunk + 2u * c), yw);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
               uint32_t got[NT];
               weigh<NT>(bf2(yw[p]), w[p >> 1][0], w[p >> 1][1], w[p >> 1][2], got);
 #pragma unroll
-              for (int m = 0; m < NT; ++m) terms[m][p] = got[m];
+              for (int m = 0; m < NT; ++m) terms[t][c][m][p] = got[m];
             }
-#pragma unroll
-            for (int m = 0; m < NT; ++m)
-              ptx::tmem_st_16x8(to + ((uint32_t)(16 * c) << 16) + (uint32_t)m * (SLICE / 2), terms[m]);
           }
         }
+        if (n && !wait_warp(BAR_EMPTY + half, (uint32_t)n + 1u)) return false;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < SLICE / 16; ++t)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int m = 0; m < NT; ++m)
+              ptx::tmem_st_16x8(quad + TM_W + ((uint32_t)(16 * c) << 16) + (uint32_t)half * kSlot +
+                                    (uint32_t)(m * (SLICE / 2) + 8 * t),
+                                terms[t][c][m]);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(BAR_FULL + slot));
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_FULL + half));
       }
       return true;
     };
@@ -706,21 +778,19 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
     }
 #pragma unroll 1
     for (int c = 4 * half; c < 4 * half + 4; ++c) {
-      uint32_t v[16];
-      if (start) {
-        load_state(start, flip_start, c * 16, v);
-      } else {
+      uint32_t v[16], zero[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = 0u;
-      }
+      for (int j = 0; j < 16; ++j) v[j] = zero[j] = 0u;
+      if (start) load_state(start, flip_start, c * 16, v);
       __syncwarp();
-      ptx::tmem_st16(quad + TM_S + c * 16, v);
+      ptx::tmem_st16(quad + TM_S + c * 16, zero);
+      ptx::tmem_st16(quad + TM_OUT + c * 16, v);  // as if it were the U of a chunk before the first
     }
     ptx::tmem_wait_st();
     // marks of this thread's part of the state behind group `g` of chunks
     auto mark_unit = [&](int g) { return (size_t)mark_slot(unit / H, pc.t0 + g * kGroup * C) * H + h; };
     auto ends_group = [&](int no) { return (no + 1) % kGroup == 0 || no == nch - 1; };
-    int seen = 0;  // updates waited for
+    float2 g2 = make_float2(1.f, 0.f);  // the last chunk's decay
     for (int k = 0; k <= nch; ++k) {
       const int s = k & 1;
       const uint32_t par = (uint32_t)(k >> 1);
@@ -743,106 +813,70 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
           if (lane == 0) ptx::mbar_arrive(bar(BAR_CLEAN));
           if (!wait_warp(BAR_CLEAN, 0u)) break;  // other warps' rows are read too
         }
-        // the first slice, while the last update still runs
+        // the first slice, while the last U is still summed
         if (!weigh_slices(k, 0, 1)) break;
-      } else if (!wait_warp(BAR_DEC + s, par)) {
-        break;
       }
-      // the state before the k-th chunk walked: its copy for X S, and scaled back where due
-      const uint32_t gs = dec + DEC_W + (uint32_t)s * DEC_STAGE + DEC_G;
-      const float behind = lds_f32(gs), back = last ? 1.f : lds_f32(gs + 4);
-      const float2 behind2 = make_float2(behind, behind);
-      // with neither a copy to write nor anything to scale, the state is not read: the next update
-      // follows at once.  One update stays unseen at most, so that no phase is missed.
-      const bool pass = only && !last && back == 1.f;
-      const int need = pass ? k - 1 : k;  // updates that have to be done
-      bool ok = true;
-      while (ok && seen < need) {
-        ok = wait_warp(BAR_U + (seen & 1), (uint32_t)(seen >> 1));
-        ++seen;
-      }
-      if (!ok) break;
-      if (pass) {
-        if (lane == 0) ptx::mbar_arrive(bar(BAR_SREAD));
-      } else {
-        ptx::tc_fence_after();
-        const float *mark_in = nullptr;
-        float *mark_out = nullptr;
-        size_t mu = 0;
-        if (r.marks && !only) {
-          const int no = chunk_no(k);  // forward: the group in front of chunk k is done; backward: k's begins
-          if (BACK && !last && ends_group(no)) {
-            mu = mark_unit(no / kGroup);
-            if (WAY == 1 || r.mark_dots) mark_in = r.marks + mu * (D * D) + 4 * yrow;
-            else mark_out = r.marks + mu * (D * D) + 4 * yrow;
-          }
-          if (!BACK && k && ends_group(k - 1)) mark_out = r.marks + mark_unit((k - 1) / kGroup) * (D * D) + 4 * yrow;
-          // the next group's mark, two chunks ahead
-          if (BACK && (WAY == 1 || r.mark_dots) && !last && no % kGroup == 1 && no > kGroup) {
-            const char *next = reinterpret_cast<const char *>(r.marks + mark_unit(no / kGroup - 1) * (D * D)) + stid * 128;
-            prefetch_l2(next);
-            prefetch_l2(next + 32768);
-          }
-        }
-        float dot = 0.f;
-        uint32_t copy[32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = 4 * half + i;  // 16 columns each
-          uint32_t v[16];
+      // the state before the k-th chunk walked, and its copy for X S.  This loop is what a chunk waits for:
+      // all that only some calls or chunks do stands behind it (jumped over in it, it cost half as much again).
+      if (k && !wait_warp(BAR_U + (s ^ 1), (uint32_t)((k - 1) >> 1))) break;
+      if (k && !only && !wait_warp(BAR_XS, (uint32_t)k + 1u)) break;  // the last copy has been read
+      ptx::tc_fence_after();
+      {
+        const uint32_t tu = quad + (k == 0 || (only && !s) ? TM_OUT : TM_G);  // U of chunk k - 1
+        const float2 hi2 = make_float2(g2.x, g2.x), lo2 = make_float2(g2.y, g2.y);
+#pragma unroll 1
+        for (int c = 4 * half; c < 4 * half + 4; ++c) {  // 16 columns each
+          uint32_t v[16], u[16];
           ptx::tmem_ld16(quad + TM_S + c * 16, v);
+          ptx::tmem_ld16(tu + c * 16, u);
           ptx::tmem_wait_ld();
-          if (back != 1.f) {
-            uint32_t u[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(back * __uint_as_float(v[j]));
-            ptx::tmem_st16(quad + TM_S + c * 16, u);
-          }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float2 w = mul2(behind2, pair(v[2 * j], v[2 * j + 1]));
+            const float2 x = pair(v[2 * j], v[2 * j + 1]);
+            const float2 w = fma2(hi2, x, fma2(lo2, x, pair(u[2 * j], u[2 * j + 1])));
             v[2 * j] = __float_as_uint(w.x);
             v[2 * j + 1] = __float_as_uint(w.y);
-            copy[8 * i + j] = pack_bf16x2(w.x, w.y);
+            u[j] = pack_bf16x2(w.x, w.y);
           }
-          if (mark_in) {
+          ptx::tmem_st16(quad + TM_S + c * 16, v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 w = *reinterpret_cast<const float4 *>(mark_in + (c * 4 + j) * 512);
-              dot = fmaf(w.x, __uint_as_float(v[4 * j]), fmaf(w.y, __uint_as_float(v[4 * j + 1]),
-                    fmaf(w.z, __uint_as_float(v[4 * j + 2]), fmaf(w.w, __uint_as_float(v[4 * j + 3]), dot))));
-            }
-          }
-          if (mark_out) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4 *>(mark_out + (c * 4 + j) * 512) =
-                  make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          }
-          if (last && dst) store_state(dst, flip_dst, c * 16, v);
-        }
-        if (last) break;
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(BAR_SREAD));
-        if (!only) {
-          if (k && !wait_warp(BAR_XS, (uint32_t)k + 1u)) break;  // the last copy has been read
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            sts_v4(sb + OFF_S + half * kBlock + swz(yrow, (uint32_t)j),
-                   make_uint4(copy[4 * j], copy[4 * j + 1], copy[4 * j + 2], copy[4 * j + 3]));
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(BAR_S));
-        }
-        if (mark_in) {
-#pragma unroll
-          for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-          if (lane == 0) r.mark_dots[mu * kMarkDots + (warp - kState0)] = dot;
+          for (int j = 0; j < 2; ++j)
+            sts_v4(sb + OFF_S + half * kBlock + swz(yrow, (uint32_t)(2 * (c & 3) + j)),
+                   make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]));
         }
       }
-      if (!weigh_slices(k, 1, SLICES)) break;
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (k) ptx::mbar_arrive(bar(BAR_UREAD + (s ^ 1)));
+        ptx::mbar_arrive(bar(BAR_S));
+      }
+      if (last) {
+        if (dst) put_state(dst, flip_dst);
+        if (!BACK && k && marks) put_mark(mark_unit((k - 1) / kGroup));
+        break;
+      }
+      if (marks) {
+        const int no = chunk_no(k);  // forward: the group in front of chunk k is done; backward: k's begins
+        if (!BACK && k && ends_group(k - 1)) put_mark(mark_unit((k - 1) / kGroup));
+        if (BACK && ends_group(no)) {
+          const size_t mu = mark_unit(no / kGroup);
+          if (WAY == 1 || r.mark_dots) dot_mark(mu);
+          else put_mark(mu);
+        }
+        // the next group's mark, two chunks ahead
+        if (BACK && (WAY == 1 || r.mark_dots) && no % kGroup == 1 && no > kGroup) {
+          const char *next = reinterpret_cast<const char *>(r.marks + mark_unit(no / kGroup - 1) * (D * D)) + stid * 128;
+          prefetch_l2(next);
+          prefetch_l2(next + 32768);
+        }
+      }
+      if (!weigh_slices(k, 1, SLICES / 2)) break;
+      const uint32_t gs = dec + DEC_W + (uint32_t)s * DEC_STAGE + DEC_G;
+      g2 = make_float2(lds_f32(gs), lds_f32(gs + 4));
+      __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(BAR_WFREE + s));
     }
   }

@@ -68,3 +68,99 @@ def test_threads_with_heads_of_two_sizes(g, tmp_path):
     for call, (_, want, o, S, *_) in zip(calls, kept):
         assert call.bad == 0
         assert torch.equal(o, want[0]) and torch.equal(S, want[1])
+
+
+# lengths and heads: 160 units of 16 chunks each, uncut; one sequence cut into many pieces; chunks of one token
+STILL = [((2048,) * 8, 20), ((20000,), 1), ((1,) * 3, 4), ((300, 0, 129), 2)]
+
+
+@pytest.mark.parametrize("lens,H", STILL, ids=["uncut", "cut", "one", "ragged"])
+@pytest.mark.parametrize("zero", ["k", "v"])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 32)])
+def test_a_state_that_nothing_is_written_to(g, dtype, d, zero, lens, H):
+    """Without a decay it stays bit for bit, however many tokens pass; so does its gradient."""
+    p, _ = ref.problem(lens, H, H, d, d, dtype, "none", True, seed=60)
+    q, k, v, la, dO = (p[x] for x in ("q", "k", "v", "log_a", "dO"))
+    o, S = g.linattn_fwd(q, torch.zeros_like(k) if zero == "k" else k, torch.zeros_like(v) if zero == "v" else v, la,
+                         p["S0"], p["cu"])
+    assert torch.equal(S, p["S0"])
+    # dLoss/dS gains q_t dO_t^T with every token
+    got = g.linattn_bwd(torch.zeros_like(q) if zero == "k" else q, k, v, la, torch.zeros_like(dO) if zero == "v" else dO,
+                        p["S0"], p["dS_T"], p["cu"])
+    assert torch.equal(got["dS0"], p["dS_T"])
+
+
+@pytest.mark.parametrize("lens,H", STILL, ids=["uncut", "cut", "one", "ragged"])
+@pytest.mark.parametrize("la", [-1e-9, -1e-4, -0.003, -0.3])
+def test_a_state_that_only_decays(g, la, lens, H):
+    """log_a is summed in steps of 2^-32 in log2 (half a step a token, and two fp32 roundings of the product); a
+    chunk's factor rounds the state once and is off by less than that itself; a piece's takes three roundings
+    and an exponential of 2 ulp (at most 40 pieces of 512 tokens)."""
+    p, cu = ref.problem(lens, H, H, 128, 128, BF, "none", True, seed=61)
+    decay = torch.full((H,), la, device="cuda")
+    _, S = g.linattn_fwd(p["q"], torch.zeros_like(p["k"]), p["v"], decay, p["S0"], p["cu"])
+    got = g.linattn_bwd(torch.zeros_like(p["q"]), p["k"], p["v"], decay, p["dO"], p["S0"], p["dS_T"], p["cu"])
+    for n, length in enumerate(lens):
+        total = length * decay.double()[:, None, None]
+        roundings = 2 * (length // 128 + 1) + (8 * 40 if len(lens) == 1 else 0) + 2 * float(total.abs().max())
+        bound = length * 2.0 ** -33 + roundings * ref.FP32
+        for x, start in ((S, p["S0"]), (got["dS0"], p["dS_T"])):
+            want = torch.exp(total) * start[n].double()
+            off = (x[n].double() - want).abs() - bound * want.abs()
+            assert (off <= 2.0 ** -120).all(), (n, float((off / want.abs()).max()), bound)  # below: fp32's last bits
+
+
+def _norms(got, want):
+    """|got - want| / |want| over everything, both float64."""
+    got, want = got.detach().cpu().double(), want.double()
+    assert got.shape == want.shape and torch.isfinite(got).all()
+    return float((got - want).norm() / want.norm())
+
+
+def test_states_near_the_end_of_the_range(g):
+    """Values of 2^110 written under decays on both sides of 2^-32 a chunk: nothing in between is larger."""
+    p, cu = ref.problem((1000, 40), 3, 3, 128, 128, BF, "none", False, seed=62)
+    decay = torch.tensor([-0.01, -0.05, -0.3], device="cuda")
+    p["log_a"] = decay
+    k, v = p["k"] * 2.0 ** 56, p["v"] * 2.0 ** 54
+    o, S = g.linattn_fwd(p["q"], k, v, decay, None, p["cu"])
+    want = ref.forward(dict(p, k=k, v=v), cu, 3, 3, True)
+    assert torch.isfinite(o).all() and _norms(S, want["S_T"][0]) < 1.2e-6
+
+
+# lengths, H, H_qk, decay: few tokens and many, one launch and three, pieces
+DENSE = [((500, 129, 1), 2, 1, "token"), ((2048,), 160, 160, "none"), ((2048,), 160, 80, "token"), ((6000,), 1, 1, "none"),
+         ((300, 40), 2, 2, "reset"), ((385, 64), 2, 2, "strong"), ((700,), 2, 1, "head")]
+
+
+def _problem(lens, H, Hqk, decay, dtype, d, seed):
+    p, cu = ref.problem(lens, H, Hqk, d, d, dtype, decay, True, seed=seed)
+    keep = min(H, 2 * (H // Hqk))  # heads that are checked: the first groups'
+    one = dict(p)
+    for x in ("q", "k"):
+        one[x] = p[x][:, :keep * Hqk // H].contiguous()
+    for x in ("v", "dO"):
+        one[x] = p[x][:, :keep].contiguous()
+    one["log_a"] = p["log_a"][:keep] if p["log_a"].dim() == 1 else p["log_a"][:, :keep].contiguous()
+    for x in ("S0", "dS_T"):
+        one[x] = p[x][:, :keep].contiguous()
+    return p, cu, one, keep
+
+
+@pytest.mark.parametrize("case", DENSE, ids=lambda c: f"{'-'.join(map(str, c[0]))}_h{c[1]}.{c[2]}_{c[3]}")
+def test_states_in_the_norm(g, case):
+    """S_T and dS0 of the tensor-core runs.  A weighted row of y keeps 26 bits.  A chunk's sum takes 32 products, each
+    cut off in the last bit at most: on average less than half a step (2^-24 / 1.4 of the value), of partial sums that
+    come to two thirds of the whole: 0.95e-6, and the state itself is rounded once a chunk (2^-24 / sqrt(3) each, at
+    random).  1.2e-6; rows kept to 17 bits (2^-17 / sqrt(3) / 1.4) would be off by 3e-6."""
+    lens, H, Hqk, decay = case
+    p, cu, one, keep = _problem(lens, H, Hqk, decay, BF, 128, 70)
+    _, S = g.linattn_fwd(p["q"], p["k"], p["v"], p["log_a"], p["S0"], p["cu"])
+    got = g.linattn_bwd(p["q"], p["k"], p["v"], p["log_a"], p["dO"], p["S0"], p["dS_T"], p["cu"])
+    heads = keep * Hqk // H
+    want = ref.forward(one, cu, keep, heads, True)["S_T"][0]
+    assert _norms(S[:, :keep], want) < 1.2e-6
+    want = torch.zeros_like(want)
+    for n, h, _, u in ref.units(one, cu, keep, heads):
+        want[n, h] = ref.run(u["k"], u["q"], u["dO"], u["la"], u["dS_T"], back=True)["fin"]
+    assert _norms(got["dS0"][:, :keep], want) < 1.2e-6
