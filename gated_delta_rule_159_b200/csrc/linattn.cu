@@ -10,37 +10,44 @@ namespace lin {
 namespace {
 
 // ---------------------------------------------------------------- plan and join
-// Exclusive running count of pieces over the sequences (one block) into seg_off, and the pieces'
-// numbers from the longest down into order; either may be NULL.
-__global__ void __launch_bounds__(1024) plan_kernel(Cut c, int32_t *seg_off, int32_t *order) {
-  __shared__ int warp_sum[32];
-  __shared__ int base;
+// Exclusive running counts over the sequences (one block) of their pieces into seg_off and of those of cut
+// sequences into cut_off, and the pieces' numbers from the longest down into order; the first two or the
+// last may be NULL.
+__global__ void __launch_bounds__(1024) plan_kernel(Cut c, int32_t *seg_off, int32_t *cut_off, int32_t *order) {
+  __shared__ long long warp_sum[32];  // cut sequences' pieces above bit 32
+  __shared__ long long base;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) base = 0;
   for (int n0 = 0; seg_off && n0 < c.n_seqs; n0 += 1024) {
     const int n = n0 + threadIdx.x;
-    int v = 0;
+    long long v = 0;
     if (n < c.n_seqs) {
       int t0, len;
       seq_bounds(c, n, &t0, &len);
       v = piece_count(len, c.target, c.grain);
+      if (v > 1) v |= v << 32;
     }
-    int incl = v;
+    long long incl = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, d);
+      const long long up = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += up;
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int before = base;
+    long long before = base;
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    // n_pieces bounds the count for offsets in order; anything else is cut back to it
-    if (n < c.n_seqs) seg_off[n] = min(before + incl - v, c.n_pieces);
+    // n_pieces and n_cut bound the counts for offsets in order; anything else is cut back to them
+    auto put = [&](int at, long long sum) {
+      seg_off[at] = (int)min(sum & 0xffffffffll, (long long)c.n_pieces);
+      cut_off[at] = (int)min(sum >> 32, (long long)c.n_cut);
+    };
+    if (n < c.n_seqs) put(n, before + incl - v);
     __syncthreads();
     if (threadIdx.x == 1023) {
-      base = before + incl;
-      if (n0 + 1024 >= c.n_seqs) seg_off[c.n_seqs] = min(base, c.n_pieces);
+      const long long sum = before + incl;
+      base = min(sum & 0xffffffffll, (long long)c.n_pieces) | min(sum >> 32, (long long)c.n_cut) << 32;
+      if (n0 + 1024 >= c.n_seqs) put(c.n_seqs, base);
     }
     __syncthreads();
   }
@@ -49,6 +56,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(Cut c, int32_t *seg_off, int
   // keys: chunks, then the lower number first; 0 is no piece.  A bitonic sort, largest first.
   __shared__ uint32_t key[kMaxSorted];
   c.seg_off = seg_off;
+  c.cut_off = cut_off;
   const int i = threadIdx.x;
   Piece p;
   key[i] = i < c.n_pieces && find_piece(c, i, &p)
@@ -80,10 +88,10 @@ struct Runs {
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Runs P) {
   const Run &r = P.run[blockIdx.z];
   const int size = r.dy * r.dz, H = r.cut.H;
-  const int n = blockIdx.x / H, h = blockIdx.x % H;
-  const int first = r.cut.seg_off ? r.cut.seg_off[n] : n * r.cut.per_seq;
-  const int count = r.cut.seg_off ? r.cut.seg_off[n + 1] - first : r.cut.per_seq;
-  if (count < 2) return;
+  const int h = blockIdx.x % H;
+  Piece pc;  // the first of a cut sequence
+  if (!find_cut_piece(r.cut, blockIdx.x / H, &pc) || pc.s) return;
+  const int n = pc.n, count = min(pc.count, r.cut.n_cut - pc.cut);
   const int e = blockIdx.y * 256 + threadIdx.x;
   if (e >= size) return;
   float cur = 0.f;
@@ -91,7 +99,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Runs 
     const float *s0 = r.start + (size_t)(n * H + h) * size;
     cur = r.start_t ? s0[(size_t)(e % r.dz) * r.dy + e / r.dz] : s0[e];
   }
-  const int64_t unit0 = (int64_t)first * H + h;
+  const int64_t unit0 = (int64_t)pc.cut * H + h;
   for (int i0 = 0; i0 < count; i0 += 4) {
     float got[4], g[4];
 #pragma unroll
@@ -163,8 +171,9 @@ __global__ void __launch_bounds__(kRunThreads, 2) run_kernel(const __grid_consta
   __shared__ float fs[TB], ws[TB];
   const int H = p.cut.H, tid = threadIdx.x;
   Piece pc;
-  if (blockIdx.y * COLS >= p.dz || !find_unit(p.cut, blockIdx.x, &pc)) return;
-  const int unit = pc.unit, h = unit % H;
+  if (blockIdx.y * COLS >= p.dz || !find_unit(p.cut, blockIdx.x, p.state_only, &pc)) return;
+  const int h = blockIdx.x % H;
+  const size_t cut_unit = (size_t)pc.cut * H + h;
   if (p.state_only && (pc.count < 2 || pc.s == (p.back ? 0 : pc.count - 1))) return;
   const RunSmem L(p.dy, p.m != nullptr);
   float *xs = sm, *yv = sm + L.off_y, *zs = sm + L.off_z, *ss = sm + L.off_s, *ms = sm + L.off_m;
@@ -182,7 +191,7 @@ __global__ void __launch_bounds__(kRunThreads, 2) run_kernel(const __grid_consta
   bool st = false;
   if (!p.state_only) {
     if (p.piece_state && pc.count > 1) {
-      start = p.piece_state + (size_t)unit * state;
+      start = p.piece_state + cut_unit * state;
     } else if (p.start) {
       start = p.start + ((size_t)pc.n * H + h) * state;
       st = p.start_t;
@@ -372,8 +381,8 @@ __global__ void __launch_bounds__(kRunThreads, 2) run_kernel(const __grid_consta
   float *dst = nullptr;
   bool dt = false;
   if (p.state_only) {
-    dst = p.piece_state + (size_t)unit * state;
-    if (blockIdx.y == 0 && tid == 0) p.piece_log[unit] = (double)logs * 0x1p-32;
+    dst = p.piece_state + cut_unit * state;
+    if (blockIdx.y == 0 && tid == 0) p.piece_log[cut_unit] = (double)logs * 0x1p-32;
   } else if (p.fin && pc.s == (p.back ? 0 : pc.count - 1)) {
     dst = p.fin + ((size_t)pc.n * H + h) * state;
     dt = p.fin_t;
@@ -400,7 +409,7 @@ cudaError_t launch_run_t(const Run *r, int n, int widest, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = prepare_kernel(run_kernel<T, ROWS>, RunSmem(128, true).total * (int)sizeof(float), ready);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((int64_t)r->cut.n_pieces * r->cut.H), (unsigned)simt_slices(widest), (unsigned)n);
+  const dim3 grid((unsigned)run_blocks(r->cut, r->state_only), (unsigned)simt_slices(widest), (unsigned)n);
   run_kernel<T, ROWS><<<grid, kRunThreads, bytes, s>>>(P);
   return cudaGetLastError();
 }
@@ -603,15 +612,15 @@ cudaError_t launch_step_t(const StepProblem &p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_plan(const Cut &c, int32_t *seg_off, int32_t *order, cudaStream_t s) {
-  plan_kernel<<<1, 1024, 0, s>>>(c, seg_off, order);
+cudaError_t launch_plan(const Cut &c, int32_t *seg_off, int32_t *cut_off, int32_t *order, cudaStream_t s) {
+  plan_kernel<<<1, 1024, 0, s>>>(c, seg_off, cut_off, order);
   return cudaGetLastError();
 }
 
 cudaError_t launch_join(const Run *r, int n, cudaStream_t s) {
   Runs P;
   for (int i = 0; i < n; ++i) P.run[i] = r[i];
-  const dim3 grid((unsigned)(r->cut.n_seqs * r->cut.H), (unsigned)((r->dy * r->dz + 255) / 256), (unsigned)n);
+  const dim3 grid((unsigned)run_blocks(r->cut, 1), (unsigned)((r->dy * r->dz + 255) / 256), (unsigned)n);
   join_kernel<<<grid, 256, 0, s>>>(P);
   return cudaGetLastError();
 }

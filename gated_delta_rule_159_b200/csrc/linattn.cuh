@@ -19,12 +19,16 @@ struct Cut {
   const int32_t *cu;       // device [n_seqs + 1] token offsets, or NULL: n_seqs x seq_len tokens
   const int32_t *seg_off;  // device [n_seqs + 1]: first piece of every sequence (packed batches with
                            // cuts), or NULL: every sequence has `per_seq` pieces
+  const int32_t *cut_off;  // device [n_seqs + 1] beside it: pieces of cut sequences in front of every sequence.
+                           // Only they have a state of their own to keep: a batch of many short sequences
+                           // needs no room for each.
   const int32_t *order;    // device [n_pieces]: the pieces from the longest down (-1 behind the last), or
                            // NULL: as they come.  Blocks start in that order, so that no long piece is left
                            // for the end of a ragged batch.
   int n_seqs, seq_len, H;
   int per_seq;             // pieces per sequence without seg_off
   int n_pieces;            // pieces in all (an upper bound with seg_off)
+  int n_cut;               // pieces of cut sequences (an upper bound with cut_off)
   int target, grain;       // pieces are cut at multiples of grain
   int t_total;
   int sorted;              // the call asks for an order
@@ -45,8 +49,8 @@ __host__ __device__ inline int piece_count(int len, int target, int grain) {
 struct Piece {
   int n, s, count;  // sequence, index of the piece in it, pieces of the sequence
   int t0, len;      // first token, tokens
-  int first_piece;  // global index of the sequence's piece 0
   int unit;         // global index of the piece, times H, plus the head
+  int cut;          // its number among the pieces of cut sequences (count > 1)
 };
 constexpr int kMaxSorted = 1024;  // pieces that one block sorts
 
@@ -62,31 +66,45 @@ __device__ __forceinline__ void seq_bounds(const Cut &c, int n, int *t0, int *le
   *len = b - a;
 }
 
-// Piece number g; false past the last one (the grid covers an upper bound).
-__device__ __forceinline__ bool find_piece(const Cut &c, int g, Piece *p) {
-  int n, first;
-  if (c.seg_off) {
-    if (g >= c.seg_off[c.n_seqs]) return false;
-    int lo = 0, hi = c.n_seqs;  // last n with seg_off[n] <= g
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (c.seg_off[mid] <= g) lo = mid; else hi = mid;
-    }
-    n = lo;
-    first = c.seg_off[n];
-  } else {
-    n = g / c.per_seq;
-    first = n * c.per_seq;
+// The last of n offsets that is not above g.
+__device__ __forceinline__ int last_below(const int32_t *off, int n, int g) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= g) lo = mid; else hi = mid;
   }
+  return lo;
+}
+// Piece s of sequence n.
+__device__ __forceinline__ void fill_piece(const Cut &c, int n, int s, Piece *p) {
   int t0, len;
   seq_bounds(c, n, &t0, &len);
   const int pl = piece_len(len, c.target, c.grain);
   p->n = n;
-  p->s = g - first;
-  p->count = c.seg_off ? c.seg_off[n + 1] - first : c.per_seq;
-  p->first_piece = first;
-  p->t0 = t0 + min(p->s * pl, len);
-  p->len = min(pl, len - min(p->s * pl, len));
+  p->s = s;
+  p->count = c.seg_off ? c.seg_off[n + 1] - c.seg_off[n] : c.per_seq;
+  p->t0 = t0 + min(s * pl, len);
+  p->len = min(pl, len - min(s * pl, len));
+  // (offsets out of order may count more pieces than there is room for)
+  p->cut = min((c.cut_off ? c.cut_off[n] : n * c.per_seq) + s, c.n_cut - 1);
+}
+// Piece number g; false past the last one (the grid covers an upper bound).
+__device__ __forceinline__ bool find_piece(const Cut &c, int g, Piece *p) {
+  if (c.seg_off) {
+    if (g >= c.seg_off[c.n_seqs]) return false;
+    const int n = last_below(c.seg_off, c.n_seqs, g);
+    fill_piece(c, n, g - c.seg_off[n], p);
+  } else {
+    fill_piece(c, g / c.per_seq, g % c.per_seq, p);
+  }
+  return true;
+}
+// The same by the number among the pieces of cut sequences.
+__device__ __forceinline__ bool find_cut_piece(const Cut &c, int i, Piece *p) {
+  if (!c.cut_off) return find_piece(c, i, p);
+  if (i >= c.cut_off[c.n_seqs]) return false;
+  const int n = last_below(c.cut_off, c.n_seqs, i);
+  fill_piece(c, n, i - c.cut_off[n], p);
   return true;
 }
 
@@ -100,12 +118,19 @@ constexpr int kMarkDots = 8;  // partial products a mark, one of each state warp
 __host__ __device__ inline int mark_slot(int g, int t) { return g + t / (kGroup * kChunk); }
 inline size_t mark_slots(const Cut &c) { return (size_t)c.n_pieces + (size_t)(c.t_total / (kGroup * kChunk)) + 1; }
 
-// The piece of the block's unit (a position in the order, and a head).
-__device__ __forceinline__ bool find_unit(const Cut &c, int block, Piece *p) {
-  const int pos = block / c.H, g = c.order ? c.order[pos] : pos;
+// The piece of the block's unit (a position in the order, and a head); with `cuts` one of a cut sequence.
+__device__ __forceinline__ bool find_unit(const Cut &c, int block, bool cuts, Piece *p) {
+  const int pos = block / c.H;
+  if (cuts) {
+    p->unit = 0;
+    return find_cut_piece(c, pos, p);
+  }
+  const int g = c.order ? c.order[pos] : pos;
   p->unit = g * c.H + block % c.H;
   return g >= 0 && find_piece(c, g, p);
 }
+// Blocks of a run: all units, or those whose end states the others start from.
+inline int64_t run_blocks(const Cut &c, int state_only) { return (int64_t)(state_only ? c.n_cut : c.n_pieces) * c.H; }
 
 // log_a below this is a reset: e^-104 is 0 in fp32, and sums over a chunk stay finite and fine enough
 // (32 resets come to 4800 in log2, a float's step there is 2^-11).
@@ -131,8 +156,8 @@ struct Run {
   int back;              // the backward form
   // Cut sequences: the end state of every piece from a zero start, then the start of every
   // piece (natural [dy][dz] layout), and the sum of its log_a.
-  float *piece_state;    // [n_pieces * H][dy * dz], NULL when nothing is cut
-  double *piece_log;     // [n_pieces * H]
+  float *piece_state;    // [n_cut * H][dy * dz], NULL when nothing is cut
+  double *piece_log;     // [n_cut * H]
   int state_only;        // write piece_state and piece_log, no out
   // For the gradient of log_a: partial dots of every out row with the row of m (Hm heads, dz
   // columns) over the columns of one slice, [slices][T, H] (the tensor-core runs: two halves, [2][H, T]);
@@ -149,7 +174,7 @@ struct Run {
   int dtype;
 };
 
-cudaError_t launch_plan(const Cut &c, int32_t *seg_off, int32_t *order, cudaStream_t stream);
+cudaError_t launch_plan(const Cut &c, int32_t *seg_off, int32_t *cut_off, int32_t *order, cudaStream_t stream);
 // n runs over the same cut: the forward, or the three of the gradients in one launch.
 constexpr int kMaxRuns = 3;
 cudaError_t launch_join(const Run *r, int n, cudaStream_t stream);

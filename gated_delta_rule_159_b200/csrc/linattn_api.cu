@@ -72,6 +72,8 @@ int sm_count() {
   return sms;
 }
 
+constexpr int64_t kLeastTc = 512;  // tokens of the shortest pieces of the tensor-core runs
+
 // Where the (sequence, head) units alone leave SMs idle, long sequences are cut into pieces that
 // run side by side (each piece's end state first, the join, then the outputs): half as much again
 // of the work, spread over all SMs.  The target is the balanced share of tokens per worker; the
@@ -87,7 +89,7 @@ Cut make_cut(const gdn2_linattn_dims *d, const int32_t *cu, bool packed, int run
   // Pieces no shorter than what a pass over their states costs: 512 tokens on the tensor cores; in fp32,
   // where a step of 32 tokens is long, one step (4 heads of 32 x 32, 600 tokens: 37 us, from pieces of
   // 64 on 43, of 128 on 78; 3 ragged sequences' gradients, 1201 tokens, 48 x 80: 111, 115 and 162 us).
-  const int64_t least = tc ? 512 : gdn2::lin::kTile32;
+  const int64_t least = tc ? kLeastTc : gdn2::lin::kTile32;
   if (target < least) target = least;
   Cut c;
   memset(&c, 0, sizeof(c));
@@ -99,28 +101,30 @@ Cut make_cut(const gdn2_linattn_dims *d, const int32_t *cu, bool packed, int run
   c.target = target < gdn2::lin::kNoCut / 2 ? (int)target : gdn2::lin::kNoCut;
   c.grain = tc ? gdn2::lin::kChunk : gdn2::lin::kTile32;
   if (packed) {
-    const bool any = T / c.target >= 2;
-    if (!any) c.target = gdn2::lin::kNoCut;
+    // a cut sequence has two targets of tokens at least, and no more pieces than targets
+    if (T / c.target < 2) c.target = gdn2::lin::kNoCut;
     c.per_seq = 1;
-    c.n_pieces = any ? (int)(d->n_seqs + T / c.target) : d->n_seqs;
+    c.n_cut = (int)(T / c.target);
+    c.n_pieces = d->n_seqs + c.n_cut;
   } else {
     c.per_seq = gdn2::lin::piece_count(d->seq_len, c.target, c.grain);
     c.n_pieces = d->n_seqs * c.per_seq;
+    c.n_cut = c.per_seq > 1 ? c.n_pieces : 0;
   }
   c.sorted = packed && c.n_pieces > 1 && c.n_pieces <= gdn2::lin::kMaxSorted && (int64_t)c.n_pieces * c.H * slices * runs > workers;
   return c;
 }
-bool has_cuts(const Cut &c) { return c.n_pieces > c.n_seqs; }
+bool has_cuts(const Cut &c) { return c.n_cut > 0; }
 
-// The cut's part of a workspace: piece offsets and order, log sums and states.
+// The cut's part of a workspace: piece offsets (of all, and of cut sequences) and order, log sums and states.
 struct CutLayout {
   size_t off_seg, off_order, off_log, off_state, end;
 };
 CutLayout cut_layout(const Cut &c, size_t at, size_t state, size_t runs = 1) {
   CutLayout L;
-  const size_t units = has_cuts(c) ? (size_t)c.n_pieces * c.H : 0;
+  const size_t units = (size_t)c.n_cut * c.H;
   L.off_seg = at;
-  L.off_order = L.off_seg + (units ? up256(((size_t)c.n_seqs + 1) * sizeof(int32_t)) : 0);
+  L.off_order = L.off_seg + (units ? up256(2 * ((size_t)c.n_seqs + 1) * sizeof(int32_t)) : 0);
   L.off_log = L.off_order + (c.sorted ? up256((size_t)c.n_pieces * sizeof(int32_t)) : 0);
   L.off_state = L.off_log + up256(runs * units * sizeof(double));
   L.end = L.off_state + up256(runs * units * state * sizeof(float));
@@ -181,9 +185,11 @@ cudaError_t prepare(Cut &c, char *ws, const CutLayout &L, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (c.cu && (has_cuts(c) || c.sorted)) {
     int32_t *off = has_cuts(c) ? reinterpret_cast<int32_t *>(ws + L.off_seg) : nullptr;
+    int32_t *cut_off = off ? off + c.n_seqs + 1 : nullptr;
     int32_t *order = c.sorted ? reinterpret_cast<int32_t *>(ws + L.off_order) : nullptr;
-    e = gdn2::lin::launch_plan(c, off, order, s);
+    e = gdn2::lin::launch_plan(c, off, cut_off, order, s);
     c.seg_off = off;
+    c.cut_off = cut_off;
     c.order = order;
   }
   return e;
@@ -202,22 +208,31 @@ Run base_run(const gdn2_linattn_dims *d, const void *log_a, const Cut &c, char *
 }
 
 // The three runs of the gradients go side by side in one launch in fp32 (3 ragged sequences, 1201
-// tokens, 4 heads of 48 x 80: 157 us, one after the other 312), and on the tensor cores where a run alone
-// would leave half of the SMs idle or need cuts, of which three need fewer (16 heads; 11 ragged
-// sequences, 9001 tokens: 222 us for 322; one of 4096: 160 for 190; where the pieces then divide badly
-// among the SMs it costs: 3 of 20246, 697 for 573).  Else one after the other (8 x 4096 tokens: 510 us,
-// in one launch 682): each run has a kernel of its own, smaller and faster, and with gradients of log_a
-// the second run's states need not be written and read again for the products.
+// tokens, 4 heads of 48 x 80: 157 us, one after the other 312).  On the tensor cores that kernel is slower a
+// chunk (four terms for all, 97 KB of code), and with gradients of log_a the second run's states are
+// written and read again for the products.  It pays where a run alone leaves SMs idle or needs more cuts than
+// three: with lengths that are known, where it needs cuts or has units for half of the SMs; with
+// cu_seqlens, whose lengths the host does not see, up to two units an SM, since ragged ones leave many
+// idle.  With gradients of log_a, only where it takes no cuts (known) or at most two of the shortest
+// pieces' tokens an SM.  Times in one launch / one after the other, with gradients of log_a and without, us, 16 heads:
+//   one launch taken:  1 x 4096 170/207, 119/183; 3 x 6748 430/500, 346/426; 11 ragged, 9001 tokens 250/373, 189/324;
+//                      8 ragged, 8192 342/345, 218/289; 16 ragged, 32768, without 483/727
+//   three taken:       8 x 4096 686/483, 516/405; 1 x 20000 593/512; 3 ragged, 20246 678/571; 11 ragged, 30000 881/722;
+//                      64 ragged, 32768 875/727, 665/597
+//   taken and slower:  8 x 4096 given by cu_seqlens, without gradients of log_a, 516 for 405; 16 ragged, 32768, with
+//                      them, 862 for 665
 struct BwdPlan {
   bool together;
   Cut cut;
 };
 BwdPlan plan_bwd(const gdn2_linattn_dims *d, const int32_t *cu, bool packed) {
   BwdPlan p;
-  p.cut = make_cut(d, cu, packed);
-  const bool idle = 2 * (int64_t)d->n_seqs * d->n_heads <= sm_count();
-  p.together = !tensor_core(d) || has_cuts(p.cut) || idle;
-  if (p.together) p.cut = make_cut(d, cu, packed, 3);
+  const Cut one = make_cut(d, cu, packed), three = make_cut(d, cu, packed, 3);
+  const int64_t units = (int64_t)d->n_seqs * d->n_heads, sms = sm_count();
+  const bool light = (d->flags & GDN2_LINATTN_HEAD_DECAY) || tokens_of(d, packed) * d->n_heads <= 2 * kLeastTc * sms;
+  p.together = !tensor_core(d) || (packed ? units <= 2 * sms && light
+                                          : (has_cuts(one) || 2 * units <= sms) && (light || !has_cuts(three)));
+  p.cut = p.together ? three : one;
   return p;
 }
 
@@ -275,7 +290,7 @@ int bwd_runs(const void *q, const void *k, const void *v, const void *log_a, con
   for (int i = 0; i < 3; ++i) {
     runs[i] = base_run(d, log_a, c, ws, L.cut);
     if (plan.together) {
-      const size_t units = (size_t)c.n_pieces * H;
+      const size_t units = (size_t)c.n_cut * H;
       runs[i].piece_log += i * units;
       runs[i].piece_state += i * units * d->d_k * d->d_v;
     }

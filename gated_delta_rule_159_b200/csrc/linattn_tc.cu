@@ -216,9 +216,10 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int H = r.cut.H;
   Piece pc;
-  if (!find_unit(r.cut, block, &pc)) return;
-  const int unit = pc.unit, h = unit % H;
   const bool only = r.state_only != 0;
+  if (!find_unit(r.cut, block, only, &pc)) return;
+  const int h = block % H;
+  const size_t cut_unit = (size_t)pc.cut * H + h;
   // the runs with four terms that have a launch of their own (the forward's, dv's) have no dots, marks or fp32 rows
   constexpr bool PLAIN = WAY != 2 && NT == 4;
   const bool marks = !PLAIN && !only && r.marks, out_f32 = !PLAIN && r.out_f32;
@@ -454,7 +455,7 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
         if (lane == 0) ptx::mbar_arrive(bar(BAR_ROWDEC));
       }
     }
-    if (only && lane == 0) r.piece_log[unit] = (double)logs * (0x1p-32 / (double)kLog2);
+    if (only && lane == 0) r.piece_log[cut_unit] = (double)logs * (0x1p-32 / (double)kLog2);
   } else if (warp < kOut0) {
     // ---------------------------------------------------------------- P: half a token row a thread
     const int wq = warp & 3, row = wq * 32 + lane, half = (warp - kRows0) >> 2;
@@ -763,10 +764,10 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
     float *dst = nullptr;
     bool flip_start = false, flip_dst = false;
     if (only) {
-      dst = r.piece_state + (size_t)unit * D * D;
+      dst = r.piece_state + cut_unit * D * D;
     } else {
       if (r.piece_state && pc.count > 1) {
-        start = r.piece_state + (size_t)unit * D * D;
+        start = r.piece_state + cut_unit * D * D;
       } else if (r.start) {
         start = r.start + ((size_t)pc.n * H + h) * D * D;
         flip_start = r.start_t;
@@ -788,7 +789,7 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
     }
     ptx::tmem_wait_st();
     // marks of this thread's part of the state behind group `g` of chunks
-    auto mark_unit = [&](int g) { return (size_t)mark_slot(unit / H, pc.t0 + g * kGroup * C) * H + h; };
+    auto mark_unit = [&](int g) { return (size_t)mark_slot(pc.unit / H, pc.t0 + g * kGroup * C) * H + h; };
     auto ends_group = [&](int no) { return (no + 1) % kGroup == 0 || no == nch - 1; };
     float2 g2 = make_float2(1.f, 0.f);  // the last chunk's decay
     for (int k = 0; k <= nch; ++k) {
@@ -970,7 +971,7 @@ cudaError_t launch_t(const TcRun &P, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = prepare_kernel(run_tc_kernel<WAY, NT>, (int)kSmemBytes, ready);
   if (e != cudaSuccess) return e;
-  run_tc_kernel<WAY, NT><<<(unsigned)((int64_t)P.r.cut.n_pieces * P.r.cut.H), kThreads, kSmemBytes, s>>>(P);
+  run_tc_kernel<WAY, NT><<<(unsigned)run_blocks(P.r.cut, P.r.state_only), kThreads, kSmemBytes, s>>>(P);
   return cudaGetLastError();
 }
 
@@ -1008,7 +1009,7 @@ cudaError_t launch_grads_tc(const Run *r, int32_t *status, cudaStream_t s) {
   TcGrads P;
   for (int i = 0; i < 3; ++i)
     if (!fill(&P.run[i], r[i], status, hook_ns)) return cudaErrorInvalidValue;
-  grads_tc_kernel<<<(unsigned)(3 * (int64_t)r[0].cut.n_pieces * r[0].cut.H), kThreads, kSmemBytes, s>>>(P);
+  grads_tc_kernel<<<(unsigned)(3 * run_blocks(r[0].cut, r[0].state_only)), kThreads, kSmemBytes, s>>>(P);
   return cudaGetLastError();
 }
 

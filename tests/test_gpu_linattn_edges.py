@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import linattn_ref as ref
+from test_gpu_linattn_long import _check_units
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +165,11 @@ def test_states_in_the_norm(g, case):
     for n, h, _, u in ref.units(one, cu, keep, heads):
         want[n, h] = ref.run(u["k"], u["q"], u["dO"], u["la"], u["dS_T"], back=True)["fin"]
     assert _norms(got["dS0"][:, :keep], want) < 1.2e-6
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 24)])
+def test_cut_sequences_among_many_short_ones(g, dtype, d):
+    """More sequences than the plan counts at once; the two long ones are cut, and only they."""
+    lens = (2,) * 700 + (3000,) + (1, 0, 3) * 300 + (2500,) + (5,)
+    p, cu = ref.problem(lens, 1, 1, d, d, dtype, "token", True, seed=80)
+    _check_units(g, p, cu, 1, 1, dtype == BF, [(0, 0), (700, 0), (701, 0), (1601, 0), (1602, 0)])

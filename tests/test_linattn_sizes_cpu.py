@@ -33,3 +33,38 @@ def test_token_numbers_stay_in_32_bits(g, d, dtype):
         cu = P if packed else None
         assert g.lib.gdn2_linattn_fwd(P, P, P, P, None, cu, P, None, ctypes.byref(dims), P, 1 << 50,
                                       None) == g.ERR_UNSUPPORTED
+
+
+def test_short_sequences_need_no_state_each(g):
+    """A packed batch has room for the states of cut sequences' pieces: no more than the balanced share calls for,
+    however many sequences there are."""
+    H, d = 16, 128
+    state = 4 * d * d * H
+
+    def fwd(n, tokens):
+        return g.lib.gdn2_linattn_fwd_workspace_size(ctypes.byref(g.LinattnDims(n, tokens, H, H, d, d, 0, 0, 0, 0)), 1)
+
+    few, many = fwd(32, 65536), fwd(1024, 65536)
+    assert many - few < 1024 * 64               # offsets and order, no states
+    assert many < 160 * 4 * d * d + (1 << 20)   # at most a piece for each of the SMs
+    assert fwd(32, 65536) > state               # sequences long enough to be cut may be among them
+    # the gradients': marks and dots grow with the batch, the pieces' states (three runs) do not
+    bwd = [g.lib.gdn2_linattn_bwd_workspace_size(
+        ctypes.byref(g.LinattnDims(n, 65536, H, H, d, d, 0, 0, g.LINATTN_HEAD_DECAY, 0)), 1) for n in (1, 1024)]
+    assert bwd[1] < bwd[0] + 1024 * 64 and bwd[1] < 3 * 160 * 4 * d * d + (1 << 20)
+
+
+def test_gradients_of_a_packed_batch_take_one_launch_by_its_size(g):
+    """Seen from the workspace: two runs' marks of the state where the three share a launch, one run's else."""
+    H, d = 16, 128
+    mark = 4 * d * d * H
+
+    def bwd(n, tokens, packed):
+        return g.lib.gdn2_linattn_bwd_workspace_size(
+            ctypes.byref(g.LinattnDims(n, tokens if packed else tokens // n, H, H, d, d, 0, 0, 0, 0)), packed)
+
+    groups = 32768 // 256 + 8
+    both = 2 * groups * mark
+    assert bwd(8, 32768, 0) < both and bwd(8, 32768, 1) < both        # as many units as SMs, long: one after the other
+    assert bwd(11, 9001, 1) > 2 * (9001 // 256 + 11) * mark           # short ones, ragged: one launch
+    assert bwd(1, 4096, 0) > 2 * (4096 // 256) * mark                 # SMs idle: one launch
