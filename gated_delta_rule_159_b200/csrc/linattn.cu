@@ -417,12 +417,13 @@ cudaError_t launch_run_t(const Run *r, int n, int widest, cudaStream_t s) {
 // ---------------------------------------------------------------- gradient of log_a
 // a_t stands once in every pair (i, j) with j < t <= i:
 //   dlog_a_t = sum_{i >= t} (q_i . dq_i - k_i . dk_i) + <S_T, dS_T>,
-// a suffix sum over the sequence, held in fp64: its terms cancel.
+// a suffix sum over the sequence, held in fp64: its terms cancel.  At a reset they do so wholly (a_t = 0), but for
+// their roundings: 0 is written there.
 constexpr int kScan = 256;
 template <typename T>
 __global__ void __launch_bounds__(kScan) dlog_kernel(const float *dq, int nq, const float *dk, int nk,
                                                      const float *S_T, const float *dS_T, int size, int no_start,
-                                                     Cut c, T *dlog) {
+                                                     const T *log_a, Cut c, T *dlog) {
   __shared__ double sums[kScan / 32];
   const int H = c.H, n = blockIdx.x / H, h = blockIdx.x % H;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -459,7 +460,8 @@ __global__ void __launch_bounds__(kScan) dlog_kernel(const float *dq, int nq, co
     double before = carry;
     for (int w = 0; w < warp; ++w) before += sums[w];
     // the first token decays nothing where no state comes in
-    if (t >= 0) dlog[at] = from_f32<T>(no_start && t == 0 ? 0.f : (float)(before + incl));
+    if (t >= 0)
+      dlog[at] = from_f32<T>((no_start && t == 0) || to_f32<T>(log_a[at]) <= kMinLog ? 0.f : (float)(before + incl));
     for (int w = 0; w < kScan / 32; ++w) carry += sums[w];
   }
 }
@@ -638,13 +640,15 @@ cudaError_t launch_run_simt(const Run *r, int n, cudaStream_t s) {
 }
 
 cudaError_t launch_dlog_simt(const float *dots_q, int nq, const float *dots_k, int nk, const float *S_T,
-                             const float *dS_T, int dk, int dv, bool no_start, const Cut &c, void *dlog, int dtype,
-                             cudaStream_t s) {
+                             const float *dS_T, int dk, int dv, bool no_start, const void *log_a, const Cut &c, void *dlog,
+                             int dtype, cudaStream_t s) {
   const unsigned grid = (unsigned)(c.n_seqs * c.H);
   if (dtype == GDN2_BF16)
-    dlog_kernel<<<grid, kScan, 0, s>>>(dots_q, nq, dots_k, nk, S_T, dS_T, dk * dv, no_start, c, static_cast<__nv_bfloat16 *>(dlog));
+    dlog_kernel<<<grid, kScan, 0, s>>>(dots_q, nq, dots_k, nk, S_T, dS_T, dk * dv, no_start,
+                                       static_cast<const __nv_bfloat16 *>(log_a), c, static_cast<__nv_bfloat16 *>(dlog));
   else
-    dlog_kernel<<<grid, kScan, 0, s>>>(dots_q, nq, dots_k, nk, S_T, dS_T, dk * dv, no_start, c, static_cast<float *>(dlog));
+    dlog_kernel<<<grid, kScan, 0, s>>>(dots_q, nq, dots_k, nk, S_T, dS_T, dk * dv, no_start,
+                                       static_cast<const float *>(log_a), c, static_cast<float *>(dlog));
   return cudaGetLastError();
 }
 

@@ -190,11 +190,11 @@ cudaError_t launch_marks(const float *a, const float *b, float *mark_dots, const
 // dlog_a of the fp32 runs: dots_q (of dq with q), dots_k (of dk with k), and <S_T, dS_T> (S_T
 // may be NULL with dS_T).
 cudaError_t launch_dlog_simt(const float *dots_q, int nq, const float *dots_k, int nk, const float *S_T,
-                             const float *dS_T, int dk, int dv, bool no_start, const Cut &c, void *dlog, int dtype,
-                             cudaStream_t stream);
+                             const float *dS_T, int dk, int dv, bool no_start, const void *log_a, const Cut &c, void *dlog,
+                             int dtype, cudaStream_t stream);
 // dlog_a of the tensor-core runs (linattn_tc.cu).
-cudaError_t launch_dlog_tc(const float *dots_q, const float *dots_k, const float *mark_dots, const Cut &c, bool no_start,
-                           void *dlog, cudaStream_t stream);
+cudaError_t launch_dlog_tc(const float *dots_q, const float *dots_k, const float *mark_dots, const void *log_a, const Cut &c,
+                           bool no_start, void *dlog, cudaStream_t stream);
 // out[t, g, :] = sum over the heads of group g of part[t, h, :], for n (1 or 2) of them
 cudaError_t launch_group_sum(const float *const *part, void *const *out, int n, const Cut &c, int Hg, int d, int dtype,
                              cudaStream_t stream);

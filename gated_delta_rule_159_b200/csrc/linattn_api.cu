@@ -346,8 +346,8 @@ int bwd_runs(const void *q, const void *k, const void *v, const void *log_a, con
   }
   if (dlog_a) {
     const int n = gdn2::lin::simt_slices(d->d_k);
-    e = tc ? gdn2::lin::launch_dlog_tc(dots_q, dots_k, mark_dots, c, !S0, dlog_a, s)
-           : gdn2::lin::launch_dlog_simt(dots_q, n, dots_k, n, fin, dS_T, d->d_k, d->d_v, !S0, c, dlog_a, d->dtype_in, s);
+    e = tc ? gdn2::lin::launch_dlog_tc(dots_q, dots_k, mark_dots, log_a, c, !S0, dlog_a, s)
+           : gdn2::lin::launch_dlog_simt(dots_q, n, dots_k, n, fin, dS_T, d->d_k, d->d_v, !S0, log_a, c, dlog_a, d->dtype_in, s);
     if (e != cudaSuccess) return cuda_fail("linattn dlog_a", e);
   }
   return GDN2_OK;

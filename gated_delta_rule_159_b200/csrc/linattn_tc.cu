@@ -928,11 +928,12 @@ __global__ void __launch_bounds__(256) marks_kernel(const float *a, const float 
 
 // dlog_a_t = sum_{t <= i in the group} (q_i . dq_i - k_i . dk_i) + <S, dLoss/dS> behind the group.  The dots carry
 // bf16 products whose errors would add up along a sequence; the marks' product starts each group afresh.
+// It is a_t <S_{t-1}, dLoss/dS_t>: exactly 0 at a reset, where the sums leave the roundings of what cancels.
 // A warp per group of kGroup chunks.
 constexpr int kDlogWarps = 4;
 __global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *dots_q, const float *dots_k,
-                                                                  const float *mark_dots, Cut c, int no_start,
-                                                                  __nv_bfloat16 *dlog) {
+                                                                  const float *mark_dots, const __nv_bfloat16 *log_a,
+                                                                  Cut c, int no_start, __nv_bfloat16 *dlog) {
   constexpr int kTokens = kGroup * C;
   const int H = c.H, unit = blockIdx.x, h = unit % H, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Piece pc;
@@ -959,8 +960,10 @@ __global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *d
         if (lane + d < 32) v[j] += down;
       }
       // the first token decays nothing where no state comes in
-      const bool none = no_start && pc.s == 0 && g == 0 && 32 * j + lane == 0;
-      if (32 * j + lane < cnt) dlog[(t0 + 32 * j + lane) * H + h] = __float2bfloat16_rn(none ? 0.f : v[j] + behind);
+      const size_t out = (t0 + 32 * j + lane) * H + h;
+      const bool first = no_start && pc.s == 0 && g == 0 && 32 * j + lane == 0;
+      if (32 * j + lane < cnt)
+        dlog[out] = __float2bfloat16_rn(first || __bfloat162float(log_a[out]) <= kMinLog ? 0.f : v[j] + behind);
       behind += __shfl_sync(0xffffffffu, v[j], 0);
     }
   }
@@ -1020,12 +1023,13 @@ cudaError_t launch_marks(const float *a, const float *b, float *mark_dots, const
   return cudaGetLastError();
 }
 
-cudaError_t launch_dlog_tc(const float *dots_q, const float *dots_k, const float *mark_dots, const Cut &c, bool no_start,
-                           void *dlog, cudaStream_t s) {
+cudaError_t launch_dlog_tc(const float *dots_q, const float *dots_k, const float *mark_dots, const void *log_a, const Cut &c,
+                           bool no_start, void *dlog, cudaStream_t s) {
   if (c.t_total == 0) return cudaSuccess;
   const int64_t groups = (int64_t)c.t_total / (kGroup * C * kDlogWarps) + 1;  // of the longest piece, at most
   const dim3 grid((unsigned)((int64_t)c.n_pieces * c.H), (unsigned)(groups < 16 ? groups : 16));
-  dlog_tc_kernel<<<grid, 32 * kDlogWarps, 0, s>>>(dots_q, dots_k, mark_dots, c, no_start, static_cast<__nv_bfloat16 *>(dlog));
+  dlog_tc_kernel<<<grid, 32 * kDlogWarps, 0, s>>>(dots_q, dots_k, mark_dots, static_cast<const __nv_bfloat16 *>(log_a), c,
+                                                  no_start, static_cast<__nv_bfloat16 *>(dlog));
   return cudaGetLastError();
 }
 

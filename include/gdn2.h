@@ -522,8 +522,8 @@ int gdn2_linattn_step(const void *q, const void *k, const void *v, const void *l
  *   dO              [T_tot, H, d_v] dtype_in
  *   dS_T            [N, H, d_k, d_v] fp32 or NULL (zero)
  *   dq, dk, dv      written, dtype_in, shaped like q, k, v
- *   dlog_a          [T_tot, H] dtype_in; NULL with GDN2_LINATTN_HEAD_DECAY (fixed decays have no
- *                   gradient here)
+ *   dlog_a          [T_tot, H] dtype_in, 0 where log_a is at most -104; NULL with
+ *                   GDN2_LINATTN_HEAD_DECAY (fixed decays have no gradient here)
  *   dS0             [N, H, d_k, d_v] fp32 or NULL to skip
  *   workspace       at least gdn2_linattn_bwd_workspace_size bytes, as for gdn2_linattn_fwd
  * No output may alias an input or another output.

@@ -173,3 +173,13 @@ def test_cut_sequences_among_many_short_ones(g, dtype, d):
     lens = (2,) * 700 + (3000,) + (1, 0, 3) * 300 + (2500,) + (5,)
     p, cu = ref.problem(lens, 1, 1, d, d, dtype, "token", True, seed=80)
     _check_units(g, p, cu, 1, 1, dtype == BF, [(0, 0), (700, 0), (701, 0), (1601, 0), (1602, 0)])
+
+
+@pytest.mark.parametrize("dtype,d,H", [(BF, 128, 2), (BF, 128, 160), (F32, 24, 2)])
+def test_no_gradient_through_a_reset(g, dtype, d, H):
+    """a_t <S_{t-1}, dLoss/dS_t> is 0 where a_t is."""
+    p, cu = ref.problem((700, 90), H, H, d, d, dtype, "reset", True, seed=72)
+    got = g.linattn_bwd(p["q"], p["k"], p["v"], p["log_a"], p["dO"], p["S0"], p["dS_T"], p["cu"])
+    reset = p["log_a"].float() < -104.0
+    assert reset.any() and (got["dlog_a"][reset] == 0).all()
+    assert (got["dlog_a"][~reset] != 0).any()
