@@ -1,6 +1,7 @@
 // linattn.cu -- linear attention with a decay per head on the CUDA cores: the run for fp32 inputs
 // and for head sizes the tensor-core run does not take, the single-token step, and the helpers
 // both runs share (the cut plan, the join of the pieces, the gradient of log_a, head sums).
+#include <cmath>
 #include <type_traits>
 
 #include "linattn.cuh"
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kRunThreads, 2) run_kernel(const __grid_consta
   __shared__ __align__(16) float ps[TB][TB + 4];
   __shared__ float dot[TB][COLS / 4 + 1];
   __shared__ long long cum[TB];  // sums of log_a from the tile's first token, inclusive
-  __shared__ float fs[TB], ws[TB];
+  __shared__ float fs[TB], ws[TB], tile_g;
   const int H = p.cut.H, tid = threadIdx.x;
   Piece pc;
   if (blockIdx.y * COLS >= p.dz || !find_unit(p.cut, blockIdx.x, p.state_only, &pc)) return;
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(kRunThreads, 2) run_kernel(const __grid_consta
 
   const float fixed = p.per_head ? static_cast<const float *>(p.log_a)[h] : 0.f;
   long long logs = 0;
+  bool lost = false;  // a NaN was among the log_a
   const int tiles = (pc.len + TB - 1) / TB;
   for (int it = 0; it < tiles; ++it) {
     const int t0 = (p.back ? tiles - 1 - it : it) * TB, cnt = min(TB, pc.len - t0);
@@ -258,12 +260,17 @@ __global__ void __launch_bounds__(kRunThreads, 2) run_kernel(const __grid_consta
       const long long all = __shfl_sync(0xffffffffu, sum, TB - 1);
       cum[tid] = sum;
       const float here = expf(__ll2float_rn(sum) * 0x1p-32f), rest = expf(__ll2float_rn(all - sum) * 0x1p-32f);
-      fs[tid] = p.back ? rest : here;
+      // a NaN among them: what the state reaches through it, and the state
+      const uint32_t nans = __ballot_sync(0xffffffffu, isnan(la));
+      const bool hit = (p.back ? nans >> tid >> 1 : nans & (0xffffffffu >> (31 - tid))) != 0;
+      lost |= nans != 0;
+      fs[tid] = hit ? NAN : p.back ? rest : here;
       ws[tid] = p.back ? here : rest;
+      if (tid == TB - 1) tile_g = nans ? NAN : here;
       logs += all;
     }
     __syncthreads();
-    const float g = expf(__ll2float_rn(cum[TB - 1]) * 0x1p-32f);
+    const float g = tile_g;
 
     if (!p.state_only) {
       {  // P: rows i, i + 1 and columns j = c + 8 q, half of the sum over k a thread
@@ -382,7 +389,7 @@ __global__ void __launch_bounds__(kRunThreads, 2) run_kernel(const __grid_consta
   bool dt = false;
   if (p.state_only) {
     dst = p.piece_state + cut_unit * state;
-    if (blockIdx.y == 0 && tid == 0) p.piece_log[cut_unit] = (double)logs * 0x1p-32;
+    if (blockIdx.y == 0 && tid == 0) p.piece_log[cut_unit] = lost ? (double)NAN : (double)logs * 0x1p-32;
   } else if (p.fin && pc.s == (p.back ? 0 : pc.count - 1)) {
     dst = p.fin + ((size_t)pc.n * H + h) * state;
     dt = p.fin_t;

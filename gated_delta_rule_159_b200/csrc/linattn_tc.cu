@@ -31,6 +31,7 @@
 // and they still are what the CUDA cores wait for while products run.  X has one tile, Y and Z two stages.
 // The loops stay rolled, and what few calls need stands outside them or is compiled out: unrolled, or with such
 // code to jump over, the roles ran out of the instruction cache (8 x 4096 tokens: 182 us for 162).
+#include <cmath>
 #include <cstring>
 
 #include "linattn.cuh"
@@ -391,15 +392,20 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
              __uint_as_float((uint32_t)(n - a + 127) << 23);
     };
     fix logs = 0;
+    bool lost = false;  // a NaN was among them: the state is NaN from there on
     float a[4];
     if (nch > 0) load(0, a);
     bool ok = true;
     for (int k = 0; k < nch && ok; ++k) {
       const uint32_t stage = dec + DEC_W + (uint32_t)(k & 1) * DEC_STAGE;
       fix own[4];  // inclusive sums inside the lane
+      int nan = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j) {
         own[j] = __float2ll_rn(fmaxf(a[j], kMinLog) * kLog2 * 0x1p32f) + (j ? own[j - 1] : 0);
+        nan |= (int)isnan(a[j]) << j;
+      }
+      const uint32_t nans = __ballot_sync(0xffffffffu, nan != 0);
       if (k + 1 < nch) load(k + 1, a);
       fix incl = own[3];
 #pragma unroll
@@ -417,7 +423,7 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
       }
       logs += all;
       const bool mild = all >= -kMild;
-      const float2 g = power2(all);
+      float2 g = power2(all);
       float one[4], two[4];
       uint32_t w[2][3];
 #pragma unroll
@@ -432,6 +438,18 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
           const uint32_t b = bf16_bits(left);
           left -= bf16_value((uint16_t)b);
           w[j >> 1][n] = j & 1 ? w[j >> 1][n] | b << 16 : b;
+        }
+      }
+      if (nans) {  // the tokens that the state reaches through it, and the state
+        lost = true;
+        g.x = __int_as_float(0x7fc00000);
+        bool hit = (BACK ? nans >> lane >> 1 : nans & ((1u << lane) - 1u)) != 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = BACK ? 3 - i : i;
+          if (!BACK) hit |= (nan >> j & 1) != 0;
+          if (hit) one[j] = g.x;
+          if (BACK) hit |= (nan >> j & 1) != 0;
         }
       }
       if (k >= 2) ok = wait_warp(BAR_WFREE + (k & 1), (uint32_t)(k >> 1) + 1u);
@@ -455,7 +473,7 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
         if (lane == 0) ptx::mbar_arrive(bar(BAR_ROWDEC));
       }
     }
-    if (only && lane == 0) r.piece_log[cut_unit] = (double)logs * (0x1p-32 / (double)kLog2);
+    if (only && lane == 0) r.piece_log[cut_unit] = lost ? (double)NAN : (double)logs * (0x1p-32 / (double)kLog2);
   } else if (warp < kOut0) {
     // ---------------------------------------------------------------- P: half a token row a thread
     const int wq = warp & 3, row = wq * 32 + lane, half = (warp - kRows0) >> 2;

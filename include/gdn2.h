@@ -458,7 +458,8 @@ int gdn2_chunk_fwd_noalloc_status(gdn2_stream_t stream);
  *   flags       GDN2_LINATTN_HEAD_DECAY: log_a is fp32 [H], one fixed decay per head; else log_a is
  *               [T_tot, H] of dtype_in.
  * log_a <= 0 (not checked); -infinity (a reset) is allowed; in the prompt and gradient calls log_a below
- * -104 counts as -104 (a factor of 0 in fp32), and so does a NaN.  Conventions otherwise as above.
+ * -104 counts as -104 (a factor of 0 in fp32).  A NaN in log_a makes the state NaN from its token on, and what
+ * is read from it.  Conventions otherwise as above.
  * Supported: d_k and d_v up to 128, bf16 or fp32.  d_k = d_v = 128 in bf16 runs on the tensor cores: bf16
  * products and fp32 sums.  The state is fp32: S_T and dS0 are off by less than 1e-6 of themselves (in the
  * norm) whatever the length, beside 2^-33 a token from sums of log_a, and a state that nothing is written to

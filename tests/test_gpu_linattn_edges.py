@@ -183,3 +183,27 @@ def test_no_gradient_through_a_reset(g, dtype, d, H):
     reset = p["log_a"].float() < -104.0
     assert reset.any() and (got["dlog_a"][reset] == 0).all()
     assert (got["dlog_a"][~reset] != 0).any()
+
+
+@pytest.mark.parametrize("dtype,d,lens,H", [(BF, 128, (300, 200), 2), (BF, 128, (5000,), 1), (F32, 24, (300, 200), 2),
+                                            (BF, 128, (200, 300), 160)])
+def test_a_nan_decay_shows(g, dtype, d, lens, H):
+    """As in the single-token call: the state behind it is NaN, and so is every gradient that passed it."""
+    p, cu = ref.problem(lens, H, H, d, d, dtype, "token", True, seed=73)
+    at = 150
+    p["log_a"][at, 0] = float("nan")
+    o, S = g.linattn_fwd(p["q"], p["k"], p["v"], p["log_a"], p["S0"], p["cu"])
+    clean = torch.ones(len(lens), H, dtype=torch.bool, device="cuda")
+    clean[0, 0] = False
+    assert torch.isnan(S[0, 0]).all() and torch.isfinite(S[clean]).all()
+    assert torch.isnan(o[at:cu[1], 0]).all() and torch.isfinite(o[:, 1:]).all() and torch.isfinite(o[cu[1]:]).all()
+    assert torch.isfinite(o[:at, 0]).all()
+    got = g.linattn_bwd(p["q"], p["k"], p["v"], p["log_a"], p["dO"], p["S0"], p["dS_T"], p["cu"])
+    assert torch.isnan(got["dS0"][0, 0]).all() and torch.isfinite(got["dS0"][clean]).all()
+    assert torch.isnan(got["dq"][at:cu[1], 0]).all() and torch.isnan(got["dv"][:at, 0]).all()
+    assert torch.isfinite(got["dq"][:at, 0]).all() and torch.isfinite(got["dv"][at:, 0]).all()
+    assert torch.isnan(got["dlog_a"][at, 0]) and torch.isfinite(got["dlog_a"][:, 1:]).all()
+    step = p["log_a"][at:at + 1].contiguous()
+    S1 = p["S0"][:1].clone()
+    o1 = g.linattn_step(*(p[x][at:at + 1].contiguous() for x in "qkv"), step, S1)
+    assert torch.isnan(S1[0, 0]).all() and torch.isnan(o1[0, 0]).all() and torch.isfinite(S1[0, 1:]).all()
