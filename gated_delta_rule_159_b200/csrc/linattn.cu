@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kRunThreads, 2) run_kernel(const __grid_consta
       fs[tid] = hit ? NAN : p.back ? rest : here;
       ws[tid] = p.back ? here : rest;
       if (tid == TB - 1) tile_g = nans ? NAN : here;
-      logs += all;
+      logs = max(logs + all, kMinLogs);
     }
     __syncthreads();
     const float g = tile_g;

@@ -135,6 +135,8 @@ inline int64_t run_blocks(const Cut &c, int state_only) { return (int64_t)(state
 // log_a below this is a reset: e^-104 is 0 in fp32, and sums over a chunk stay finite and fine enough
 // (32 resets come to 4800 in log2, a float's step there is 2^-11).
 constexpr float kMinLog = -104.f;
+// A piece's sum of them, in units of 2^-32, stops here: 64 bits hold 14 million resets.
+constexpr long long kMinLogs = -(1ll << 60);
 
 // One run over all (piece, head) units:
 //   forward:   out_t = sum_{j <= t} e^{L_t - L_j} (x_t . y_j) z_j + e^{L_t} start^T x_t

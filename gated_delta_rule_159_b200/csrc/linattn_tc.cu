@@ -421,7 +421,7 @@ __device__ __forceinline__ void run_block(const TcRun &P, int block) {
         all += t;
         if (BACK ? b < (lane >> 3) : b > (lane >> 3)) far += t;
       }
-      logs += all;
+      logs = max(logs + all, kMinLogs);
       const bool mild = all >= -kMild;
       float2 g = power2(all);
       float one[4], two[4];
