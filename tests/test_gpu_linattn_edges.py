@@ -207,3 +207,47 @@ def test_a_nan_decay_shows(g, dtype, d, lens, H):
     S1 = p["S0"][:1].clone()
     o1 = g.linattn_step(*(p[x][at:at + 1].contiguous() for x in "qkv"), step, S1)
     assert torch.isnan(S1[0, 0]).all() and torch.isnan(o1[0, 0]).all() and torch.isfinite(S1[0, 1:]).all()
+
+
+# a decay per token only: a fixed one has no gradient
+DLOG = [((1, 0, 127, 300, 128, 129), 4, 2, "token"), ((385, 64), 2, 2, "strong"), ((400, 31), 2, 2, "reset"),
+        ((512,), 1, 1, "none"), ((1700, 90), 1, 1, "token"), ((2048,), 160, 160, "token"), ((2048,), 160, 80, "none"),
+        ((900,), 80, 80, "reset")]
+
+
+@pytest.mark.parametrize("dtype,d,limit", [
+    # bf16: the weights, the state's copy and the result are rounded to 2^-8, 0.17% of the value in the root mean
+    # square each; dlog_a is a sum of differences of two such dots, over 256 tokens at most
+    (BF, 128, 1e-2),
+    # fp32: some 2000 roundings of 2^-24, even if they all went one way
+    (F32, 40, 1.2e-4)])
+@pytest.mark.parametrize("case", DLOG, ids=lambda c: f"{'-'.join(map(str, c[0]))}_h{c[1]}.{c[2]}_{c[3]}")
+def test_gradients_in_the_norm(g, case, dtype, d, limit):
+    """Every gradient, log_a's above all: a bound from absolute values is larger than it is."""
+    lens, H, Hqk, decay = case
+    p, cu, one, keep = _problem(lens, H, Hqk, decay, dtype, d, 71)
+    got = g.linattn_bwd(p["q"], p["k"], p["v"], p["log_a"], p["dO"], p["S0"], p["dS_T"], p["cu"])
+    assert g.check_status(got["workspace"]) == g.OK
+    heads = keep * Hqk // H
+    want = ref.gradients(one, cu, keep, heads, dtype == BF)
+    for name in ("dlog_a", "dq", "dk", "dv"):
+        n = heads if name in ("dq", "dk") else keep
+        assert _norms(got[name][:, :n], want[name][0]) < limit, name
+
+
+def test_steps_do_not_drift(g):
+    """A fixed decay over 1000 single tokens with nothing written.  The step's factor is off by 2^-28 at most (0.4e-5
+    over all of them); a single float's error adds up, and these decays are some whose float is off by more than
+    2^-25.5 (2.1e-5).  The states' own roundings are at random and leave the mean of 16384 of them alone."""
+    la = -torch.exp2(torch.linspace(-14, -6, 4000, dtype=torch.float64)).float()
+    a = torch.exp(la.double())
+    worst = la[((a.float().double() - a).abs() / a) > 2.0 ** -25.5][:4]
+    assert worst.numel() == 4
+    H = 4
+    S = torch.randn(1, H, 128, 128, device="cuda").abs() + 0.5
+    want = torch.exp(1000 * worst.double()).cuda()[None, :, None, None] * S.double()
+    q, v = torch.zeros(1, H, 128, device="cuda"), torch.randn(1, H, 128, device="cuda")
+    for _ in range(1000):
+        g.linattn_step(q, q, v, worst.cuda(), S)
+    drift = ((S.double() - want) / want).mean((0, 2, 3)).abs()
+    assert (drift < 1000 * 2.0 ** -28 + 4 * 2.0 ** -24 * (1000 / 16384) ** 0.5).all(), drift
