@@ -162,9 +162,13 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# torch's own query (0.07 us a call; the public one builds a Stream, 1.3 us), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
-    index = device.index
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    return torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
 
 
 def _check(rc: int):

@@ -251,3 +251,16 @@ def test_steps_do_not_drift(g):
         g.linattn_step(q, q, v, worst.cuda(), S)
     drift = ((S.double() - want) / want).mean((0, 2, 3)).abs()
     assert (drift < 1000 * 2.0 ** -28 + 4 * 2.0 ** -24 * (1000 / 16384) ** 0.5).all(), drift
+
+
+def test_the_stream_is_the_current_one(g, monkeypatch):
+    """With torch's quick query and without it."""
+    dev = torch.device("cuda", torch.cuda.current_device())
+    side = torch.cuda.Stream()
+    for quick in (True, False):
+        if not quick:
+            monkeypatch.setattr(g, "_raw_stream", None)
+        assert g._stream(dev) == torch.cuda.current_stream().cuda_stream
+        with torch.cuda.stream(side):
+            assert g._stream(dev) == side.cuda_stream
+            assert g._stream(torch.device("cuda")) == side.cuda_stream
