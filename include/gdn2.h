@@ -459,7 +459,10 @@ int gdn2_chunk_fwd_noalloc_status(gdn2_stream_t stream);
  *               [T_tot, H] of dtype_in.
  * log_a <= 0 (not checked); -infinity (a reset) is allowed; in the prompt and gradient calls log_a below
  * -104 counts as -104 (a factor of 0 in fp32).  A NaN in log_a makes the state NaN from its token on, and what
- * is read from it.  Conventions otherwise as above.
+ * is read from it.  Products are formed over tiles of tokens: a NaN or an infinity in q, k, v or dO stays in its
+ * sequence and heads, but reaches tokens there that the sums themselves would not, up to 127 before or behind
+ * it.  So padding is left out by cu_seqlens, or finite.  Sums (q.k) v above 2^95 may come out infinite.
+ * Conventions otherwise as above.
  * Supported: d_k and d_v up to 128, bf16 or fp32.  d_k = d_v = 128 in bf16 runs on the tensor cores: bf16
  * products and fp32 sums.  The state is fp32: S_T and dS0 are off by less than 1e-6 of themselves (in the
  * norm) whatever the length, beside 2^-33 a token from sums of log_a, and a state that nothing is written to

@@ -264,3 +264,28 @@ def test_the_stream_is_the_current_one(g, monkeypatch):
         with torch.cuda.stream(side):
             assert g._stream(dev) == side.cuda_stream
             assert g._stream(torch.device("cuda")) == side.cuda_stream
+
+
+@pytest.mark.parametrize("dtype,d,tile", [(BF, 128, 128), (F32, 24, 32)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_how_far_a_nan_reaches(g, dtype, d, tile, bad):
+    """One bad value: tokens in front of its tile (behind it, for what is summed backward) keep every bit, and so do
+    the other head and the other sequence."""
+    p, cu = ref.problem((400, 300), 2, 2, d, d, dtype, "token", False, seed=81)
+    names = ("q", "k", "v", "log_a", "dO")
+    clean_o, clean_S = g.linattn_fwd(*(p[x] for x in names[:4]), None, p["cu"])
+    clean = g.linattn_bwd(*(p[x] for x in names), None, None, p["cu"])
+    at = 300
+    first, behind = at // tile * tile, (at // tile + 1) * tile
+    p["v"][at, 0, d // 2] = bad
+    o, S = g.linattn_fwd(*(p[x] for x in names[:4]), None, p["cu"])
+    far = torch.ones(700, 2, dtype=torch.bool, device="cuda")
+    far[first:400, 0] = False
+    assert torch.equal(o[far], clean_o[far]) and not torch.isfinite(o[at, 0]).all()
+    assert torch.equal(S[:, 1], clean_S[:, 1]) and torch.equal(S[1], clean_S[1])
+    got = g.linattn_bwd(*(p[x] for x in names), None, None, p["cu"])
+    assert torch.equal(got["dv"], clean["dv"])      # v is not in it
+    assert torch.equal(got["dq"][far], clean["dq"][far])
+    near = torch.zeros(700, 2, dtype=torch.bool, device="cuda")
+    near[first:behind, 0] = True                    # dk is k's tile of v alone
+    assert torch.equal(got["dk"][~near], clean["dk"][~near])
