@@ -421,8 +421,9 @@ int gdn2_linattn_fwd(const void *q, const void *k, const void *v, const void *lo
   Cut c = make_cut(dims, cu_seqlens, cu_seqlens != nullptr);
   const CutLayout L = cut_layout(c, kHeader, (size_t)dims->d_k * dims->d_v);
   rc = check_workspace(workspace, workspace_bytes, L.end);
-  const void *in[4] = {q, k, v, log_a}, *out[1] = {o};
-  if (!rc) rc = check_apart(out, 1, in, 4);
+  const void *in[5] = {q, k, v, log_a, cu_seqlens}, *out[2] = {o, S_T};
+  if (!rc) rc = check_apart(out, 2, in, 5);
+  if (!rc) rc = check_apart(out, 1, reinterpret_cast<const void *const *>(&S0), 1);  // S_T may be S0
   if (rc) return rc;
   char *ws = static_cast<char *>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -450,8 +451,8 @@ int gdn2_linattn_step(const void *q, const void *k, const void *v, const void *l
   if (!S || !aligned(S, 16)) return fail(GDN2_ERR_INVALID_ARG, "S must be non-NULL and 16-byte aligned");
   if (state_idx && n_slots < 1) return fail(GDN2_ERR_INVALID_ARG, "n_slots must be at least 1 (got %d)", n_slots);
   if (!aligned(state_idx, 4)) return fail(GDN2_ERR_INVALID_ARG, "state_idx is misaligned");
-  const void *in[4] = {q, k, v, log_a}, *out[2] = {o, S};
-  rc = check_apart(out, 2, in, 4);
+  const void *in[5] = {q, k, v, log_a, state_idx}, *out[2] = {o, S};
+  rc = check_apart(out, 2, in, 5);
   if (rc) return rc;
   gdn2::lin::StepProblem p;
   memset(&p, 0, sizeof(p));
@@ -486,8 +487,8 @@ int gdn2_linattn_bwd(const void *q, const void *k, const void *v, const void *lo
   BwdPlan plan = plan_bwd(dims, cu_seqlens, cu_seqlens != nullptr);
   const BwdLayout L = bwd_layout(dims, plan, false);
   rc = check_workspace(workspace, workspace_bytes, L.total);
-  const void *in[7] = {q, k, v, log_a, dO, S0, dS_T}, *out[5] = {dq, dk, dv, dlog_a, dS0};
-  if (!rc) rc = check_apart(out, 5, in, 7);
+  const void *in[8] = {q, k, v, log_a, dO, S0, dS_T, cu_seqlens}, *out[5] = {dq, dk, dv, dlog_a, dS0};
+  if (!rc) rc = check_apart(out, 5, in, 8);
   if (rc) return rc;
   char *ws = static_cast<char *>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -546,9 +547,9 @@ int gdn2_linattn_bwd_ckpt8(const int8_t *q_codes, const uint8_t *q_scales, const
   BwdPlan plan = plan_bwd(dims, cu_seqlens, cu_seqlens != nullptr);
   const BwdLayout L = bwd_layout(dims, plan, true);
   rc = check_workspace(workspace, workspace_bytes, L.total);
-  const void *in[10] = {q_codes, q_scales, k_codes, k_scales, v_codes, v_scales, log_a, dO, S0, dS_T};
+  const void *in[11] = {q_codes, q_scales, k_codes, k_scales, v_codes, v_scales, log_a, dO, S0, dS_T, cu_seqlens};
   const void *out[5] = {dq, dk, dv, dlog_a, dS0};
-  if (!rc) rc = check_apart(out, 5, in, 10);
+  if (!rc) rc = check_apart(out, 5, in, 11);
   if (rc) return rc;
   char *ws = static_cast<char *>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

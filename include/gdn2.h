@@ -491,7 +491,7 @@ typedef struct gdn2_linattn_dims {
  *   cu_seqlens   device int32 [N + 1] token offsets, or NULL: N sequences of seq_len tokens
  *   o            [T_tot, H, d_v] dtype_out = dtype_in (written; rows outside every sequence stay);
  *                must not alias an input
- *   S_T          [N, H, d_k, d_v] fp32 or NULL
+ *   S_T          [N, H, d_k, d_v] fp32 or NULL; must not alias an input but S0
  *   workspace    at least gdn2_linattn_fwd_workspace_size(dims, cu_seqlens != NULL) bytes, 256-byte
  *                aligned, uninitialised; one call at a time.  The size depends on the current
  *                device's SM count: sequences much longer than the balanced share of tokens per SM

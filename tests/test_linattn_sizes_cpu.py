@@ -68,3 +68,34 @@ def test_gradients_of_a_packed_batch_take_one_launch_by_its_size(g):
     assert bwd(8, 32768, 0) < both and bwd(8, 32768, 1) < both        # as many units as SMs, long: one after the other
     assert bwd(11, 9001, 1) > 2 * (9001 // 256 + 11) * mark           # short ones, ragged: one launch
     assert bwd(1, 4096, 0) > 2 * (4096 // 256) * mark                 # SMs idle: one launch
+
+
+def test_every_output_apart_from_every_input(g):
+    """S_T, the offsets and the indices as well: an address used twice is refused, but for S_T at S0's."""
+    at = [ctypes.c_void_p((i + 1) << 20) for i in range(20)]
+    dims = g.LinattnDims(2, 100, 2, 2, 128, 128, 0, 0, 0, 0)
+    ws = ctypes.c_void_p(1 << 40)
+
+    def fwd(**kw):
+        a = dict(zip(("q", "k", "v", "log_a", "S0", "cu", "o", "S_T"), at), **kw)
+        rc = g.lib.gdn2_linattn_fwd(a["q"], a["k"], a["v"], a["log_a"], a["S0"], a["cu"], a["o"], a["S_T"],
+                                    ctypes.byref(dims), ws, 1 << 50, None)
+        return rc, g.lib.gdn2_last_error().decode()
+
+    for kw in (dict(S_T=at[0]), dict(S_T=at[1]), dict(S_T=at[2]), dict(S_T=at[3]), dict(S_T=at[5]), dict(o=at[4]),
+               dict(o=at[5]), dict(o=at[7])):
+        rc, msg = fwd(**kw)
+        assert rc == g.ERR_INVALID_ARG and "address" in msg, kw
+    one = g.LinattnDims(2, 1, 2, 2, 128, 128, 0, 0, 0, 0)
+    for S, o in ((at[4], at[6]), (at[5], at[4])):  # the indices at at[4]
+        rc = g.lib.gdn2_linattn_step(at[0], at[1], at[2], at[3], S, 2, at[4], o, ctypes.byref(one), None)
+        assert rc == g.ERR_INVALID_ARG and "address" in g.lib.gdn2_last_error().decode()
+    grads = [at[7 + i] for i in range(5)]
+    for i in range(5):
+        out = [at[6] if i == j else x for j, x in enumerate(grads)]  # the offsets at at[6]
+        rc = g.lib.gdn2_linattn_bwd(at[0], at[1], at[2], at[3], None, at[6], at[4], None, *out, ctypes.byref(dims), ws,
+                                    1 << 50, None)
+        assert rc == g.ERR_INVALID_ARG and "address" in g.lib.gdn2_last_error().decode()
+        rc = g.lib.gdn2_linattn_bwd_ckpt8(*[at[12 + j] for j in range(6)], at[3], None, at[6], at[4], None, *out,
+                                          ctypes.byref(dims), ws, 1 << 50, None)
+        assert rc == g.ERR_INVALID_ARG and "address" in g.lib.gdn2_last_error().decode()
