@@ -86,12 +86,15 @@ __global__ void __launch_bounds__(1024) plan_kernel(Cut c, int32_t *seg_off, int
 struct Runs {
   Run run[kMaxRuns];
 };
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Runs P) {
+// A block for a sequence, or, of many sequences, for a piece of a cut one (its first works).
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Runs P, int by_seq) {
   const Run &r = P.run[blockIdx.z];
   const int size = r.dy * r.dz, H = r.cut.H;
   const int h = blockIdx.x % H;
   Piece pc;  // the first of a cut sequence
-  if (!find_cut_piece(r.cut, blockIdx.x / H, &pc) || pc.s) return;
+  if (by_seq) fill_piece(r.cut, blockIdx.x / H, 0, &pc);
+  else if (!find_cut_piece(r.cut, blockIdx.x / H, &pc)) return;
+  if (pc.count < 2 || pc.s) return;
   const int n = pc.n, count = min(pc.count, r.cut.n_cut - pc.cut);
   const int e = blockIdx.y * 256 + threadIdx.x;
   if (e >= size) return;
@@ -450,8 +453,10 @@ __global__ void __launch_bounds__(kScan) dlog_kernel(const float *dq, int nq, co
   for (int done = 0; done < len; done += kScan) {
     const int t = len - 1 - done - (int)threadIdx.x;  // thread 0 has the latest token
     double v = 0.0;
+    float la = 0.f;
     const size_t at = (size_t)(t0 + t) * H + h, slice = (size_t)c.t_total * H;
     if (t >= 0) {
+      la = to_f32<T>(log_a[at]);
       for (int i = 0; i < nq; ++i) v += (double)dq[i * slice + at];
       for (int i = 0; i < nk; ++i) v -= (double)dk[i * slice + at];
     }
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(kScan) dlog_kernel(const float *dq, int nq, co
     for (int w = 0; w < warp; ++w) before += sums[w];
     // the first token decays nothing where no state comes in
     if (t >= 0)
-      dlog[at] = from_f32<T>((no_start && t == 0) || to_f32<T>(log_a[at]) <= kMinLog ? 0.f : (float)(before + incl));
+      dlog[at] = from_f32<T>((no_start && t == 0) || la <= kMinLog ? 0.f : (float)(before + incl));
     for (int w = 0; w < kScan / 32; ++w) carry += sums[w];
   }
 }
@@ -629,8 +634,10 @@ cudaError_t launch_plan(const Cut &c, int32_t *seg_off, int32_t *cut_off, int32_
 cudaError_t launch_join(const Run *r, int n, cudaStream_t s) {
   Runs P;
   for (int i = 0; i < n; ++i) P.run[i] = r[i];
-  const dim3 grid((unsigned)run_blocks(r->cut, 1), (unsigned)((r->dy * r->dz + 255) / 256), (unsigned)n);
-  join_kernel<<<grid, 256, 0, s>>>(P);
+  const int by_seq = r->cut.n_seqs <= r->cut.n_cut;
+  const dim3 grid((unsigned)((by_seq ? r->cut.n_seqs : r->cut.n_cut) * r->cut.H), (unsigned)((r->dy * r->dz + 255) / 256),
+                  (unsigned)n);
+  join_kernel<<<grid, 256, 0, s>>>(P, by_seq);
   return cudaGetLastError();
 }
 

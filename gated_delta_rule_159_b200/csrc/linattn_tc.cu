@@ -961,9 +961,11 @@ __global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *d
     const size_t t0 = (size_t)pc.t0 + (size_t)g * kTokens, at = (size_t)h * c.t_total + t0;
     const int cnt = min(kTokens, pc.len - g * kTokens);
     float v[kTokens / 32];
+    uint32_t resets = 0;
 #pragma unroll
     for (int j = 0; j < kTokens / 32; ++j) {
       const size_t i = at + 32 * j + lane;
+      if (32 * j + lane < cnt && __bfloat162float(log_a[(t0 + 32 * j + lane) * H + h]) <= kMinLog) resets |= 1u << j;
       v[j] = 32 * j + lane < cnt ? (dots_q[i] + dots_q[half + i]) - (dots_k[i] + dots_k[half + i]) : 0.f;
     }
     const float *end = mark_dots + ((size_t)mark_slot(unit / H, (int)t0) * H + h) * kMarkDots;
@@ -981,7 +983,7 @@ __global__ void __launch_bounds__(32 * kDlogWarps) dlog_tc_kernel(const float *d
       const size_t out = (t0 + 32 * j + lane) * H + h;
       const bool first = no_start && pc.s == 0 && g == 0 && 32 * j + lane == 0;
       if (32 * j + lane < cnt)
-        dlog[out] = __float2bfloat16_rn(first || __bfloat162float(log_a[out]) <= kMinLog ? 0.f : v[j] + behind);
+        dlog[out] = __float2bfloat16_rn(first || (resets >> j & 1) ? 0.f : v[j] + behind);
       behind += __shfl_sync(0xffffffffu, v[j], 0);
     }
   }
