@@ -66,7 +66,8 @@ __device__ __forceinline__ void load8<float>(const float *p, float (&f)[8]) {
 // cols % 8 == 0: a thread holds 8 values (one 16-byte load in bf16) and 4 lanes a block.  The unit
 // of work is a (row, block) pair of 4 lanes, so a row's last block may have fewer than 4 live lanes.
 // FLAT: cols % 32 == 0, so the rows need not be told apart and the 64-bit divisions, which took
-// longer than the memory, fall away.
+// longer than the memory, fall away (32768 x 2048 bf16: 51 us).  Other multiples of 8 divide once a unit (2040
+// columns: 64 us); what is no multiple of 8 goes one value a thread (2047 columns: 257 us).
 // Streaming bounds it: a thread takes kUnits units a thread block's span apart and asks for all of
 // them before it uses the first, 16 KB (bf16) a thread block in flight.
 constexpr int kUnits = 4;

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Runs 
 // ---------------------------------------------------------------- the run in fp32
 // Tiles of 32 tokens: G = X Y^T, P = G o D, out = P Z + f o (X S), S <- g S + (w o Y)^T Z, all in fp32 on
 // the CUDA cores.  A block takes a (piece, head) and 64 of the state's columns, which do not mix.
-// Per tile and token a block does 64 (2 dy + 64) + 32 dy multiply-adds; shared memory, read by 16
+// Per tile and token a block does 64 (2 dy + 32) + 32 dy multiply-adds; shared memory, read by 16
 // bytes, bounds it (79% of its rate with two blocks on an SM, now 70%).  So a thread takes 2 x 4 of P and 4 x 4 of
 // out, over half of the sums each, which a shuffle joins: 8 x 2048 tokens' gradients of 16 heads of
 // 64 x 64 took 1580 us with 1 x 4 and 2 x 4 over whole sums, then 1200, and with two multiply-adds an
@@ -516,7 +516,8 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const __grid_constant__ 
 // ---------------------------------------------------------------- single-token step
 // e^la as the sum of two floats: a fixed decay's rounding is the same at every token, and a state that
 // keeps n of them would be off by n.  la = n ln 2 + r (Cody and Waite's two-part ln 2), then the
-// Taylor series of e^r, its terms from r^2 / 2 on in one float (below 2^-4, so 2^-28 off).
+// Taylor series of e^r, its terms from r^2 / 2 on in one float: off by about r^2 2^-23, 2^-25 at most, and by far
+// less for the weak decays that are remembered long.
 __device__ __forceinline__ float2 split_exp(float la) {
   if (la <= kMinLog) return make_float2(0.f, 0.f);
   const float n = rintf(la * 1.44269504f);

@@ -111,7 +111,7 @@ __device__ __forceinline__ bool find_cut_piece(const Cut &c, int i, Piece *p) {
 // Groups of chunks that dlog_a of the tensor-core runs is summed over, numbered from each piece's
 // start.  A group ends with an exact product of the two states, in between bf16 products add up: over
 // 4096 tokens dlog_a is off by 0.40% with groups of 4 chunks, 0.32% with 2 and 0.27% with 1 (0.17% is its
-// own rounding), and the gradients of 8 x 4096 take 553, 553 and 613 us.  Slot of the group that starts at
+// own rounding), and the gradients of 8 x 4096 took 553, 553 and 613 us (now 535 to 554).  Slot of the group that starts at
 // token t of piece g: pieces are in token order, so no two share one.
 constexpr int kGroup = 2;
 constexpr int kMarkDots = 8;  // partial products a mark, one of each state warp
